@@ -64,6 +64,12 @@ typedef enum {
   MOE_GMM_TILED = 2    /* LDS-staged activation tiles: many rows per expert    */
 } moe_gmm_kernel_t;
 
+/* Scores of moe_topk_gate. */
+typedef enum {
+  MOE_GATE_SOFTMAX = 0, /* softmax of a token's logits                         */
+  MOE_GATE_SIGMOID = 1  /* sigmoid of each logit                               */
+} moe_gate_t;
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* moe_status_string(int status);
 
@@ -357,6 +363,154 @@ int moe_gmm_w4a4(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, c
 int moe_combine(const void* y, int y_dtype, const float* topk_weights,
                 const int32_t* pair_row, int32_t T, int32_t k, int32_t N,
                 void* out, int out_dtype, void* stream);
+
+/*
+ * moe_topk_gate - the router's choice: the k experts of each token and their
+ * weights, as moe_route_sort and moe_combine take them.
+ *
+ * s_e = softmax(l)_e or sigmoid(l_e) (score).  The chosen experts are the k
+ * largest s_e, or s_e + bias[e] where bias is given (a load-balancing bias
+ * that steers the choice and not the weights), in descending order, equal
+ * ones by ascending index.  Without a bias the logits are compared
+ * themselves; with one the sums are compared in f64.
+ *   topk_weights[t, j] = scale * s_ej / (renorm ? sum of the chosen s : 1)
+ * in f32.  A logit that is -inf or NaN (or an expert whose bias is NaN)
+ * masks its expert for that token: it is never chosen and adds nothing to a
+ * softmax.  Where fewer than k experts are left, the remaining slots get id
+ * -1 and weight 0; moe_route_sort drops such pairs (and counts them).
+ *
+ * logits         [T, E] f32 or bf16 (dtype).
+ * bias           [E] float or NULL.
+ * topk_ids       out [T, k] int32.
+ * topk_weights   out [T, k] float.
+ * Limits: T >= 1, 1 <= E <= 1024, 1 <= k <= min(E, 64), T*k <= 2^24.  An
+ * unknown dtype or score returns MOE_ERR_FORMAT.
+ */
+int moe_topk_gate(const void* logits, int dtype, const float* bias, int32_t T, int32_t E, int32_t k,
+                  int score, int renorm, float scale, int32_t* topk_ids, float* topk_weights,
+                  void* stream);
+
+/*
+ * moe_topk_gate_bwd - gradient of moe_topk_gate's weights with respect to the
+ * logits, the choice held fixed.
+ *
+ * With p the scores, g_e the sum of scale * dweights over the slots that
+ * chose expert e, and the sums over the chosen:
+ *   softmax          dl_e = p_e (g_e - sum_i g_i p_i)            every e
+ *   softmax, renorm  dl_j = w_j (g_j - sum_i g_i w_i)            chosen only
+ *   sigmoid          dl_j = g_j p_j (1 - p_j)                    chosen only
+ *   sigmoid, renorm  dl_j = w_j (g_j - sum_i g_i w_i) (1 - p_j)  chosen only
+ * (w = p / sum of the chosen p); other entries 0.  Every entry of dlogits is
+ * written.  Slots whose id is outside [0, E) or whose expert is masked
+ * contribute nothing, whatever their dweights hold.
+ *
+ * logits, score, renorm, scale   as given to moe_topk_gate.
+ * topk_ids       [T, k] int32, its result.
+ * dweights       [T, k] float.
+ * dlogits        out [T, E], the type of logits.
+ * Limits and errors as moe_topk_gate.
+ */
+int moe_topk_gate_bwd(const void* logits, int dtype, const int32_t* topk_ids, const float* dweights,
+                      int32_t T, int32_t E, int32_t k, int score, int renorm, float scale,
+                      void* dlogits, void* stream);
+
+/*
+ * moe_dispatch - token rows to band order: xs[pair_row[t*k + j], :] = x[t, :].
+ *
+ * moe_gmm gathers its rows itself (row_index); this is the gathered copy, for
+ * code that needs the rows laid out (an exchange between expert-parallel
+ * ranks, a matmul of its own).  A pair whose pair_row is outside [0, rows) is
+ * dropped.  Rows of xs that no pair names are not written.
+ *
+ * x              [T, N] f32 or bf16 (dtype).
+ * pair_row       [T*k] int32 (moe_route_sort output); its entries in
+ *                [0, rows) are distinct.
+ * xs             out [rows, N], the type of x.
+ * Limits: N % 4 == 0, N <= 2^30, 1 <= k <= 64, T*k <= 2^24, 1 <= rows <= 2^24,
+ * T*N and rows*N < 2^40; x and xs 16-byte aligned.
+ */
+int moe_dispatch(const void* x, int dtype, const int32_t* pair_row, int32_t T, int32_t k, int32_t N,
+                 int32_t rows, void* xs, void* stream);
+
+/*
+ * moe_dispatch_bwd - gradient of moe_dispatch (or of moe_gmm's gather):
+ * dx[t, :] = sum over j = 0..k-1, in that order, of dxs[pair_row[t*k + j], :],
+ * in f32; no atomics.  Dropped pairs contribute nothing.
+ *
+ * dxs            [rows, N] f32 or bf16 (dxs_dtype).
+ * dx             out [T, N] f32 or bf16 (dx_dtype; bf16 = RNE of the f32 sum).
+ * Limits as moe_dispatch.
+ */
+int moe_dispatch_bwd(const void* dxs, int dxs_dtype, const int32_t* pair_row, int32_t T, int32_t k,
+                     int32_t N, int32_t rows, void* dx, int dx_dtype, void* stream);
+
+/*
+ * moe_combine_bwd - gradient of moe_combine, in one pass:
+ *   dy[pair_row[p], :] = topk_weights[p] * dout[t, :]          p = t*k + j
+ *   dweights[p]        = sum_n dout[t, n] * y[pair_row[p], n]
+ * the products and sums in f32, in a fixed order.  A dropped pair (pair_row
+ * outside [0, rows)) writes no row and has dweights 0.  Rows of dy that no
+ * pair names are not written.
+ *
+ * dout           [T, N] f32 or bf16 (dout_dtype).
+ * y              [rows, N] f32 or bf16 (y_dtype), as given to moe_combine.
+ * topk_weights   [T, k] float.
+ * dy             out [rows, N] f32 or bf16 (dy_dtype).
+ * dweights       out [T, k] float.
+ * Limits as moe_dispatch; dout, y and dy 16-byte aligned.
+ */
+int moe_combine_bwd(const void* dout, int dout_dtype, const void* y, int y_dtype,
+                    const float* topk_weights, const int32_t* pair_row, int32_t T, int32_t k,
+                    int32_t N, int32_t rows, void* dy, int dy_dtype, float* dweights, void* stream);
+
+/*
+ * moe_silu_mul - the SiLU-gated activation of moe_gmm_act by itself, for a
+ * layer that keeps its gate/up sums for the gradient:
+ *   h[r, j] = silu(y[r, j]) * y[r, N/2 + j],  silu(z) = z / (1 + e^-z), f32.
+ *
+ * y              [M, N] f32 or bf16 (y_dtype): moe_gmm's output.
+ * n_rows         NULL (all M rows), or a device pointer to the number of rows
+ *                that hold values (group_offsets + E): the rows behind them
+ *                are neither read nor written.
+ * h              out [M, N/2] f32 or bf16 (h_dtype; RNE).
+ * Limits: N % 8 == 0, N <= 2^30, 1 <= M <= 2^24, M*N < 2^40; y and h 16-byte
+ * aligned.
+ */
+int moe_silu_mul(const void* y, int y_dtype, int32_t M, int32_t N, const int32_t* n_rows, void* h,
+                 int h_dtype, void* stream);
+
+/*
+ * moe_gmm_dgrad - gradient of the grouped matmul's input through the packed
+ * 4-bit weights:  dx[r, k] = sum_n dy[r, n] * W_e[n, k]  for every row r of
+ * band e, from the pack that moe_gmm streams (no second copy of the weights).
+ * Each decoded weight is exact in bf16, products exact, sums f32 on the bf16
+ * matrix unit; the NVFP4 tensor scale multiplies the f32 sums.
+ *
+ * act = MOE_ACT_NONE: dx is [M, K]; preact must be NULL.
+ * act = MOE_ACT_SILU_MUL: the matmul's input was h = silu(g) * u, with g and u
+ *   the column halves of preact [M, 2K].  The gradient dh = dx above (f32, not
+ *   rounded, not written) goes on through the activation, s = 1 / (1 + e^-g):
+ *     dx[r, k]     = dh u s (1 + g (1 - s))
+ *     dx[r, K + k] = dh g s
+ *   and dx is [M, 2K]: the gradient of the gate/up matmul's output.
+ *
+ * packed         mxfp4_encode output for (fmt, E, N, K), fmt MOE_W_MXFP4 or
+ *                MOE_W_NVFP4 (MOE_W_BF16 returns MOE_ERR_UNSUPPORTED).
+ * dy             bf16 [M, N], band-ordered rows.
+ * group_offsets  [E+1] int32 device array from moe_route_sort.
+ * preact         f32 or bf16 (preact_dtype), as moe_gmm wrote it.
+ * dx             out, f32 or bf16 (dx_dtype; RNE).  Rows [group_offsets[E], M)
+ *                are not written.
+ * Preconditions not checked: group_offsets is non-decreasing with
+ * group_offsets[0] = 0 and group_offsets[E] <= M.  Exact-decode domain as
+ * moe_gmm.
+ * Limits: K % 128 == 0, N % 64 == 0, E <= 1024, M <= 2^24, N*K/2 and 256*N
+ * <= 2^31 - 64 KiB, and a grid of (M/128 + min(E, M)) * ceil(K/256) <=
+ * 16,777,215 workgroups; packed 256-byte, dy, preact and dx 16-byte aligned.
+ */
+int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
+                  const int32_t* group_offsets, int32_t M, const void* preact, int preact_dtype,
+                  void* dx, int dx_dtype, int act, void* stream);
 
 /*
  * moe_mxfp4_to_nvfp4 - the lossless MXFP4 -> NVFP4 scale cast.

@@ -18,12 +18,15 @@ __all__ = [
     "MoeGmmError", "library", "route_sort", "route_sort_workspace_bytes", "packed_weight_bytes", "mxfp4_encode",
     "moe_gmm", "moe_combine", "mxfp4_to_nvfp4", "debug_decode", "bf16_encode",
     "mxfp4_quantize", "moe_gmm_w4a4",
+    "GATE_SOFTMAX", "GATE_SIGMOID", "topk_gate", "topk_gate_bwd", "moe_dispatch", "moe_dispatch_bwd",
+    "moe_combine_bwd", "silu_mul", "moe_gmm_dgrad",
 ]
 
 MXFP4, NVFP4, W_BF16 = 0, 1, 2
 F32, BF16 = 0, 1
 GMM_AUTO, GMM_STREAM, GMM_TILED = 0, 1, 2
 ACT_NONE, ACT_SILU_MUL = 0, 1
+GATE_SOFTMAX, GATE_SIGMOID = 0, 1
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoegmm.so")
 _lib = None
@@ -49,6 +52,17 @@ _SIGNATURES = {
     "moe_combine": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _i32, _i32, _i32, _vp,
                                    ctypes.c_int, _vp]),
     "moe_mxfp4_to_nvfp4": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "moe_topk_gate": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i32, _i32, _i32, ctypes.c_int, ctypes.c_int,
+                                     ctypes.c_float, _vp, _vp, _vp]),
+    "moe_topk_gate_bwd": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _i32, _i32, _i32, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_float, _vp, _vp]),
+    "moe_dispatch": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),
+    "moe_dispatch_bwd": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i32, _i32, _i32, _i32, _vp, ctypes.c_int, _vp]),
+    "moe_combine_bwd": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _i32, _i32, _i32, _i32,
+                                       _vp, ctypes.c_int, _vp, _vp]),
+    "moe_silu_mul": (ctypes.c_int, [_vp, ctypes.c_int, _i32, _i32, _vp, _vp, ctypes.c_int, _vp]),
+    "moe_gmm_dgrad": (ctypes.c_int, [_vp, ctypes.c_int, _i32, _i32, _i32, _vp, _vp, _i32, _vp, ctypes.c_int, _vp,
+                                     ctypes.c_int, ctypes.c_int, _vp]),
     "moe_debug_decode": (ctypes.c_int, [_vp, ctypes.c_int, _i32, _i32, _i32, _vp, _vp]),
     "moe_calib_mfma_bf16": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _vp]),
     "moe_calib_hbm_read": (ctypes.c_int, [_vp, _sz, _i32, _vp, _vp]),
@@ -298,6 +312,176 @@ def moe_combine(y, topk_weights, pair_row, out_dtype=F32):
                                  _ptr(topk_weights), _ptr(pair_row), T, k, N, _ptr(out),
                                  out_dtype, _stream()))
     return out
+
+
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+_OUT = {F32: torch.float32, BF16: torch.bfloat16}
+
+
+def _float(t, name, ndim):
+    """A contiguous float32 or bfloat16 device tensor; returns its dtype enum."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
+        raise MoeGmmError("%s must be a float32 or bfloat16 tensor" % name)
+    _dev(t, t.dtype, name, ndim)
+    return _FLOATS[t.dtype]
+
+
+def _out(out, shape, dtype, name, dev):
+    """out checked, or a new tensor; dtype is an F32/BF16 enum or a torch dtype."""
+    dtype = _OUT.get(dtype, dtype)
+    if not isinstance(dtype, torch.dtype):
+        raise MoeGmmError("the type of %s must be F32 or BF16" % name)
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _dev(out, dtype, name, len(shape))
+    if tuple(out.shape) != tuple(shape):
+        raise MoeGmmError("%s must be %s" % (name, list(shape)))
+    return out
+
+
+def _launch(fn, tensors, *args):
+    """fn(*args, stream) on the device that holds every tensor of tensors (None
+    skipped), on that device's current stream."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise MoeGmmError("the tensors must be on one device, got %s and %s" % (dev, t.device))
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream()))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream()))
+
+
+def topk_gate(logits, k, score=GATE_SOFTMAX, bias=None, renormalize=True, scale=1.0):
+    """moe_topk_gate.  logits [T, E] float32 or bfloat16, bias [E] float32 or
+    None -> (topk_ids [T, k] int32, topk_weights [T, k] float32), as
+    route_sort and moe_combine take them."""
+    dt = _float(logits, "logits", 2)
+    T, E = logits.shape
+    if bias is not None:
+        _dev(bias, torch.float32, "bias", 1)
+        if bias.numel() != E:
+            raise MoeGmmError("bias must have E entries")
+    ids = torch.empty((T, max(0, k)), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, max(0, k)), dtype=torch.float32, device=logits.device)
+    _launch(library().moe_topk_gate, (logits, bias), _ptr(logits), dt, _ptr(bias), T, E, k, score,
+            int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights))
+    return ids, weights
+
+
+def topk_gate_bwd(logits, topk_ids, dweights, score=GATE_SOFTMAX, renormalize=True, scale=1.0):
+    """moe_topk_gate_bwd.  logits [T, E] and the score, renormalize and scale
+    given to topk_gate, its topk_ids [T, k], dweights [T, k] float32 ->
+    dlogits [T, E] of the logits' type."""
+    dt = _float(logits, "logits", 2)
+    _dev(topk_ids, torch.int32, "topk_ids", 2)
+    _dev(dweights, torch.float32, "dweights", 2)
+    T, E = logits.shape
+    if topk_ids.shape[0] != T or dweights.shape != topk_ids.shape:
+        raise MoeGmmError("topk_ids and dweights must be [T, k]")
+    out = torch.empty_like(logits)
+    _launch(library().moe_topk_gate_bwd, (logits, topk_ids, dweights), _ptr(logits), dt, _ptr(topk_ids),
+            _ptr(dweights), T, E, topk_ids.shape[1], score, int(bool(renormalize)), float(scale), _ptr(out))
+    return out
+
+
+def _pairs(pair_row, k):
+    """pair_row checked against k slots per token; returns T."""
+    _dev(pair_row, torch.int32, "pair_row", 1)
+    if k < 1 or pair_row.numel() % k:
+        raise MoeGmmError("pair_row must have T*k entries")
+    return pair_row.numel() // k
+
+
+def moe_dispatch(x, pair_row, k, out=None):
+    """moe_dispatch.  x [T, N] float32 or bfloat16, pair_row [T*k] int32 ->
+    xs [T*k, N] of x's type (or out, [rows, N]); rows no pair names are left
+    as they were."""
+    dt = _float(x, "x", 2)
+    T, N = x.shape
+    if _pairs(pair_row, k) != T:
+        raise MoeGmmError("pair_row must have T*k entries")
+    rows = T * k
+    if out is not None:
+        _dev(out, x.dtype, "out", 2)
+        rows = out.shape[0]
+    out = _out(out, (rows, N), x.dtype, "out", x.device)
+    _launch(library().moe_dispatch, (x, pair_row, out), _ptr(x), dt, _ptr(pair_row), T, k, N, rows, _ptr(out))
+    return out
+
+
+def moe_dispatch_bwd(dxs, pair_row, k, out_dtype=F32):
+    """moe_dispatch_bwd.  dxs [rows, N] float32 or bfloat16, pair_row [T*k]
+    int32 -> dx [T, N]."""
+    dt = _float(dxs, "dxs", 2)
+    T = _pairs(pair_row, k)
+    rows, N = dxs.shape
+    dx = _out(None, (T, N), out_dtype, "dx", dxs.device)
+    _launch(library().moe_dispatch_bwd, (dxs, pair_row), _ptr(dxs), dt, _ptr(pair_row), T, k, N, rows, _ptr(dx),
+            _FLOATS[dx.dtype])
+    return dx
+
+
+def moe_combine_bwd(dout, y, topk_weights, pair_row, out_dtype=F32, out=None):
+    """moe_combine_bwd.  dout [T, N] and y [rows, N] float32 or bfloat16,
+    topk_weights [T, k] float32, pair_row [T*k] int32 -> (dy [rows, N],
+    dweights [T, k] float32).  out: a [rows, N] tensor for dy whose rows no
+    pair names are left as they were."""
+    gdt = _float(dout, "dout", 2)
+    ydt = _float(y, "y", 2)
+    _dev(topk_weights, torch.float32, "topk_weights", 2)
+    T, k = topk_weights.shape
+    rows, N = y.shape
+    if _pairs(pair_row, k) != T or tuple(dout.shape) != (T, N):
+        raise MoeGmmError("dout must be [T, N] and pair_row must have T*k entries")
+    dy = _out(out, (rows, N), out_dtype, "out", y.device)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    _launch(library().moe_combine_bwd, (dout, y, topk_weights, pair_row, dy), _ptr(dout), gdt, _ptr(y), ydt,
+            _ptr(topk_weights), _ptr(pair_row), T, k, N, rows, _ptr(dy), _FLOATS[dy.dtype], _ptr(dweights))
+    return dy, dweights
+
+
+def silu_mul(y, group_offsets=None, out_dtype=F32, out=None):
+    """moe_silu_mul.  y [M, N] float32 or bfloat16 -> h [M, N/2].  With
+    group_offsets [E+1] int32 only the rows of its bands are read and
+    written."""
+    dt = _float(y, "y", 2)
+    M, N = y.shape
+    n_rows = None
+    if group_offsets is not None:
+        _dev(group_offsets, torch.int32, "group_offsets", 1)
+        if group_offsets.numel() < 2:
+            raise MoeGmmError("group_offsets must have E+1 entries")
+        n_rows = ctypes.c_void_p(group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1))
+    h = _out(out, (M, N // 2), out_dtype, "out", y.device)
+    _launch(library().moe_silu_mul, (y, group_offsets, h), _ptr(y), dt, M, N, n_rows, _ptr(h), _FLOATS[h.dtype])
+    return h
+
+
+def moe_gmm_dgrad(packed, fmt, E, N, K, dy, group_offsets, M, out_dtype=F32, act=ACT_NONE, preact=None, out=None):
+    """moe_gmm_dgrad.  dy bf16 [M, N] in band order -> dx [M, K], the gradient
+    of moe_gmm's input (act=ACT_NONE), or with act=ACT_SILU_MUL and preact
+    [M, 2K] float32 or bfloat16 the gradient [M, 2K] of the gate/up sums whose
+    activation that input was."""
+    _dev(packed, torch.uint8, "packed", 1)
+    db = _bits16(dy, "dy")
+    _dev(group_offsets, torch.int32, "group_offsets", 1)
+    if group_offsets.numel() != E + 1:
+        raise MoeGmmError("group_offsets must have E+1 entries")
+    if tuple(db.shape) != (M, N):
+        raise MoeGmmError("dy must be [M, N]")
+    if packed.numel() < packed_weight_bytes(fmt, E, N, K):
+        raise MoeGmmError("packed buffer too small")
+    pdt = F32
+    if preact is not None:
+        pdt = _float(preact, "preact", 2)
+        if tuple(preact.shape) != (M, 2 * K):
+            raise MoeGmmError("preact must be [M, 2K]")
+    dx = _out(out, (M, 2 * K if act == ACT_SILU_MUL else K), out_dtype, "out", packed.device)
+    _launch(library().moe_gmm_dgrad, (packed, db, group_offsets, preact, dx), _ptr(packed), fmt, E, N, K, _ptr(db),
+            _ptr(group_offsets), M, _ptr(preact), pdt, _ptr(dx), _FLOATS[dx.dtype], act)
+    return dx
 
 
 def mxfp4_to_nvfp4(scales):

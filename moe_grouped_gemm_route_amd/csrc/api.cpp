@@ -47,6 +47,25 @@ int route_sort_shape(int32_t T, int32_t k, int32_t E) {
   return MOE_OK;
 }
 
+// Columns of the row operators: whole 16-byte f32 (8-byte bf16) words.
+constexpr int32_t kMaxCols = 1 << 30;
+
+int gate_shape(int32_t T, int32_t E, int32_t k) {
+  if (T < 1 || E < 1 || E > 1024 || k < 1 || k > 64 || k > E) return MOE_ERR_SHAPE;
+  if ((int64_t)T * k > kMaxRows) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+int permute_shape(int32_t T, int32_t k, int32_t N, int32_t rows) {
+  if (T < 1 || k < 1 || k > 64 || N < 4 || N % 4 != 0 || N > kMaxCols) return MOE_ERR_SHAPE;
+  if (rows < 1 || rows > kMaxRows) return MOE_ERR_SHAPE;
+  if ((int64_t)T * k > kMaxRows || (int64_t)T * N >= (int64_t(1) << 40)) return MOE_ERR_SHAPE;
+  if ((int64_t)rows * N >= (int64_t(1) << 40)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -227,6 +246,100 @@ int moe_combine(const void* y, int y_dtype, const float* topk_weights, const int
   return hip_status(moe::launch_combine(y, y_dtype == MOE_BF16, topk_weights, pair_row, T, k, N,
                                         out, out_dtype == MOE_BF16,
                                         static_cast<hipStream_t>(stream)));
+}
+
+int moe_topk_gate(const void* logits, int dtype, const float* bias, int32_t T, int32_t E, int32_t k, int score,
+                  int renorm, float scale, int32_t* topk_ids, float* topk_weights, void* stream) {
+  if (!dtype_ok(dtype) || (score != MOE_GATE_SOFTMAX && score != MOE_GATE_SIGMOID)) return MOE_ERR_FORMAT;
+  if (!logits || !topk_ids || !topk_weights) return MOE_ERR_NULL;
+  const int st = gate_shape(T, E, k);
+  if (st != MOE_OK) return st;
+  return hip_status(moe::launch_topk_gate(logits, dtype == MOE_BF16, bias, T, E, k, score, renorm != 0, scale,
+                                          topk_ids, topk_weights, static_cast<hipStream_t>(stream)));
+}
+
+int moe_topk_gate_bwd(const void* logits, int dtype, const int32_t* topk_ids, const float* dweights, int32_t T,
+                      int32_t E, int32_t k, int score, int renorm, float scale, void* dlogits, void* stream) {
+  if (!dtype_ok(dtype) || (score != MOE_GATE_SOFTMAX && score != MOE_GATE_SIGMOID)) return MOE_ERR_FORMAT;
+  if (!logits || !topk_ids || !dweights || !dlogits) return MOE_ERR_NULL;
+  const int st = gate_shape(T, E, k);
+  if (st != MOE_OK) return st;
+  return hip_status(moe::launch_topk_gate_bwd(logits, dtype == MOE_BF16, topk_ids, dweights, T, E, k, score,
+                                              renorm != 0, scale, dlogits, static_cast<hipStream_t>(stream)));
+}
+
+int moe_dispatch(const void* x, int dtype, const int32_t* pair_row, int32_t T, int32_t k, int32_t N, int32_t rows,
+                 void* xs, void* stream) {
+  if (!dtype_ok(dtype)) return MOE_ERR_FORMAT;
+  if (!x || !pair_row || !xs) return MOE_ERR_NULL;
+  const int st = permute_shape(T, k, N, rows);
+  if (st != MOE_OK) return st;
+  if (!aligned16(x) || !aligned16(xs)) return MOE_ERR_SHAPE;
+  return hip_status(moe::launch_dispatch(x, dtype == MOE_BF16, pair_row, T, k, N, rows, xs,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int moe_dispatch_bwd(const void* dxs, int dxs_dtype, const int32_t* pair_row, int32_t T, int32_t k, int32_t N,
+                     int32_t rows, void* dx, int dx_dtype, void* stream) {
+  if (!dtype_ok(dxs_dtype) || !dtype_ok(dx_dtype)) return MOE_ERR_FORMAT;
+  if (!dxs || !pair_row || !dx) return MOE_ERR_NULL;
+  const int st = permute_shape(T, k, N, rows);
+  if (st != MOE_OK) return st;
+  if (!aligned16(dxs) || !aligned16(dx)) return MOE_ERR_SHAPE;
+  return hip_status(moe::launch_dispatch_bwd(dxs, dxs_dtype == MOE_BF16, pair_row, T, k, N, rows, dx,
+                                             dx_dtype == MOE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_bwd(const void* dout, int dout_dtype, const void* y, int y_dtype, const float* topk_weights,
+                    const int32_t* pair_row, int32_t T, int32_t k, int32_t N, int32_t rows, void* dy, int dy_dtype,
+                    float* dweights, void* stream) {
+  if (!dtype_ok(dout_dtype) || !dtype_ok(y_dtype) || !dtype_ok(dy_dtype)) return MOE_ERR_FORMAT;
+  if (!dout || !y || !topk_weights || !pair_row || !dy || !dweights) return MOE_ERR_NULL;
+  const int st = permute_shape(T, k, N, rows);
+  if (st != MOE_OK) return st;
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(dy)) return MOE_ERR_SHAPE;
+  return hip_status(moe::launch_combine_bwd(dout, dout_dtype == MOE_BF16, y, y_dtype == MOE_BF16, topk_weights,
+                                            pair_row, T, k, N, rows, dy, dy_dtype == MOE_BF16, dweights,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+int moe_silu_mul(const void* y, int y_dtype, int32_t M, int32_t N, const int32_t* n_rows, void* h, int h_dtype,
+                 void* stream) {
+  if (!dtype_ok(y_dtype) || !dtype_ok(h_dtype)) return MOE_ERR_FORMAT;
+  if (!y || !h) return MOE_ERR_NULL;
+  if (M < 1 || M > kMaxRows || N < 8 || N % 8 != 0 || N > kMaxCols) return MOE_ERR_SHAPE;
+  if ((int64_t)M * N >= (int64_t(1) << 40)) return MOE_ERR_SHAPE;
+  if (!aligned16(y) || !aligned16(h)) return MOE_ERR_SHAPE;
+  return hip_status(moe::launch_silu_mul(y, y_dtype == MOE_BF16, M, N, n_rows, h, h_dtype == MOE_BF16,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
+                  const int32_t* group_offsets, int32_t M, const void* preact, int preact_dtype, void* dx,
+                  int dx_dtype, int act, void* stream) {
+  const int st = check_weight_shape(fmt, E, N, K);
+  if (st != MOE_OK) return st;
+  if (fmt == MOE_W_BF16) return MOE_ERR_UNSUPPORTED;
+  if (E > kMaxGmmExperts) return MOE_ERR_SHAPE;
+  if (!dtype_ok(dx_dtype)) return MOE_ERR_FORMAT;
+  if (act != MOE_ACT_NONE && act != MOE_ACT_SILU_MUL) return MOE_ERR_FORMAT;
+  if (!packed || !dy || !group_offsets || !dx) return MOE_ERR_NULL;
+  if (act == MOE_ACT_SILU_MUL) {
+    if (!preact) return MOE_ERR_NULL;
+    if (!dtype_ok(preact_dtype)) return MOE_ERR_FORMAT;
+    if (!aligned16(preact)) return MOE_ERR_SHAPE;
+  } else if (preact) {
+    return MOE_ERR_FORMAT;
+  }
+  if (M < 1 || M > kMaxRows) return MOE_ERR_SHAPE;
+  // an expert's codes and a tile's dy rows are addressed with 32-bit byte
+  // offsets, below the lane offset that reads zeros
+  if ((int64_t)N * (K / 2) > (int64_t)moe::kLaneOob || (int64_t)N * 256 > (int64_t)moe::kLaneOob) return MOE_ERR_SHAPE;
+  if (((uintptr_t)packed & 255) || !aligned16(dy) || !aligned16(dx)) return MOE_ERR_SHAPE;
+  if (moe::dgrad_workgroups(E, K, M) > kMaxWorkgroups) return MOE_ERR_SHAPE;
+  return hip_status(moe::launch_dgrad(static_cast<const uint8_t*>(packed), fmt, E, N, K, dy, group_offsets, M, preact,
+                                      preact_dtype == MOE_BF16, dx, dx_dtype == MOE_BF16, act,
+                                      static_cast<hipStream_t>(stream)));
 }
 
 int moe_mxfp4_to_nvfp4(const uint8_t* scales, int32_t E, int32_t N, int32_t K,

@@ -1,0 +1,265 @@
+// moe_topk_gate / moe_topk_gate_bwd: the router's top-k choice and weights,
+// and their gradient.
+//
+// One wave per token; lane l holds experts l, l + 64, l + 128, ...  The k
+// choices are k rounds of "largest key over the wave, lowest index among
+// equals": the maximum is one DPP reduction, and because a slot's 64 experts
+// are consecutive, the lowest index is the first set bit of the first
+// non-empty ballot of (key == maximum), slot by slot.  No shuffle of indices
+// and no LDS.
+//
+// Keys.  Without a bias the scores rise with the logits, so the keys are the
+// logits themselves and the choice is exact.  With a bias the key is
+// score + bias, where two experts can come within an f32 rounding of each
+// other; those keys are computed in f64, so the choice does not hang on the
+// last bit of an exponential (at 4,096 tokens x 256 experts f32 keys would
+// put a pair in another order about once a batch).
+//
+// Weights are f32.  A renormalised weight is s_j / sum s over the chosen,
+// with s scaled by a common factor so that the largest chosen score cannot
+// underflow: softmax subtracts the largest chosen logit; for the sigmoid,
+//     sigma(l) = e^min(l, 0) / (1 + e^-|l|),
+// and the largest chosen min(l, 0) is subtracted in that exponent.
+#include "common.h"
+#include "launch.h"
+#include "wave.h"
+
+namespace moe {
+
+constexpr int GATE_WAVES = 4;   // tokens per workgroup
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* __restrict__ logits, int64_t i) {
+  if (BF16) return bf16_lo(reinterpret_cast<const uint16_t*>(logits)[i]);
+  return reinterpret_cast<const float*>(logits)[i];
+}
+
+// A row's logits, NaN and places past E as -inf (masked).
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_row(const void* __restrict__ logits, int64_t t, int E, float (&x)[VPL]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 64 + lane;
+    x[i] = -INFINITY;
+    if (e < E) {
+      const float v = load_logit<BF16>(logits, t * E + e);
+      if (v == v) x[i] = v;
+    }
+  }
+}
+
+// e^(x - m), 1 at x = m (infinities included), 0 for a masked x.
+__device__ __forceinline__ float exp_below(float x, float m) { return x == m && x > -INFINITY ? 1.f : x > -INFINITY ? expf(x - m) : 0.f; }
+
+template <int VPL>
+__device__ __forceinline__ float row_max(const float (&x)[VPL]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) m = fmaxf(m, x[i]);
+  return wave_max(m);
+}
+
+template <int VPL>
+__device__ __forceinline__ float row_exp_sum(const float (&x)[VPL], float m) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) s += exp_below(x[i], m);
+  return wave_sum(s);
+}
+
+// The unscaled weights of lanes j < k from the chosen logits (-inf in lanes
+// whose slot chose nothing, and in lanes >= k): softmax (score 0) or sigmoid
+// (1), over the chosen (renorm) or as they are.  m and z: the row's largest
+// logit and sum of exponentials (softmax without renorm only).
+__device__ __forceinline__ float chosen_weight(float l, int score, int renorm, float m, float z) {
+  const bool live = l > -INFINITY;
+  if (score == 0) {
+    if (renorm) {
+      m = wave_max(l);
+      const float s = exp_below(l, m);
+      z = wave_sum(s);
+      return live ? s / z : 0.f;
+    }
+    return live ? exp_below(l, m) / z : 0.f;
+  }
+  const float low = fminf(l, 0.f);
+  const float ref = renorm ? wave_max(low) : 0.f;
+  const float s = live ? expf(low - (ref > -INFINITY ? ref : 0.f)) / (1.f + expf(-fabsf(l))) : 0.f;
+  if (!renorm) return s;
+  z = wave_sum(s);
+  return live ? s / z : 0.f;
+}
+
+// KEY is float (no bias: the logits) or double (score + bias).
+template <int VPL, bool BF16, typename KEY>
+__global__ __launch_bounds__(GATE_WAVES * 64) void gate_kernel(const void* __restrict__ logits,
+                                                               const float* __restrict__ bias, int32_t T, int32_t E,
+                                                               int32_t k, int score, int renorm, float scale,
+                                                               int32_t* __restrict__ ids, float* __restrict__ weights) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = blockIdx.x * (int64_t)GATE_WAVES + (threadIdx.x >> 6);
+  if (t >= T) return;
+  float x[VPL];
+  load_row<VPL, BF16>(logits, t, E, x);
+  float m = -INFINITY, z = 0.f;
+  if (score == 0 && !renorm) {
+    m = row_max(x);
+    z = row_exp_sum(x, m);
+  }
+  KEY key[VPL];
+  if constexpr (sizeof(KEY) == 8) {
+    double zd = 0.0, md = 0.0;
+    double p[VPL];
+    if (score == 0) {
+      md = (double)row_max(x);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        p[i] = x[i] > -INFINITY ? ((double)x[i] == md ? 1.0 : exp((double)x[i] - md)) : 0.0;
+        zd += p[i];
+      }
+      zd = wave_sum(zd);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 64 + lane;
+      const double s = score == 0 ? p[i] / zd : 1.0 / (1.0 + exp(-(double)x[i]));
+      key[i] = x[i] > -INFINITY ? s + (double)bias[e] : -(double)INFINITY;
+      if (key[i] != key[i]) key[i] = -(double)INFINITY;   // a NaN bias masks its expert
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = x[i];
+  }
+
+  int my_id = -1;
+  float my_logit = -INFINITY;
+  for (int j = 0; j < k; ++j) {
+    KEY best = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) best = key[i] > best ? key[i] : best;
+    best = wave_max(best);
+    if (!(best > -(KEY)INFINITY)) break;   // uniform: nothing is left to choose
+    int e = -1;
+    float l = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const uint64_t hit = __ballot(key[i] == best);
+      if (e < 0 && hit != 0) {
+        const int src = __ffsll((unsigned long long)hit) - 1;
+        e = i * 64 + src;
+        l = read_lane(x[i], src);
+        if (lane == src) key[i] = -(KEY)INFINITY;
+      }
+    }
+    if (lane == j) {
+      my_id = e;
+      my_logit = l;
+    }
+  }
+  const float w = chosen_weight(my_logit, score, renorm, m, z);
+  if (lane < k) {
+    ids[t * k + lane] = my_id;
+    weights[t * k + lane] = w * scale;
+  }
+}
+
+// dlogits of one token: lane j < k computes the gradient that reaches the
+// logit of its slot, then every lane adds up the slots that chose its
+// experts, in slot order (a repeated id adds twice).
+template <int VPL, bool BF16>
+__global__ __launch_bounds__(GATE_WAVES * 64) void gate_bwd_kernel(const void* __restrict__ logits,
+                                                                   const int32_t* __restrict__ ids,
+                                                                   const float* __restrict__ dweights, int32_t T,
+                                                                   int32_t E, int32_t k, int score, int renorm,
+                                                                   float scale, void* __restrict__ dlogits) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = blockIdx.x * (int64_t)GATE_WAVES + (threadIdx.x >> 6);
+  if (t >= T) return;
+  int id = -1;
+  float g = 0.f, l = -INFINITY;
+  if (lane < k) {
+    id = ids[t * k + lane];
+    if (id < 0 || id >= E) id = -1;
+    if (id >= 0) {
+      g = dweights[t * k + lane] * scale;
+      const float v = load_logit<BF16>(logits, t * E + id);
+      if (v == v) l = v;
+    }
+  }
+  const bool dense = score == 0 && !renorm;
+  float x[VPL];
+  float m = -INFINITY, z = 0.f;
+  if (dense) {
+    load_row<VPL, BF16>(logits, t, E, x);
+    m = row_max(x);
+    z = row_exp_sum(x, m);
+  }
+  const float w = chosen_weight(l, score, renorm, m, z);
+  // a slot that chose nothing (or a masked expert) has weight 0 whatever its
+  // logits, so nothing flows back through it
+  const bool live = l > -INFINITY;
+  const float gl = live ? g : 0.f;
+  const float mean = score == 0 || renorm ? wave_sum(gl * w) : 0.f;
+  float d = live ? w * (gl - (dense ? 0.f : mean)) : 0.f;
+  if (score == 1 && live) d *= l >= 0.f ? expf(-l) / (1.f + expf(-l)) : 1.f / (1.f + expf(l));   // 1 - sigma
+  float a[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    a[i] = dense && x[i] > -INFINITY ? -mean * (exp_below(x[i], m) / z) : 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int e = read_lane(id, j);
+    const float dj = read_lane(d, j);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e == i * 64 + lane) a[i] += dj;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 64 + lane;
+    if (e < E) {
+      if (BF16) reinterpret_cast<uint16_t*>(dlogits)[t * E + e] = f32_to_bf16_rne(a[i]);
+      else reinterpret_cast<float*>(dlogits)[t * E + e] = a[i];
+    }
+  }
+}
+
+// Calls f with the logits per lane, rounded up to the built sizes.
+template <typename F>
+static void for_vpl(int32_t E, F f) {
+  if (E <= 64) f(std::integral_constant<int, 1>{});
+  else if (E <= 128) f(std::integral_constant<int, 2>{});
+  else if (E <= 256) f(std::integral_constant<int, 4>{});
+  else if (E <= 512) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
+}
+
+hipError_t launch_topk_gate(const void* logits, int bf16, const float* bias, int32_t T, int32_t E, int32_t k,
+                            int score, int renorm, float scale, int32_t* ids, float* weights, hipStream_t stream) {
+  const dim3 grid((unsigned)((T + GATE_WAVES - 1) / GATE_WAVES)), block(GATE_WAVES * 64);
+  for_vpl(E, [&](auto v) {
+    constexpr int VPL = decltype(v)::value;
+    if (bf16) {
+      if (bias) hipLaunchKernelGGL((gate_kernel<VPL, true, double>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
+      else hipLaunchKernelGGL((gate_kernel<VPL, true, float>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
+    } else {
+      if (bias) hipLaunchKernelGGL((gate_kernel<VPL, false, double>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
+      else hipLaunchKernelGGL((gate_kernel<VPL, false, float>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
+    }
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_topk_gate_bwd(const void* logits, int bf16, const int32_t* ids, const float* dweights, int32_t T,
+                                int32_t E, int32_t k, int score, int renorm, float scale, void* dlogits,
+                                hipStream_t stream) {
+  const dim3 grid((unsigned)((T + GATE_WAVES - 1) / GATE_WAVES)), block(GATE_WAVES * 64);
+  for_vpl(E, [&](auto v) {
+    constexpr int VPL = decltype(v)::value;
+    if (bf16) hipLaunchKernelGGL((gate_bwd_kernel<VPL, true>), grid, block, 0, stream, logits, ids, dweights, T, E, k, score, renorm, scale, dlogits);
+    else hipLaunchKernelGGL((gate_bwd_kernel<VPL, false>), grid, block, 0, stream, logits, ids, dweights, T, E, k, score, renorm, scale, dlogits);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -89,4 +89,34 @@ hipError_t launch_combine(const void* y, int y_bf16, const float* w, const int32
                           int32_t T, int32_t k, int32_t N, void* out, int out_bf16,
                           hipStream_t stream);
 
+// Router: k choices and weights per token (score 0 softmax, 1 sigmoid; bias
+// may be NULL), and the gradient of the logits.
+hipError_t launch_topk_gate(const void* logits, int bf16, const float* bias, int32_t T, int32_t E, int32_t k,
+                            int score, int renorm, float scale, int32_t* ids, float* weights, hipStream_t stream);
+hipError_t launch_topk_gate_bwd(const void* logits, int bf16, const int32_t* ids, const float* dweights, int32_t T,
+                                int32_t E, int32_t k, int score, int renorm, float scale, void* dlogits,
+                                hipStream_t stream);
+
+// Rows to band order and back, and the combine's gradient (rows: band rows
+// that exist; a pair_row outside them is a dropped pair).
+hipError_t launch_dispatch(const void* x, int bf16, const int32_t* pair_row, int32_t T, int32_t k, int32_t N,
+                           int32_t rows, void* xs, hipStream_t stream);
+hipError_t launch_dispatch_bwd(const void* dxs, int in_bf16, const int32_t* pair_row, int32_t T, int32_t k, int32_t N,
+                               int32_t rows, void* dx, int out_bf16, hipStream_t stream);
+hipError_t launch_combine_bwd(const void* dout, int dout_bf16, const void* y, int y_bf16, const float* w,
+                              const int32_t* pair_row, int32_t T, int32_t k, int32_t N, int32_t rows, void* dy,
+                              int dy_bf16, float* dweights, hipStream_t stream);
+
+// SiLU-gated activation of [M, N] gate/up sums (the first *n_rows rows, or
+// all where n_rows is NULL).
+hipError_t launch_silu_mul(const void* y, int y_bf16, int32_t M, int32_t N, const int32_t* n_rows, void* h,
+                           int h_bf16, hipStream_t stream);
+
+// Gradient of the grouped matmul's input; act 1 also takes it through the
+// SiLU-gated activation of preact [M, 2K].
+hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
+                        const int32_t* group_offsets, int32_t M, const void* preact, int preact_bf16, void* dx,
+                        int dx_bf16, int act, hipStream_t stream);
+int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M);
+
 }  // namespace moe

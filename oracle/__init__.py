@@ -21,6 +21,9 @@ routed-expert path computes, written from these pages:
 * "DeepSeek-V4-Flash-0731-NVFP4": the W4A4 execution with 4-bit activations,
   here with MXFP4 (power-of-two block scale) activation quantization
   (quant.py).
+* The router's top-k choice (gate.py) and the gradients of the layer's steps
+  (grad.py), which the pages do not cover: the usual definitions and the plain
+  derivatives of the steps above.
 
 It shares no code with the HIP path and imports nothing from it.
 """
@@ -41,3 +44,5 @@ from .gmm import gmm, gmm_w4a4, gmm_sampled, dense_weights  # noqa: F401
 from .quant import nearest_e2m1, quantize_mxfp4_rows, dequantize_mxfp4_rows  # noqa: F401
 from .combine import combine  # noqa: F401
 from .act import silu, silu_mul  # noqa: F401
+from .gate import topk_gate, topk_gate_bwd, slot_weights  # noqa: F401
+from .grad import dispatch, dispatch_bwd, combine_bwd, gmm_dgrad, silu_mul_bwd  # noqa: F401
