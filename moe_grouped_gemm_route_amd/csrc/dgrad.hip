@@ -54,7 +54,8 @@ struct BandTile {
   int e, m0, rows;
 };
 
-// Tile t of the list "for each expert, its band cut into BM-row tiles", found
+// Tile t of the list "for each expert, its band cut into ceil(rows / BM) even
+// tiles", found
 // by the whole wave from the band offsets: lane l covers experts
 // [l per, l per + per), whose offsets it loads in one batch; a wave prefix sum
 // of the lanes' tile counts picks the lane, which then finds its expert.
@@ -91,9 +92,11 @@ __device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, i
       const int c = o[i + 1] - o[i];
       const int n = (c + BM - 1) / BM;
       if (left < n) {
+        // an even share of the band, in whole 16-row subtiles
+        const int share = ((c + n - 1) / n + 15) & ~15;
         b.e = e0 + i;
-        b.m0 = o[i] + left * BM;
-        b.rows = min(BM, c - left * BM);
+        b.m0 = o[i] + left * share;
+        b.rows = min(share, c - left * share);
         found = true;
       }
       left -= n;
@@ -204,12 +207,20 @@ struct DgradArgs {
   void* dx;
 };
 
+// Ends a step: this wave's LDS operations are done, then the workgroup
+// barrier.  Loads into registers stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4));   // vmcnt 63, expcnt 7, lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <int FMT, bool OBF16, int ACT>
 __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
   constexpr int S_BYTES = (FMT == 1 ? DG_NV_HALVES : 1) * DG_BN * (DG_BK / 32) * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_a[DG_A_BYTES];
-  __shared__ __attribute__((aligned(1024))) uint8_t s_c[DG_C_BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t s_s[S_BYTES];
+  constexpr int STAGE = DG_A_BYTES + DG_C_BYTES + S_BYTES;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_stage[2 * STAGE];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -224,14 +235,30 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
   const int kc2 = wave >> 1;                   // this wave's chunk column
   const int kb0 = (wave & 1) * 2;              // and first k block in it
 
-  // dy rows of the tile: rows past the band and columns past N do not exist
-  // in the range, so they read zeros
+  // dy rows of the tile: rows past the band do not exist in the range, so
+  // they read zeros
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.dy + (int64_t)tile.m0 * N, (uint32_t)tile.rows * N * 2);
   const int64_t et = (int64_t)tile.e * L.NT;
   const __amdgpu_buffer_rsrc_t cr = make_rsrc(p.packed + ((et * KC) << 10), (uint32_t)((int64_t)N * K / 2));
-  const uint32_t* sw =
-      reinterpret_cast<const uint32_t*>(p.packed + L.scales_off) +
-      (et * L.groups + (FMT == 0 ? kc0 >> 2 : kc0 >> 1)) * 64 + lane;
+  const __amdgpu_buffer_rsrc_t sr =
+      make_rsrc(p.packed + L.scales_off + et * L.groups * 256, (uint32_t)(L.NT * L.groups * 256));
+  const int rec = FMT == 0 ? kc0 >> 2 : kc0 >> 1;
+  const int groups = (int)L.groups;
+
+  // source offsets of this lane's staging loads: 1 KiB (8 rows of 128 bytes)
+  // each, lane l landing in row l / 8 at segment l & 7, which holds the row's
+  // segment (l & 7) ^ (row / 2 & 7): the 16 rows of a fragment read then fall
+  // into 16 different 16-byte bank groups
+  uint32_t avo[4], cvo[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = (wave * 4 + j) * 8 + (lane >> 3);
+    avo[j] = row < tile.rows ? (uint32_t)row * N * 2 + (((lane & 7) ^ ((row >> 1) & 7)) << 4) : kLaneOob;
+  }
+  // chunk column (wave >> 1) of the workgroup, 16-row blocks (wave & 1)*2 + j
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    cvo[j] = kc0 + kc2 < KC ? (uint32_t)((((kb0 + j) * KC + kc0 + kc2) << 10) + lane * 16) : kLaneOob;
 
   f32x4_t acc[DG_MS][2][2];
 #pragma unroll
@@ -247,39 +274,49 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
     any = __ballot(f != 0) != 0;
   }
 
-  for (int n0 = 0; n0 < N; n0 += DG_BN) {
-    // stage: 16 KiB of dy (row 8i + l/8, its 16-byte segment l & 7 swizzled by
-    // the row), eight code chunks, and the block scales
+  const int steps = N / DG_BN;
+  // A step's 4 KiB of dy, 2 KiB of codes and 256 bytes of scale words per
+  // wave, loaded into registers one step ahead and written to LDS once the
+  // step before is computed.  Past the last step the lane offsets lie outside
+  // the buffers, so the loads fetch nothing.
+  u32x4_t ra[4], rc[2];
+  uint32_t rw;
+  auto load = [&](int i) {
+    const bool live = i < steps;
+    const uint32_t q = live ? (uint32_t)i : 0u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = wave * 4 + j;
-      const int row = i * 8 + (lane >> 3);
-      const int seg = (lane & 7) ^ ((row >> 1) & 7);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_void_t)(s_a + i * 1024), 16,
-                                               row < tile.rows ? (uint32_t)row * N * 2 + seg * 16 : kLaneOob, n0 * 2, 0, 0);
-    }
+    for (int j = 0; j < 2; ++j)
+      rc[j] = __builtin_amdgcn_raw_buffer_load_b128(cr, live ? cvo[j] : kLaneOob, (q * (DG_BN / 16) * KC) << 10, 0);
+    rw = __builtin_amdgcn_raw_buffer_load_b32(sr, live ? lane * 4 : kLaneOob,
+                                              ((q * (DG_BN / 16) + wave) * groups + rec) * 256, 0);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = wave * 2 + j;              // chunk (column i >> 2, 16-row block i & 3)
-      const int kc = kc0 + (i >> 2);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(cr, (lds_void_t)(s_c + i * 1024), 16, kc < KC ? lane * 16 : kLaneOob,
-                                               kc < KC ? ((n0 / 16 + (i & 3)) * KC + kc) << 10 : 0, 0, 0);
+    for (int j = 0; j < 4; ++j)
+      ra[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, live ? avo[j] : kLaneOob, q * DG_BN * 2, 0);
+  };
+  // Writes them to a stage: dy and codes as they are, the scale word (16-row
+  // block `wave`, row c16, k block g of both chunk columns) as bf16 patterns,
+  // [block][half][n].
+  auto put = [&](uint8_t* st) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(st + (wave * 4 + j) * 1024 + lane * 16) = ra[j];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<u32x4_t*>(st + DG_A_BYTES + (wave * 2 + j) * 1024 + lane * 16) = rc[j];
+    uint16_t* s = reinterpret_cast<uint16_t*>(st + DG_A_BYTES + DG_C_BYTES) + wave * 16 + c16;
+    if (FMT == 0) {
+      s[g * 64] = e8m0_bf16((rw >> (8 * (kc0 & 3))) & 0xFFu);
+      s[(4 + g) * 64] = e8m0_bf16((rw >> (8 * (kc0 & 3) + 8)) & 0xFFu);
+    } else {
+      s[(g * 2) * 64] = e4m3_bf16<0>(rw);
+      s[(g * 2 + 1) * 64] = e4m3_bf16<1>(rw);
+      s[((4 + g) * 2) * 64] = e4m3_bf16<2>(rw);
+      s[((4 + g) * 2 + 1) * 64] = e4m3_bf16<3>(rw);
     }
-    {
-      const uint32_t w = sw[(int64_t)(n0 / 16 + wave) * L.groups * 64];
-      uint16_t* s = reinterpret_cast<uint16_t*>(s_s) + wave * 16 + c16;
-      if (FMT == 0) {
-        s[g * 64] = e8m0_bf16((w >> (8 * (kc0 & 3))) & 0xFFu);
-        s[(4 + g) * 64] = e8m0_bf16((w >> (8 * (kc0 & 3) + 8)) & 0xFFu);
-      } else {
-        s[(g * 2) * 64] = e4m3_bf16<0>(w);
-        s[(g * 2 + 1) * 64] = e4m3_bf16<1>(w);
-        s[((4 + g) * 2) * 64] = e4m3_bf16<2>(w);
-        s[((4 + g) * 2 + 1) * 64] = e4m3_bf16<3>(w);
-      }
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+  };
+  auto compute = [&](auto nsub, const uint8_t* a) {
+    constexpr int NSUB = decltype(nsub)::value;
+    const uint8_t* c = a + DG_A_BYTES;
+    const uint8_t* sp = c + DG_C_BYTES;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       u32x4_t w[2][2];
@@ -287,25 +324,49 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
       for (int b = 0; b < 2; ++b) {
         const int kb = kb0 + b;
         const i32x2_t q = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (lds_i32x2_t)(s_c + (kc2 * 4 + 2 * s + (g >> 1)) * 1024 + kb * 256 + (g & 1) * 128 + c16 * 8));
+            (lds_i32x2_t)(c + (kc2 * 4 + 2 * s + (g >> 1)) * 1024 + kb * 256 + (g & 1) * 128 + c16 * 8));
         const int blk = FMT == 0 ? kc2 * 4 + kb : (kc2 * 4 + kb) * 2 + (c16 >> 3);
-        const u32x4_t sc = *reinterpret_cast<const u32x4_t*>(s_s + (blk * 64 + s * 32 + g * 8) * 2);
+        const u32x4_t sc = *reinterpret_cast<const u32x4_t*>(sp + (blk * 64 + s * 32 + g * 8) * 2);
         if (FMT == 1 && any) decode_pair<true>(q, sc, w[b][0], w[b][1]);
         else decode_pair<false>(q, sc, w[b][0], w[b][1]);
       }
 #pragma unroll
-      for (int ms = 0; ms < DG_MS; ++ms) {
+      for (int ms = 0; ms < NSUB; ++ms) {
         const int row = ms * 16 + c16;
-        const u32x4_t a =
-            *reinterpret_cast<const u32x4_t*>(s_a + row * 128 + (((s * 4 + g) ^ ((row >> 1) & 7)) << 4));
+        const u32x4_t x =
+            *reinterpret_cast<const u32x4_t*>(a + row * 128 + (((s * 4 + g) ^ ((row >> 1) & 7)) << 4));
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          acc[ms][b][0] = mfma16(w[b][0], a, acc[ms][b][0]);
-          acc[ms][b][1] = mfma16(w[b][1], a, acc[ms][b][1]);
+          acc[ms][b][0] = mfma16(w[b][0], x, acc[ms][b][0]);
+          acc[ms][b][1] = mfma16(w[b][1], x, acc[ms][b][1]);
         }
       }
     }
-    __syncthreads();
+  };
+
+  // step i + 1 loads while step i computes; the walk of a tile with fewer
+  // rows leaves out the subtiles it does not have
+  load(0);
+  put(s_stage);
+  lds_barrier();
+  auto walk = [&](auto nsub) {
+    for (int i = 0; i < steps; ++i) {
+      load(i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(nsub, s_stage + (i & 1) * STAGE);
+      put(s_stage + (~i & 1) * STAGE);
+      lds_barrier();
+    }
+  };
+  switch ((tile.rows + 15) >> 4) {
+    case 1: walk(std::integral_constant<int, 1>{}); break;
+    case 2: walk(std::integral_constant<int, 2>{}); break;
+    case 3: walk(std::integral_constant<int, 3>{}); break;
+    case 4: walk(std::integral_constant<int, 4>{}); break;
+    case 5: walk(std::integral_constant<int, 5>{}); break;
+    case 6: walk(std::integral_constant<int, 6>{}); break;
+    case 7: walk(std::integral_constant<int, 7>{}); break;
+    default: walk(std::integral_constant<int, 8>{}); break;
   }
 
   if (kc0 + kc2 >= KC) return;
