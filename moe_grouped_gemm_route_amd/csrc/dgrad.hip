@@ -59,9 +59,13 @@ struct BandTile {
 // by the whole wave from the band offsets: lane l covers experts
 // [l per, l per + per), whose offsets it loads in one batch; a wave prefix sum
 // of the lanes' tile counts picks the lane, which then finds its expert.
-// (E <= 1024, so per <= 16.)  total receives the number of tiles.
+// (E <= 1024, so per <= 16.)
+// The workgroup's tile and its column group nb of NB.  Workgroup ids are dealt
+// round-robin to the 8 XCDs; they are remapped so that each XCD takes a
+// contiguous run of the (tile, column group) list: the column groups of a
+// tile then read its dy rows from one L2.
 template <int BM>
-__device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, int E, int t, int& total) {
+__device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, int E, int NB, int& nb) {
   constexpr int PER = 16;
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) >> 6;
@@ -79,9 +83,13 @@ __device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, i
     const int v = __shfl_up(incl, d, 64);
     if (lane >= d) incl += v;
   }
-  total = __builtin_amdgcn_readlane(incl, 63);
-  int left = t - (incl - mine);   // tiles of this lane's experts before tile t
-  const uint64_t hit = __ballot(left >= 0 && left < mine);
+  const int items = __builtin_amdgcn_readlane(incl, 63) * NB;
+  const int bx = blockIdx.x, x = bx & 7;
+  const int item = x * (items >> 3) + min(x, items & 7) + (bx >> 3);
+  const int t = bx < items ? item / NB : -1;
+  nb = item - t * NB;
+  int left = t - (incl - mine);   // tile t's place among this lane's tiles
+  const uint64_t hit = __ballot(t >= 0 && left >= 0 && left < mine);
   BandTile b = {0, 0, 0};
   if (hit == 0) return b;
   const int src = __ffsll((unsigned long long)hit) - 1;
@@ -225,9 +233,8 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g = lane >> 4;
-  int total;
-  const int t = blockIdx.x / p.NB, nb = blockIdx.x - t * p.NB;
-  const BandTile tile = find_tile<DG_BM>(p.off, p.E, t, total);
+  int nb;
+  const BandTile tile = find_tile<DG_BM>(p.off, p.E, p.NB, nb);
   if (tile.rows == 0) return;
   const Layout& L = p.L;
   const int N = (int)L.N, K = (int)L.K, KC = (int)L.KC;
