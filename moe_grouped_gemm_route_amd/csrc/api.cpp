@@ -338,7 +338,7 @@ int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, 
   if (((uintptr_t)packed & 255) || !aligned16(dy) || !aligned16(dx)) return MOE_ERR_SHAPE;
   if (moe::dgrad_workgroups(E, K, M) > kMaxWorkgroups) return MOE_ERR_SHAPE;
   return hip_status(moe::launch_dgrad(static_cast<const uint8_t*>(packed), fmt, E, N, K, dy, group_offsets, M, preact,
-                                      preact_dtype == MOE_BF16, dx, dx_dtype == MOE_BF16, act,
+                                      preact_dtype == MOE_BF16, dx, dx_dtype == MOE_BF16,
                                       static_cast<hipStream_t>(stream)));
 }
 

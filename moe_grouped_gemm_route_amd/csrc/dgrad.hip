@@ -16,9 +16,9 @@
 // a byte permute per pair of n sorts the words into two MFMA operands, the
 // even k and the odd k.
 //
-// The scales of a lane's eight n are the same for the 16 lanes of a group, so
-// they are laid out in LDS as bf16 bit patterns (E8M0 and E4M3 values are
-// exact in bf16), eight consecutive n per 16-byte read.
+// The scales of a lane's eight n are the same for the 16 lanes of a group (of
+// its halves, NVFP4); they are converted once per workgroup and laid out in
+// LDS as f32, eight consecutive n to two 16-byte reads.
 //
 // MFMA mapping (v_mfma_f32_16x16x32_bf16; lane l supplies one row of each
 // operand for eight slots of the sum, picked by g = l >> 4): the weights are
@@ -26,6 +26,8 @@
 // lane l of the result holds band row l & 15 and c = 4g .. 4g + 3: together
 // with the even/odd pair, eight consecutive columns, stored as whole 16-byte
 // words.
+#include <utility>
+
 #include "common.h"
 #include "launch.h"
 #include "wave.h"
@@ -39,7 +41,6 @@ constexpr int DG_BN = 64;                      // n per stage
 constexpr int DG_WAVES = 4;                    // 64 output columns each
 constexpr int DG_A_BYTES = DG_BM * DG_BN * 2;  // dy rows of 128 bytes
 constexpr int DG_C_BYTES = DG_BN * DG_BK / 2;  // eight chunks of 1 KiB
-constexpr int DG_NV_HALVES = 2;                // NVFP4: two scales per 32-block
 
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_void_t;
@@ -116,41 +117,44 @@ __device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, i
   return b;
 }
 
-// bf16 bit patterns of one lane's block scales, from its packed scale word.
-__device__ __forceinline__ uint16_t e8m0_bf16(uint32_t b) { return (uint16_t)(b << 7); }
-template <int SEL>
-__device__ __forceinline__ uint16_t e4m3_bf16(uint32_t w) {
-  return (uint16_t)(__float_as_uint(e4m3_to_f32<SEL>(w)) >> 16);
+// Codes and scales of eight n of two k columns, as they come from LDS, and the
+// two MFMA operands they decode to.
+struct RawWeights {
+  i32x2_t q;       // byte j: the codes of k even, k odd at n = j
+  f32x4_t s[2];    // scale of n = j at s[j / 4][j % 4]
+};
+struct Weights {
+  u32x4_t even, odd;
+};
+
+// Word M of both operands (n = 2M, 2M + 1).  ANY: scales that are not powers of
+// two take the exact product in f32 (at most six significant bits, so its
+// upper half is the bf16 value).
+template <bool ANY, int M>
+__device__ __forceinline__ void decode_word(const RawWeights& r, Weights& w) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const uint32_t q = (uint32_t)r.q[M / 2];
+  const float sa = r.s[M / 2][(M & 1) * 2], sb = r.s[M / 2][(M & 1) * 2 + 1];
+  constexpr int B = (M & 1) * 2;
+  if constexpr (ANY) {
+    const f32x2_t v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, B);
+    const f32x2_t v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, B + 1);
+    w.even[M] = __builtin_amdgcn_perm(__float_as_uint(v1[0] * sb), __float_as_uint(v0[0] * sa), 0x07060302u);
+    w.odd[M] = __builtin_amdgcn_perm(__float_as_uint(v1[1] * sb), __float_as_uint(v0[1] * sa), 0x07060302u);
+  } else {
+    const uint32_t p0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sa, B));
+    const uint32_t p1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sb, B + 1));
+    w.even[M] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);
+    w.odd[M] = __builtin_amdgcn_perm(p1, p0, 0x07060302u);
+  }
 }
 
-// Eight n of two k columns: byte j of q (codes of k even, k odd at n = j),
-// scaled by the bf16 pattern j of s, sorted into the even-k and odd-k MFMA
-// operands.  ANY: scales that are not powers of two take the exact product
-// in f32 (at most six significant bits, so its upper half is the bf16 value).
-template <bool ANY>
-__device__ __forceinline__ void decode_pair(i32x2_t q, u32x4_t s, u32x4_t& even, u32x4_t& odd) {
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w = (uint32_t)q[h];
-#define MOE_TWO(b0, b1, m)                                                                          \
-  {                                                                                                 \
-    const uint32_t sw = s[2 * h + m];                                                               \
-    const float s0 = __uint_as_float(sw << 16), s1 = __uint_as_float(sw & 0xFFFF0000u);             \
-    if constexpr (ANY) {                                                                            \
-      const f32x2_t v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, b0);                     \
-      const f32x2_t v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, b1);                     \
-      even[2 * h + m] = __builtin_amdgcn_perm(__float_as_uint(v1[0] * s1), __float_as_uint(v0[0] * s0), 0x07060302u); \
-      odd[2 * h + m] = __builtin_amdgcn_perm(__float_as_uint(v1[1] * s1), __float_as_uint(v0[1] * s0), 0x07060302u);  \
-    } else {                                                                                        \
-      const uint32_t p0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s0, b0)); \
-      const uint32_t p1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s1, b1)); \
-      even[2 * h + m] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);                                 \
-      odd[2 * h + m] = __builtin_amdgcn_perm(p1, p0, 0x07060302u);                                  \
-    }                                                                                               \
-  }
-    MOE_TWO(0, 1, 0) MOE_TWO(2, 3, 1)
-#undef MOE_TWO
+// Words [LO, HI) of the 2 x 4 words of two k blocks.
+template <bool ANY, int LO, int HI>
+__device__ __forceinline__ void decode_words(const RawWeights (&r)[2], Weights (&w)[2]) {
+  if constexpr (LO < HI) {
+    decode_word<ANY, LO % 4>(r[LO / 4], w[LO / 4]);
+    decode_words<ANY, LO + 1, HI>(r, w);
   }
 }
 
@@ -163,9 +167,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return (uint32_t)f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16);
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
-  if constexpr (BF16) {
+__device__ __forceinline__ void store8(void* p, bool bf16, int64_t i, const float (&v)[8]) {
+  if (bf16) {
     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) =
         make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
   } else {
@@ -204,15 +207,51 @@ __device__ __forceinline__ void silu_mul_grads(const float (&dh)[8], const float
   }
 }
 
+// One 32-n step: the NSUB row subtiles against the operands w, with the next
+// step's operands decoded from r into v on the way.  Each group is a subtile's
+// four matrix instructions, the LDS read of the subtile after next, and its
+// share of the decode, which issues in the shadow of the matrix instructions.
+template <bool ANY, int NSUB, int... MS, typename ROWS>
+__device__ __forceinline__ void dgrad_step(std::integer_sequence<int, MS...>, ROWS rows, const Weights (&w)[2],
+                                           const RawWeights (&r)[2], Weights (&v)[2], f32x4_t (&acc)[DG_MS][2][2]) {
+  constexpr int P = NSUB < 2 ? NSUB : 2;
+  u32x4_t x[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) x[i] = rows(i);
+  auto group = [&](auto mc) {
+    constexpr int ms = decltype(mc)::value;
+    const u32x4_t xa = x[ms % P];
+    acc[ms][0][0] = mfma16(w[0].even, xa, acc[ms][0][0]);
+    acc[ms][0][1] = mfma16(w[0].odd, xa, acc[ms][0][1]);
+    acc[ms][1][0] = mfma16(w[1].even, xa, acc[ms][1][0]);
+    acc[ms][1][1] = mfma16(w[1].odd, xa, acc[ms][1][1]);
+    if constexpr (ms + P < NSUB) x[ms % P] = rows(ms + P);
+    decode_words<ANY, 8 * ms / NSUB, 8 * (ms + 1) / NSUB>(r, v);
+    constexpr int VALU = (ANY ? 8 : 4) * (8 * (ms + 1) / NSUB - 8 * ms / NSUB);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  (group(std::integral_constant<int, MS>{}), ...);
+}
+
 struct DgradArgs {
   const uint8_t* packed;
   Layout L;
   const uint16_t* dy;
   const int32_t* off;
   int E, NB;            // experts, 256-column groups
-  const void* pre;      // [M, 2K] gate and up sums, or NULL (act 0)
+  const void* pre;      // [M, 2K] gate and up sums, or NULL (no activation)
   int pre_bf16;
   void* dx;
+  int dx_bf16;
 };
 
 // Ends a step: this wave's LDS operations are done, then the workgroup
@@ -224,11 +263,16 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int FMT, bool OBF16, int ACT>
+template <int FMT>
 __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
-  constexpr int S_BYTES = (FMT == 1 ? DG_NV_HALVES : 1) * DG_BN * (DG_BK / 32) * 2;
-  constexpr int STAGE = DG_A_BYTES + DG_C_BYTES + S_BYTES;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_stage[2 * STAGE];
+  // One stage of dy is computed while the next is loaded; codes and scales
+  // run one stage further ahead, so that a stage's first operands are decoded
+  // before the barrier that opens it.
+  constexpr int H = FMT == 1 ? 2 : 1;                    // scales per 32-block
+  constexpr int S_BYTES = H * DG_BN * (DG_BK / 32) * 4;
+  constexpr int CS_BYTES = DG_C_BYTES + S_BYTES;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_dy[2 * DG_A_BYTES];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_cs[3 * CS_BYTES];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -273,22 +317,14 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[ms][i >> 1][i & 1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  bool any = false;
-  if (FMT == 1) {
-    const uint32_t* flags = reinterpret_cast<const uint32_t*>(p.packed + L.flags_off) + et;
-    uint32_t f = 0;
-    for (int i = lane; i < L.NT; i += 64) f |= flags[i];
-    any = __ballot(f != 0) != 0;
-  }
-
   const int steps = N / DG_BN;
-  // A step's 4 KiB of dy, 2 KiB of codes and 256 bytes of scale words per
-  // wave, loaded into registers one step ahead and written to LDS once the
-  // step before is computed.  Past the last step the lane offsets lie outside
-  // the buffers, so the loads fetch nothing.
+  // A stage's 4 KiB of dy, and 2 KiB of codes and 256 bytes of scale words,
+  // per wave: loaded into registers, written to LDS once the stage before is
+  // computed.  Past the last step the lane offsets lie outside the buffers,
+  // so the loads fetch nothing.
   u32x4_t ra[4], rc[2];
   uint32_t rw;
-  auto load = [&](int i) {
+  auto load_codes = [&](int i) {
     const bool live = i < steps;
     const uint32_t q = live ? (uint32_t)i : 0u;
 #pragma unroll
@@ -296,85 +332,113 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
       rc[j] = __builtin_amdgcn_raw_buffer_load_b128(cr, live ? cvo[j] : kLaneOob, (q * (DG_BN / 16) * KC) << 10, 0);
     rw = __builtin_amdgcn_raw_buffer_load_b32(sr, live ? lane * 4 : kLaneOob,
                                               ((q * (DG_BN / 16) + wave) * groups + rec) * 256, 0);
+  };
+  auto load_dy = [&](int i) {
+    const bool live = i < steps;
+    const uint32_t q = live ? (uint32_t)i : 0u;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       ra[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, live ? avo[j] : kLaneOob, q * DG_BN * 2, 0);
   };
-  // Writes them to a stage: dy and codes as they are, the scale word (16-row
-  // block `wave`, row c16, k block g of both chunk columns) as bf16 patterns,
-  // [block][half][n].
-  auto put = [&](uint8_t* st) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(st + (wave * 4 + j) * 1024 + lane * 16) = ra[j];
+  // codes as they lie; the scale word (16-row block `wave`, row c16, k block g
+  // of both chunk columns) as f32, [block][half][n]
+  auto put_codes = [&](uint8_t* st) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<u32x4_t*>(st + DG_A_BYTES + (wave * 2 + j) * 1024 + lane * 16) = rc[j];
-    uint16_t* s = reinterpret_cast<uint16_t*>(st + DG_A_BYTES + DG_C_BYTES) + wave * 16 + c16;
+      *reinterpret_cast<u32x4_t*>(st + (wave * 2 + j) * 1024 + lane * 16) = rc[j];
+    float* s = reinterpret_cast<float*>(st + DG_C_BYTES) + wave * 16 + c16;
     if (FMT == 0) {
-      s[g * 64] = e8m0_bf16((rw >> (8 * (kc0 & 3))) & 0xFFu);
-      s[(4 + g) * 64] = e8m0_bf16((rw >> (8 * (kc0 & 3) + 8)) & 0xFFu);
+      s[g * 64] = e8m0_to_f32((rw >> (8 * (kc0 & 3))) & 0xFFu);
+      s[(4 + g) * 64] = e8m0_to_f32((rw >> (8 * (kc0 & 3) + 8)) & 0xFFu);
     } else {
-      s[(g * 2) * 64] = e4m3_bf16<0>(rw);
-      s[(g * 2 + 1) * 64] = e4m3_bf16<1>(rw);
-      s[((4 + g) * 2) * 64] = e4m3_bf16<2>(rw);
-      s[((4 + g) * 2 + 1) * 64] = e4m3_bf16<3>(rw);
+      s[(g * 2) * 64] = e4m3_to_f32<0>(rw);
+      s[(g * 2 + 1) * 64] = e4m3_to_f32<1>(rw);
+      s[((4 + g) * 2) * 64] = e4m3_to_f32<2>(rw);
+      s[((4 + g) * 2 + 1) * 64] = e4m3_to_f32<3>(rw);
     }
   };
-  auto compute = [&](auto nsub, const uint8_t* a) {
-    constexpr int NSUB = decltype(nsub)::value;
-    const uint8_t* c = a + DG_A_BYTES;
-    const uint8_t* sp = c + DG_C_BYTES;
+  auto put_dy = [&](uint8_t* st) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4_t w[2][2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int kb = kb0 + b;
-        const i32x2_t q = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (lds_i32x2_t)(c + (kc2 * 4 + 2 * s + (g >> 1)) * 1024 + kb * 256 + (g & 1) * 128 + c16 * 8));
-        const int blk = FMT == 0 ? kc2 * 4 + kb : (kc2 * 4 + kb) * 2 + (c16 >> 3);
-        const u32x4_t sc = *reinterpret_cast<const u32x4_t*>(sp + (blk * 64 + s * 32 + g * 8) * 2);
-        if (FMT == 1 && any) decode_pair<true>(q, sc, w[b][0], w[b][1]);
-        else decode_pair<false>(q, sc, w[b][0], w[b][1]);
-      }
-#pragma unroll
-      for (int ms = 0; ms < NSUB; ++ms) {
-        const int row = ms * 16 + c16;
-        const u32x4_t x =
-            *reinterpret_cast<const u32x4_t*>(a + row * 128 + (((s * 4 + g) ^ ((row >> 1) & 7)) << 4));
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          acc[ms][b][0] = mfma16(w[b][0], x, acc[ms][b][0]);
-          acc[ms][b][1] = mfma16(w[b][1], x, acc[ms][b][1]);
-        }
-      }
-    }
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(st + (wave * 4 + j) * 1024 + lane * 16) = ra[j];
   };
 
-  // step i + 1 loads while step i computes; the walk of a tile with fewer
-  // rows leaves out the subtiles it does not have
-  load(0);
-  put(s_stage);
-  lds_barrier();
-  auto walk = [&](auto nsub) {
-    for (int i = 0; i < steps; ++i) {
-      load(i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(nsub, s_stage + (i & 1) * STAGE);
-      put(s_stage + (~i & 1) * STAGE);
-      lds_barrier();
+  // Step s (32 n) of a stage: codes and scales of this wave's two k blocks,
+  // and the band rows of subtile ms.
+  const uint32_t q_off = (kc2 * 4 + (g >> 1)) * 1024 + kb0 * 256 + (g & 1) * 128 + c16 * 8;
+  const uint32_t s_off = DG_C_BYTES + ((((kc2 * 4 + kb0) * H + (H == 2 ? c16 >> 3 : 0)) * 64 + g * 8) << 2);
+  const uint32_t a_off = c16 * 128 + ((g ^ ((c16 >> 1) & 7)) << 4);
+  auto raw = [&](const uint8_t* st, int s, RawWeights (&r)[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      r[b].q = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(st + q_off + s * 2048 + b * 256));
+      const f32x4_t* sc = reinterpret_cast<const f32x4_t*>(st + s_off + s * 128 + b * 256 * H);
+      r[b].s[0] = sc[0];
+      r[b].s[1] = sc[1];
     }
   };
-  switch ((tile.rows + 15) >> 4) {
-    case 1: walk(std::integral_constant<int, 1>{}); break;
-    case 2: walk(std::integral_constant<int, 2>{}); break;
-    case 3: walk(std::integral_constant<int, 3>{}); break;
-    case 4: walk(std::integral_constant<int, 4>{}); break;
-    case 5: walk(std::integral_constant<int, 5>{}); break;
-    case 6: walk(std::integral_constant<int, 6>{}); break;
-    case 7: walk(std::integral_constant<int, 7>{}); break;
-    default: walk(std::integral_constant<int, 8>{}); break;
+  auto rows = [&](const uint8_t* a, int s, int ms) {
+    return *reinterpret_cast<const u32x4_t*>(a + (a_off ^ (s * 64)) + ms * 2048);
+  };
+
+  // The walk of a tile with nsub 16-row subtiles: the operands of a step are
+  // decoded among the matrix instructions of the step before.
+  auto walk = [&](auto any, auto nsub) {
+    constexpr bool any_v = decltype(any)::value;
+    constexpr int NSUB = decltype(nsub)::value;
+    uint8_t* c0 = s_cs;
+    uint8_t* c1 = s_cs + CS_BYTES;
+    uint8_t* c2 = s_cs + 2 * CS_BYTES;
+    load_codes(0);
+    load_dy(0);
+    put_codes(c0);
+    load_codes(1);
+    put_dy(s_dy);
+    put_codes(c1);
+    lds_barrier();
+    RawWeights r[2];
+    Weights w[2], v[2];
+    raw(c0, 0, r);
+    decode_words<any_v, 0, 8>(r, w);
+    for (int i = 0; i < steps; ++i) {
+      const uint8_t* a = s_dy + (i & 1) * DG_A_BYTES;
+      load_codes(i + 2);
+      load_dy(i + 1);
+      raw(c0, 1, r);
+      __builtin_amdgcn_sched_barrier(0);
+      dgrad_step<any_v, NSUB>(std::make_integer_sequence<int, NSUB>{}, [&](int ms) { return rows(a, 0, ms); }, w, r, v, acc);
+      raw(c1, 0, r);
+      __builtin_amdgcn_sched_barrier(0);
+      dgrad_step<any_v, NSUB>(std::make_integer_sequence<int, NSUB>{}, [&](int ms) { return rows(a, 1, ms); }, v, r, w, acc);
+      put_dy(s_dy + (~i & 1) * DG_A_BYTES);
+      put_codes(c2);
+      lds_barrier();
+      uint8_t* c = c0;
+      c0 = c1;
+      c1 = c2;
+      c2 = c;
+    }
+  };
+  auto walk_any = [&](auto any) {
+    switch ((tile.rows + 15) >> 4) {
+      case 1: walk(any, std::integral_constant<int, 1>{}); break;
+      case 2: walk(any, std::integral_constant<int, 2>{}); break;
+      case 3: walk(any, std::integral_constant<int, 3>{}); break;
+      case 4: walk(any, std::integral_constant<int, 4>{}); break;
+      case 5: walk(any, std::integral_constant<int, 5>{}); break;
+      case 6: walk(any, std::integral_constant<int, 6>{}); break;
+      case 7: walk(any, std::integral_constant<int, 7>{}); break;
+      default: walk(any, std::integral_constant<int, 8>{}); break;
+    }
+  };
+  bool any = false;
+  if (FMT == 1) {
+    const uint32_t* flags = reinterpret_cast<const uint32_t*>(p.packed + L.flags_off) + et;
+    uint32_t f = 0;
+    for (int i = lane; i < L.NT; i += 64) f |= flags[i];
+    any = __ballot(f != 0) != 0;
   }
+  if (FMT == 1 && any) walk_any(std::true_type{});
+  else walk_any(std::false_type{});
 
   if (kc0 + kc2 >= KC) return;
   const float post = FMT == 1 ? reinterpret_cast<const float*>(p.packed + L.tscale_off)[tile.e] : 1.0f;
@@ -392,15 +456,15 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
         v[2 * i] = acc[ms][b][0][i] * post;
         v[2 * i + 1] = acc[ms][b][1][i] * post;
       }
-      if (ACT == 1) {
+      if (p.pre) {
         float gate[8], up[8], dg[8], du[8];
         load8(p.pre, p.pre_bf16, row * 2 * K + col, gate);
         load8(p.pre, p.pre_bf16, row * 2 * K + K + col, up);
         silu_mul_grads(v, gate, up, dg, du);
-        store8<OBF16>(p.dx, row * 2 * K + col, dg);
-        store8<OBF16>(p.dx, row * 2 * K + K + col, du);
+        store8(p.dx, p.dx_bf16, row * 2 * K + col, dg);
+        store8(p.dx, p.dx_bf16, row * 2 * K + K + col, du);
       } else {
-        store8<OBF16>(p.dx, row * K + col, v);
+        store8(p.dx, p.dx_bf16, row * K + col, v);
       }
     }
   }
@@ -413,14 +477,9 @@ int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M) {
   return tiles * ((K + DG_BK - 1) / DG_BK);
 }
 
-template <int FMT, bool OBF16, int ACT>
-static void launch_dgrad_t(const DgradArgs& a, int64_t groups, hipStream_t stream) {
-  hipLaunchKernelGGL((dgrad_kernel<FMT, OBF16, ACT>), dim3((unsigned)groups), dim3(DG_WAVES * 64), 0, stream, a);
-}
-
 hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
                         const int32_t* group_offsets, int32_t M, const void* preact, int preact_bf16, void* dx,
-                        int dx_bf16, int act, hipStream_t stream) {
+                        int dx_bf16, hipStream_t stream) {
   DgradArgs a;
   a.packed = packed;
   a.L = make_layout(fmt, E, N, K);
@@ -431,14 +490,10 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
   a.pre = preact;
   a.pre_bf16 = preact_bf16;
   a.dx = dx;
-  const int64_t groups = dgrad_workgroups(E, K, M);
-  if (fmt == 0) {
-    if (dx_bf16) act ? launch_dgrad_t<0, true, 1>(a, groups, stream) : launch_dgrad_t<0, true, 0>(a, groups, stream);
-    else act ? launch_dgrad_t<0, false, 1>(a, groups, stream) : launch_dgrad_t<0, false, 0>(a, groups, stream);
-  } else {
-    if (dx_bf16) act ? launch_dgrad_t<1, true, 1>(a, groups, stream) : launch_dgrad_t<1, true, 0>(a, groups, stream);
-    else act ? launch_dgrad_t<1, false, 1>(a, groups, stream) : launch_dgrad_t<1, false, 0>(a, groups, stream);
-  }
+  a.dx_bf16 = dx_bf16;
+  const dim3 grid((unsigned)dgrad_workgroups(E, K, M)), block(DG_WAVES * 64);
+  if (fmt == 0) hipLaunchKernelGGL(dgrad_kernel<0>, grid, block, 0, stream, a);
+  else hipLaunchKernelGGL(dgrad_kernel<1>, grid, block, 0, stream, a);
   return hipGetLastError();
 }
 

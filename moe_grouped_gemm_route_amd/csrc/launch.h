@@ -112,11 +112,11 @@ hipError_t launch_combine_bwd(const void* dout, int dout_bf16, const void* y, in
 hipError_t launch_silu_mul(const void* y, int y_bf16, int32_t M, int32_t N, const int32_t* n_rows, void* h,
                            int h_bf16, hipStream_t stream);
 
-// Gradient of the grouped matmul's input; act 1 also takes it through the
-// SiLU-gated activation of preact [M, 2K].
+// Gradient of the grouped matmul's input; with preact [M, 2K] (NULL: none) it
+// goes on through the SiLU-gated activation.
 hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
                         const int32_t* group_offsets, int32_t M, const void* preact, int preact_bf16, void* dx,
-                        int dx_bf16, int act, hipStream_t stream);
+                        int dx_bf16, hipStream_t stream);
 int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M);
 
 }  // namespace moe
