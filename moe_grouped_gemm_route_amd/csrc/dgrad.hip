@@ -34,12 +34,9 @@
 
 namespace moe {
 
-constexpr int DG_BM = 128;                     // band rows per workgroup
-constexpr int DG_MS = DG_BM / 16;              // 16-row subtiles
 constexpr int DG_BK = 256;                     // output columns per workgroup: two chunks of the pack
 constexpr int DG_BN = 64;                      // n per stage
 constexpr int DG_WAVES = 4;                    // 64 output columns each
-constexpr int DG_A_BYTES = DG_BM * DG_BN * 2;  // dy rows of 128 bytes
 constexpr int DG_C_BYTES = DG_BN * DG_BK / 2;  // eight chunks of 1 KiB
 
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
@@ -209,35 +206,39 @@ __device__ __forceinline__ void silu_mul_grads(const float (&dh)[8], const float
 
 // One 32-n step: the NSUB row subtiles against the operands w, with the next
 // step's operands decoded from r into v on the way.  Each group is a subtile's
-// four matrix instructions, the LDS read of the subtile after next, and its
+// four matrix instructions, the LDS read of the subtile after next, and a
 // share of the decode, which issues in the shadow of the matrix instructions.
-template <bool ANY, int NSUB, int... MS, typename ROWS>
-__device__ __forceinline__ void dgrad_step(std::integer_sequence<int, MS...>, ROWS rows, const Weights (&w)[2],
-                                           const RawWeights (&r)[2], Weights (&v)[2], f32x4_t (&acc)[DG_MS][2][2]) {
-  constexpr int P = NSUB < 2 ? NSUB : 2;
-  u32x4_t x[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) x[i] = rows(i);
+// The last group has no decode where there are others: it issues the LDS reads
+// that the next step starts with (next).
+template <bool ANY, int NSUB, int MAX, int... MS, typename ROWS, typename NEXT>
+__device__ __forceinline__ void dgrad_step(std::integer_sequence<int, MS...>, u32x4_t (&x)[2], ROWS rows, NEXT next,
+                                           const Weights (&w)[2], const RawWeights (&r)[2], Weights (&v)[2],
+                                           f32x4_t (&acc)[MAX][2][2]) {
+  constexpr int DEC = NSUB > 1 ? NSUB - 1 : 1;   // groups that decode
   auto group = [&](auto mc) {
     constexpr int ms = decltype(mc)::value;
-    const u32x4_t xa = x[ms % P];
+    const u32x4_t xa = x[ms & 1];
     acc[ms][0][0] = mfma16(w[0].even, xa, acc[ms][0][0]);
     acc[ms][0][1] = mfma16(w[0].odd, xa, acc[ms][0][1]);
     acc[ms][1][0] = mfma16(w[1].even, xa, acc[ms][1][0]);
     acc[ms][1][1] = mfma16(w[1].odd, xa, acc[ms][1][1]);
-    if constexpr (ms + P < NSUB) x[ms % P] = rows(ms + P);
-    decode_words<ANY, 8 * ms / NSUB, 8 * (ms + 1) / NSUB>(r, v);
-    constexpr int VALU = (ANY ? 8 : 4) * (8 * (ms + 1) / NSUB - 8 * ms / NSUB);
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+    if constexpr (ms + 2 < NSUB) x[ms & 1] = rows(ms + 2);
+    if constexpr (ms < DEC) {
+      constexpr int LO = 8 * ms / DEC, HI = 8 * (ms + 1) / DEC;
+      decode_words<ANY, LO, HI>(r, v);
+      constexpr int VALU = (ANY ? 8 : 4) * (HI - LO);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (ms == NSUB - 1) next();
   };
   (group(std::integral_constant<int, MS>{}), ...);
 }
@@ -263,22 +264,25 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int FMT>
-__global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
+template <int FMT, int MS, int OCC>
+__global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) {
   // One stage of dy is computed while the next is loaded; codes and scales
   // run one stage further ahead, so that a stage's first operands are decoded
   // before the barrier that opens it.
+  constexpr int BM = MS * 16;                            // band rows per workgroup
+  constexpr int A_BYTES = BM * DG_BN * 2;                // dy rows of 128 bytes
+  constexpr int A_LOADS = A_BYTES / 1024 / DG_WAVES;     // 1 KiB loads per wave
   constexpr int H = FMT == 1 ? 2 : 1;                    // scales per 32-block
   constexpr int S_BYTES = H * DG_BN * (DG_BK / 32) * 4;
   constexpr int CS_BYTES = DG_C_BYTES + S_BYTES;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_dy[2 * DG_A_BYTES];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_dy[2 * A_BYTES];
   __shared__ __attribute__((aligned(1024))) uint8_t s_cs[3 * CS_BYTES];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g = lane >> 4;
   int nb;
-  const BandTile tile = find_tile<DG_BM>(p.off, p.E, p.NB, nb);
+  const BandTile tile = find_tile<BM>(p.off, p.E, p.NB, nb);
   if (tile.rows == 0) return;
   const Layout& L = p.L;
   const int N = (int)L.N, K = (int)L.K, KC = (int)L.KC;
@@ -300,10 +304,10 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
   // each, lane l landing in row l / 8 at segment l & 7, which holds the row's
   // segment (l & 7) ^ (row / 2 & 7): the 16 rows of a fragment read then fall
   // into 16 different 16-byte bank groups
-  uint32_t avo[4], cvo[2];
+  uint32_t avo[A_LOADS], cvo[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int row = (wave * 4 + j) * 8 + (lane >> 3);
+  for (int j = 0; j < A_LOADS; ++j) {
+    const int row = (wave * A_LOADS + j) * 8 + (lane >> 3);
     avo[j] = row < tile.rows ? (uint32_t)row * N * 2 + (((lane & 7) ^ ((row >> 1) & 7)) << 4) : kLaneOob;
   }
   // chunk column (wave >> 1) of the workgroup, 16-row blocks (wave & 1)*2 + j
@@ -311,18 +315,18 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
   for (int j = 0; j < 2; ++j)
     cvo[j] = kc0 + kc2 < KC ? (uint32_t)((((kb0 + j) * KC + kc0 + kc2) << 10) + lane * 16) : kLaneOob;
 
-  f32x4_t acc[DG_MS][2][2];
+  f32x4_t acc[MS][2][2];
 #pragma unroll
-  for (int ms = 0; ms < DG_MS; ++ms)
+  for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[ms][i >> 1][i & 1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const int steps = N / DG_BN;
-  // A stage's 4 KiB of dy, and 2 KiB of codes and 256 bytes of scale words,
+  // A stage's share of dy, and 2 KiB of codes and 256 bytes of scale words,
   // per wave: loaded into registers, written to LDS once the stage before is
   // computed.  Past the last step the lane offsets lie outside the buffers,
   // so the loads fetch nothing.
-  u32x4_t ra[4], rc[2];
+  u32x4_t ra[A_LOADS], rc[2];
   uint32_t rw;
   auto load_codes = [&](int i) {
     const bool live = i < steps;
@@ -337,7 +341,7 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
     const bool live = i < steps;
     const uint32_t q = live ? (uint32_t)i : 0u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < A_LOADS; ++j)
       ra[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, live ? avo[j] : kLaneOob, q * DG_BN * 2, 0);
   };
   // codes as they lie; the scale word (16-row block `wave`, row c16, k block g
@@ -359,7 +363,8 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
   };
   auto put_dy = [&](uint8_t* st) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(st + (wave * 4 + j) * 1024 + lane * 16) = ra[j];
+    for (int j = 0; j < A_LOADS; ++j)
+      *reinterpret_cast<u32x4_t*>(st + (wave * A_LOADS + j) * 1024 + lane * 16) = ra[j];
   };
 
   // Step s (32 n) of a stage: codes and scales of this wave's two k blocks,
@@ -399,17 +404,25 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
     Weights w[2], v[2];
     raw(c0, 0, r);
     decode_words<any_v, 0, 8>(r, w);
+    raw(c0, 1, r);
     for (int i = 0; i < steps; ++i) {
-      const uint8_t* a = s_dy + (i & 1) * DG_A_BYTES;
+      const uint8_t* a = s_dy + (i & 1) * A_BYTES;
+      u32x4_t x[2];
+      auto first_rows = [&](int s) {
+        x[0] = rows(a, s, 0);
+        if constexpr (NSUB > 1) x[1] = rows(a, s, 1);
+      };
+      first_rows(0);
+      __builtin_amdgcn_sched_barrier(0);
       load_codes(i + 2);
       load_dy(i + 1);
-      raw(c0, 1, r);
       __builtin_amdgcn_sched_barrier(0);
-      dgrad_step<any_v, NSUB>(std::make_integer_sequence<int, NSUB>{}, [&](int ms) { return rows(a, 0, ms); }, w, r, v, acc);
-      raw(c1, 0, r);
+      dgrad_step<any_v, NSUB, MS>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 0, ms); },
+                              [&] { first_rows(1); raw(c1, 0, r); }, w, r, v, acc);
+      dgrad_step<any_v, NSUB, MS>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 1, ms); },
+                              [&] { raw(c1, 1, r); }, v, r, w, acc);
       __builtin_amdgcn_sched_barrier(0);
-      dgrad_step<any_v, NSUB>(std::make_integer_sequence<int, NSUB>{}, [&](int ms) { return rows(a, 1, ms); }, v, r, w, acc);
-      put_dy(s_dy + (~i & 1) * DG_A_BYTES);
+      put_dy(s_dy + (~i & 1) * A_BYTES);
       put_codes(c2);
       lds_barrier();
       uint8_t* c = c0;
@@ -419,15 +432,21 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
     }
   };
   auto walk_any = [&](auto any) {
-    switch ((tile.rows + 15) >> 4) {
-      case 1: walk(any, std::integral_constant<int, 1>{}); break;
-      case 2: walk(any, std::integral_constant<int, 2>{}); break;
-      case 3: walk(any, std::integral_constant<int, 3>{}); break;
-      case 4: walk(any, std::integral_constant<int, 4>{}); break;
-      case 5: walk(any, std::integral_constant<int, 5>{}); break;
-      case 6: walk(any, std::integral_constant<int, 6>{}); break;
-      case 7: walk(any, std::integral_constant<int, 7>{}); break;
-      default: walk(any, std::integral_constant<int, 8>{}); break;
+    const int nsub = (tile.rows + 15) >> 4;
+    if constexpr (MS == 8) {
+      switch (nsub) {
+        case 1: walk(any, std::integral_constant<int, 1>{}); break;
+        case 2: walk(any, std::integral_constant<int, 2>{}); break;
+        case 3: walk(any, std::integral_constant<int, 3>{}); break;
+        case 4: walk(any, std::integral_constant<int, 4>{}); break;
+        case 5: walk(any, std::integral_constant<int, 5>{}); break;
+        case 6: walk(any, std::integral_constant<int, 6>{}); break;
+        case 7: walk(any, std::integral_constant<int, 7>{}); break;
+        default: walk(any, std::integral_constant<int, 8>{}); break;
+      }
+    } else {
+      if (nsub == 1) walk(any, std::integral_constant<int, 1>{});
+      else walk(any, std::integral_constant<int, MS>{});
     }
   };
   bool any = false;
@@ -443,7 +462,7 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
   if (kc0 + kc2 >= KC) return;
   const float post = FMT == 1 ? reinterpret_cast<const float*>(p.packed + L.tscale_off)[tile.e] : 1.0f;
 #pragma unroll
-  for (int ms = 0; ms < DG_MS; ++ms) {
+  for (int ms = 0; ms < MS; ++ms) {
     const int rl = ms * 16 + c16;
     if (rl >= tile.rows) continue;
     const int64_t row = tile.m0 + rl;
@@ -470,10 +489,13 @@ __global__ __launch_bounds__(DG_WAVES * 64, 2) void dgrad_kernel(DgradArgs p) {
   }
 }
 
+// Row subtiles of a workgroup's tile.
+static int dgrad_subtiles(int32_t E, int32_t M) { return (int64_t)M >= 24 * (int64_t)E ? 8 : 2; }
+
 // Workgroups: an upper bound on the row tiles (a band of c rows has at most
 // c / BM + 1) times the column groups.
 int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M) {
-  const int64_t tiles = (int64_t)M / DG_BM + (E < M ? E : M);
+  const int64_t tiles = (int64_t)M / (16 * dgrad_subtiles(E, M)) + (E < M ? E : M);
   return tiles * ((K + DG_BK - 1) / DG_BK);
 }
 
@@ -492,8 +514,13 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
   a.dx = dx;
   a.dx_bf16 = dx_bf16;
   const dim3 grid((unsigned)dgrad_workgroups(E, K, M)), block(DG_WAVES * 64);
-  if (fmt == 0) hipLaunchKernelGGL(dgrad_kernel<0>, grid, block, 0, stream, a);
-  else hipLaunchKernelGGL(dgrad_kernel<1>, grid, block, 0, stream, a);
+  if (dgrad_subtiles(E, M) == 8) {
+    if (fmt == 0) hipLaunchKernelGGL((dgrad_kernel<0, 8, 2>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((dgrad_kernel<1, 8, 2>), grid, block, 0, stream, a);
+  } else {
+    if (fmt == 0) hipLaunchKernelGGL((dgrad_kernel<0, 2, 4>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((dgrad_kernel<1, 2, 3>), grid, block, 0, stream, a);
+  }
   return hipGetLastError();
 }
 
