@@ -39,6 +39,8 @@ constexpr int DG_BN = 64;                      // n per stage
 constexpr int DG_WAVES = 4;                    // 64 output columns each
 constexpr int DG_C_BYTES = DG_BN * DG_BK / 2;  // eight chunks of 1 KiB
 
+constexpr int DG_NT = 2;                       // buffer-load cache policy of the codes: non-temporal
+
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_void_t;
 typedef __attribute__((address_space(3))) i32x2_t* lds_i32x2_t;
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) 
     const uint32_t q = live ? (uint32_t)i : 0u;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      rc[j] = __builtin_amdgcn_raw_buffer_load_b128(cr, live ? cvo[j] : kLaneOob, (q * (DG_BN / 16) * KC) << 10, 0);
+      rc[j] = __builtin_amdgcn_raw_buffer_load_b128(cr, live ? cvo[j] : kLaneOob, (q * (DG_BN / 16) * KC) << 10, DG_NT);
     rw = __builtin_amdgcn_raw_buffer_load_b32(sr, live ? lane * 4 : kLaneOob,
                                               ((q * (DG_BN / 16) + wave) * groups + rec) * 256, 0);
   };
