@@ -104,7 +104,13 @@ def _ptr(t):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream of the current device, as a pointer value."""
+    return _raw_stream(torch.cuda.current_device())
+
+
+# the pointer without a Stream object around it (2.7 us of a call otherwise)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _dev(t, dtype, name, ndim=None):
@@ -326,13 +332,14 @@ def _float(t, name, ndim):
     return _FLOATS[t.dtype]
 
 
-def _out(out, shape, dtype, name, dev):
-    """out checked, or a new tensor; dtype is an F32/BF16 enum or a torch dtype."""
+def _out(out, shape, dtype, name, like):
+    """out checked, or a new tensor beside `like`; dtype is an F32/BF16 enum or
+    a torch dtype."""
     dtype = _OUT.get(dtype, dtype)
     if not isinstance(dtype, torch.dtype):
         raise MoeGmmError("the type of %s must be F32 or BF16" % name)
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     _dev(out, dtype, name, len(shape))
     if tuple(out.shape) != tuple(shape):
         raise MoeGmmError("%s must be %s" % (name, list(shape)))
@@ -341,16 +348,18 @@ def _out(out, shape, dtype, name, dev):
 
 def _launch(fn, tensors, *args):
     """fn(*args, stream) on the device that holds every tensor of tensors (None
-    skipped), on that device's current stream."""
-    dev = tensors[0].device
+    skipped; a tensor in args stands for its pointer), on that device's current
+    stream."""
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise MoeGmmError("the tensors must be on one device, got %s and %s" % (dev, t.device))
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream()))
+        if t is not None and t.get_device() != index:
+            raise MoeGmmError("the tensors must be on one device, got %s and %s" % (tensors[0].device, t.device))
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    if index == torch.cuda.current_device():
+        _check(fn(*args, _raw_stream(index)))
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream()))
+        with torch.cuda.device(index):
+            _check(fn(*args, _raw_stream(index)))
 
 
 def topk_gate(logits, k, score=GATE_SOFTMAX, bias=None, renormalize=True, scale=1.0):
@@ -363,10 +372,10 @@ def topk_gate(logits, k, score=GATE_SOFTMAX, bias=None, renormalize=True, scale=
         _dev(bias, torch.float32, "bias", 1)
         if bias.numel() != E:
             raise MoeGmmError("bias must have E entries")
-    ids = torch.empty((T, max(0, k)), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, max(0, k)), dtype=torch.float32, device=logits.device)
-    _launch(library().moe_topk_gate, (logits, bias), _ptr(logits), dt, _ptr(bias), T, E, k, score,
-            int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights))
+    ids = logits.new_empty((T, max(0, k)), dtype=torch.int32)
+    weights = logits.new_empty((T, max(0, k)), dtype=torch.float32)
+    _launch(library().moe_topk_gate, (logits, bias), logits, dt, bias, T, E, k, score,
+            int(bool(renormalize)), float(scale), ids, weights)
     return ids, weights
 
 
@@ -381,8 +390,8 @@ def topk_gate_bwd(logits, topk_ids, dweights, score=GATE_SOFTMAX, renormalize=Tr
     if topk_ids.shape[0] != T or dweights.shape != topk_ids.shape:
         raise MoeGmmError("topk_ids and dweights must be [T, k]")
     out = torch.empty_like(logits)
-    _launch(library().moe_topk_gate_bwd, (logits, topk_ids, dweights), _ptr(logits), dt, _ptr(topk_ids),
-            _ptr(dweights), T, E, topk_ids.shape[1], score, int(bool(renormalize)), float(scale), _ptr(out))
+    _launch(library().moe_topk_gate_bwd, (logits, topk_ids, dweights), logits, dt, topk_ids,
+            dweights, T, E, topk_ids.shape[1], score, int(bool(renormalize)), float(scale), out)
     return out
 
 
@@ -406,8 +415,8 @@ def moe_dispatch(x, pair_row, k, out=None):
     if out is not None:
         _dev(out, x.dtype, "out", 2)
         rows = out.shape[0]
-    out = _out(out, (rows, N), x.dtype, "out", x.device)
-    _launch(library().moe_dispatch, (x, pair_row, out), _ptr(x), dt, _ptr(pair_row), T, k, N, rows, _ptr(out))
+    out = _out(out, (rows, N), x.dtype, "out", x)
+    _launch(library().moe_dispatch, (x, pair_row, out), x, dt, pair_row, T, k, N, rows, out)
     return out
 
 
@@ -417,8 +426,8 @@ def moe_dispatch_bwd(dxs, pair_row, k, out_dtype=F32):
     dt = _float(dxs, "dxs", 2)
     T = _pairs(pair_row, k)
     rows, N = dxs.shape
-    dx = _out(None, (T, N), out_dtype, "dx", dxs.device)
-    _launch(library().moe_dispatch_bwd, (dxs, pair_row), _ptr(dxs), dt, _ptr(pair_row), T, k, N, rows, _ptr(dx),
+    dx = _out(None, (T, N), out_dtype, "dx", dxs)
+    _launch(library().moe_dispatch_bwd, (dxs, pair_row), dxs, dt, pair_row, T, k, N, rows, dx,
             _FLOATS[dx.dtype])
     return dx
 
@@ -435,10 +444,10 @@ def moe_combine_bwd(dout, y, topk_weights, pair_row, out_dtype=F32, out=None):
     rows, N = y.shape
     if _pairs(pair_row, k) != T or tuple(dout.shape) != (T, N):
         raise MoeGmmError("dout must be [T, N] and pair_row must have T*k entries")
-    dy = _out(out, (rows, N), out_dtype, "out", y.device)
-    dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
-    _launch(library().moe_combine_bwd, (dout, y, topk_weights, pair_row, dy), _ptr(dout), gdt, _ptr(y), ydt,
-            _ptr(topk_weights), _ptr(pair_row), T, k, N, rows, _ptr(dy), _FLOATS[dy.dtype], _ptr(dweights))
+    dy = _out(out, (rows, N), out_dtype, "out", y)
+    dweights = torch.empty_like(topk_weights)
+    _launch(library().moe_combine_bwd, (dout, y, topk_weights, pair_row, dy), dout, gdt, y, ydt,
+            topk_weights, pair_row, T, k, N, rows, dy, _FLOATS[dy.dtype], dweights)
     return dy, dweights
 
 
@@ -453,9 +462,9 @@ def silu_mul(y, group_offsets=None, out_dtype=F32, out=None):
         _dev(group_offsets, torch.int32, "group_offsets", 1)
         if group_offsets.numel() < 2:
             raise MoeGmmError("group_offsets must have E+1 entries")
-        n_rows = ctypes.c_void_p(group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1))
-    h = _out(out, (M, N // 2), out_dtype, "out", y.device)
-    _launch(library().moe_silu_mul, (y, group_offsets, h), _ptr(y), dt, M, N, n_rows, _ptr(h), _FLOATS[h.dtype])
+        n_rows = group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1)
+    h = _out(out, (M, N // 2), out_dtype, "out", y)
+    _launch(library().moe_silu_mul, (y, group_offsets, h), y, dt, M, N, n_rows, h, _FLOATS[h.dtype])
     return h
 
 
@@ -478,9 +487,9 @@ def moe_gmm_dgrad(packed, fmt, E, N, K, dy, group_offsets, M, out_dtype=F32, act
         pdt = _float(preact, "preact", 2)
         if tuple(preact.shape) != (M, 2 * K):
             raise MoeGmmError("preact must be [M, 2K]")
-    dx = _out(out, (M, 2 * K if act == ACT_SILU_MUL else K), out_dtype, "out", packed.device)
-    _launch(library().moe_gmm_dgrad, (packed, db, group_offsets, preact, dx), _ptr(packed), fmt, E, N, K, _ptr(db),
-            _ptr(group_offsets), M, _ptr(preact), pdt, _ptr(dx), _FLOATS[dx.dtype], act)
+    dx = _out(out, (M, 2 * K if act == ACT_SILU_MUL else K), out_dtype, "out", packed)
+    _launch(library().moe_gmm_dgrad, (packed, db, group_offsets, preact, dx), packed, fmt, E, N, K, db,
+            group_offsets, M, preact, pdt, dx, _FLOATS[dx.dtype], act)
     return dx
 
 

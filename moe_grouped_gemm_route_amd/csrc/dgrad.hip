@@ -39,6 +39,7 @@ constexpr int DG_BN = 64;                      // n per stage
 constexpr int DG_WAVES = 4;                    // 64 output columns each
 constexpr int DG_C_BYTES = DG_BN * DG_BK / 2;  // eight chunks of 1 KiB
 
+constexpr int DG_CUS = 256;
 constexpr int DG_NT = 2;                       // buffer-load cache policy of the codes: non-temporal
 
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
@@ -266,8 +267,11 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int FMT, int MS, int OCC>
-__global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) {
+// NS groups of four waves share a workgroup; each walks its share of n (in
+// whole stages, the last share padded with empty ones) through LDS of its own,
+// and the first adds up the partial sums in order.
+template <int FMT, int MS, int OCC, int NS>
+__global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   // One stage of dy is computed while the next is loaded; codes and scales
   // run one stage further ahead, so that a stage's first operands are decoded
   // before the barrier that opens it.
@@ -277,11 +281,16 @@ __global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) 
   constexpr int H = FMT == 1 ? 2 : 1;                    // scales per 32-block
   constexpr int S_BYTES = H * DG_BN * (DG_BK / 32) * 4;
   constexpr int CS_BYTES = DG_C_BYTES + S_BYTES;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_dy[2 * A_BYTES];
-  __shared__ __attribute__((aligned(1024))) uint8_t s_cs[3 * CS_BYTES];
+  constexpr int GROUP_BYTES = 2 * A_BYTES + 3 * CS_BYTES;
+  constexpr int PART_BYTES = DG_WAVES * MS * 4 * 64 * 16;   // a group's accumulators
+  static_assert((NS - 1) * PART_BYTES <= NS * GROUP_BYTES, "the partial sums fit the stages");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_all[NS * GROUP_BYTES];
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & (DG_WAVES - 1));
+  const int part = NS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (DG_WAVES * 64)) : 0;
+  uint8_t* s_dy = s_all + part * GROUP_BYTES;
+  uint8_t* s_cs = s_dy + 2 * A_BYTES;
   const int c16 = lane & 15, g = lane >> 4;
   int nb;
   const BandTile tile = find_tile<BM>(p.off, p.E, p.NB, nb);
@@ -323,16 +332,18 @@ __global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) 
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[ms][i >> 1][i & 1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const int steps = N / DG_BN;
+  // stages [first, end) of this group; every group runs `steps`
+  const int steps = (N / DG_BN + NS - 1) / NS;
+  const int first = part * steps, end = min(N / DG_BN, first + steps);
   // A stage's share of dy, and 2 KiB of codes and 256 bytes of scale words,
   // per wave: loaded into registers, written to LDS once the stage before is
-  // computed.  Past the last step the lane offsets lie outside the buffers,
-  // so the loads fetch nothing.
+  // computed.  Past the last stage the lane offsets lie outside the buffers,
+  // so the loads fetch nothing and return zeros.
   u32x4_t ra[A_LOADS], rc[2];
   uint32_t rw;
   auto load_codes = [&](int i) {
-    const bool live = i < steps;
-    const uint32_t q = live ? (uint32_t)i : 0u;
+    const bool live = first + i < end;
+    const uint32_t q = live ? (uint32_t)(first + i) : 0u;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       rc[j] = __builtin_amdgcn_raw_buffer_load_b128(cr, live ? cvo[j] : kLaneOob, (q * (DG_BN / 16) * KC) << 10, DG_NT);
@@ -340,8 +351,8 @@ __global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) 
                                               ((q * (DG_BN / 16) + wave) * groups + rec) * 256, 0);
   };
   auto load_dy = [&](int i) {
-    const bool live = i < steps;
-    const uint32_t q = live ? (uint32_t)i : 0u;
+    const bool live = first + i < end;
+    const uint32_t q = live ? (uint32_t)(first + i) : 0u;
 #pragma unroll
     for (int j = 0; j < A_LOADS; ++j)
       ra[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, live ? avo[j] : kLaneOob, q * DG_BN * 2, 0);
@@ -435,16 +446,16 @@ __global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) 
   };
   auto walk_any = [&](auto any) {
     const int nsub = (tile.rows + 15) >> 4;
-    if constexpr (MS == 8) {
+    if constexpr (MS > 2) {
       switch (nsub) {
         case 1: walk(any, std::integral_constant<int, 1>{}); break;
         case 2: walk(any, std::integral_constant<int, 2>{}); break;
         case 3: walk(any, std::integral_constant<int, 3>{}); break;
         case 4: walk(any, std::integral_constant<int, 4>{}); break;
-        case 5: walk(any, std::integral_constant<int, 5>{}); break;
-        case 6: walk(any, std::integral_constant<int, 6>{}); break;
-        case 7: walk(any, std::integral_constant<int, 7>{}); break;
-        default: walk(any, std::integral_constant<int, 8>{}); break;
+        case 5: walk(any, std::integral_constant<int, MS < 5 ? MS : 5>{}); break;
+        case 6: walk(any, std::integral_constant<int, MS < 6 ? MS : 6>{}); break;
+        case 7: walk(any, std::integral_constant<int, MS < 7 ? MS : 7>{}); break;
+        default: walk(any, std::integral_constant<int, MS>{}); break;
       }
     } else {
       if (nsub == 1) walk(any, std::integral_constant<int, 1>{});
@@ -460,6 +471,21 @@ __global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) 
   }
   if (FMT == 1 && any) walk_any(std::true_type{});
   else walk_any(std::false_type{});
+
+  if constexpr (NS > 1) {
+    // accumulators of groups 1 .. NS - 1, a float4 per lane and register quad
+    f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_all) + (wave * MS * 4) * 64 + lane;
+    if (part > 0) {
+#pragma unroll
+      for (int j = 0; j < MS * 4; ++j) sum[(part - 1) * (PART_BYTES / 16) + j * 64] = acc[j >> 2][(j >> 1) & 1][j & 1];
+    }
+    lds_barrier();
+    if (part > 0) return;
+#pragma unroll
+    for (int q = 0; q < NS - 1; ++q)
+#pragma unroll
+      for (int j = 0; j < MS * 4; ++j) acc[j >> 2][(j >> 1) & 1][j & 1] += sum[q * (PART_BYTES / 16) + j * 64];
+  }
 
   if (kc0 + kc2 >= KC) return;
   const float post = FMT == 1 ? reinterpret_cast<const float*>(p.packed + L.tscale_off)[tile.e] : 1.0f;
@@ -491,14 +517,38 @@ __global__ __launch_bounds__(DG_WAVES * 64, OCC) void dgrad_kernel(DgradArgs p) 
   }
 }
 
-// Row subtiles of a workgroup's tile.
-static int dgrad_subtiles(int32_t E, int32_t M) { return (int64_t)M >= 24 * (int64_t)E ? 8 : 2; }
+// The kernel for E experts and M rows: row subtiles of a tile, workgroups (an
+// upper bound: a band of c rows has at most c / BM + 1 tiles), and groups per
+// workgroup.
+struct DgradPlan {
+  int subtiles, parts;
+  int64_t groups;
+};
 
-// Workgroups: an upper bound on the row tiles (a band of c rows has at most
-// c / BM + 1) times the column groups.
-int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M) {
-  const int64_t tiles = (int64_t)M / (16 * dgrad_subtiles(E, M)) + (E < M ? E : M);
-  return tiles * ((K + DG_BK - 1) / DG_BK);
+static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
+  DgradPlan pl;
+  // by the mean band: 32-row tiles up to 24 rows (w13, 4,096 x 4,096, at 24
+  // rows a band: 439 us against 463 with 64-row tiles), 64-row tiles to 72
+  // (at 48: 563 against 787 with 32 and 642 with 128), then 128 (at 96: 830
+  // against 1,034 with 64)
+  pl.subtiles = (int64_t)M <= 24 * (int64_t)E ? 2 : (int64_t)M < 72 * (int64_t)E ? 4 : 8;
+  pl.groups = ((int64_t)M / (16 * pl.subtiles) + (E < M ? E : M)) * ((K + DG_BK - 1) / DG_BK);
+  pl.parts = 1;
+  if (pl.subtiles == 2) {
+    // four groups of waves run on a CU at a time (three for NVFP4, by LDS)
+    const int64_t slots = DG_CUS * (fmt == 0 ? 4 : 3);
+    const int most = fmt == 0 ? 4 : 3;
+    if (pl.groups * most <= slots) pl.parts = most;
+    else if (pl.groups * 2 <= slots) pl.parts = 2;
+  }
+  return pl;
+}
+
+int64_t dgrad_workgroups(int fmt, int32_t E, int32_t K, int32_t M) { return dgrad_plan(fmt, E, K, M).groups; }
+
+template <int FMT, int MS, int OCC, int NS>
+static void launch_dgrad_t(const DgradArgs& a, int64_t groups, hipStream_t stream) {
+  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0, stream, a);
 }
 
 hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
@@ -515,13 +565,19 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
   a.pre_bf16 = preact_bf16;
   a.dx = dx;
   a.dx_bf16 = dx_bf16;
-  const dim3 grid((unsigned)dgrad_workgroups(E, K, M)), block(DG_WAVES * 64);
-  if (dgrad_subtiles(E, M) == 8) {
-    if (fmt == 0) hipLaunchKernelGGL((dgrad_kernel<0, 8, 2>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((dgrad_kernel<1, 8, 2>), grid, block, 0, stream, a);
+  const DgradPlan pl = dgrad_plan(fmt, E, K, M);
+  if (fmt == 0) {
+    if (pl.subtiles == 8) launch_dgrad_t<0, 8, 2, 1>(a, pl.groups, stream);
+    else if (pl.subtiles == 4) launch_dgrad_t<0, 4, 3, 1>(a, pl.groups, stream);
+    else if (pl.parts == 4) launch_dgrad_t<0, 2, 4, 4>(a, pl.groups, stream);
+    else if (pl.parts == 2) launch_dgrad_t<0, 2, 4, 2>(a, pl.groups, stream);
+    else launch_dgrad_t<0, 2, 4, 1>(a, pl.groups, stream);
   } else {
-    if (fmt == 0) hipLaunchKernelGGL((dgrad_kernel<0, 2, 4>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((dgrad_kernel<1, 2, 3>), grid, block, 0, stream, a);
+    if (pl.subtiles == 8) launch_dgrad_t<1, 8, 2, 1>(a, pl.groups, stream);
+    else if (pl.subtiles == 4) launch_dgrad_t<1, 4, 3, 1>(a, pl.groups, stream);
+    else if (pl.parts == 3) launch_dgrad_t<1, 2, 3, 3>(a, pl.groups, stream);
+    else if (pl.parts == 2) launch_dgrad_t<1, 2, 3, 2>(a, pl.groups, stream);
+    else launch_dgrad_t<1, 2, 3, 1>(a, pl.groups, stream);
   }
   return hipGetLastError();
 }

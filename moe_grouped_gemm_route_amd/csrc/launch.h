@@ -117,6 +117,7 @@ hipError_t launch_silu_mul(const void* y, int y_bf16, int32_t M, int32_t N, cons
 hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
                         const int32_t* group_offsets, int32_t M, const void* preact, int preact_bf16, void* dx,
                         int dx_bf16, hipStream_t stream);
-int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M);
+// Workgroups that launch_dgrad launches for these sizes.
+int64_t dgrad_workgroups(int fmt, int32_t E, int32_t K, int32_t M);
 
 }  // namespace moe
