@@ -34,20 +34,52 @@
 
 namespace moe {
 
-constexpr int DG_BK = 256;                     // output columns per workgroup: two chunks of the pack
 constexpr int DG_BN = 64;                      // n per stage
-constexpr int DG_WAVES = 4;                    // 64 output columns each
-constexpr int DG_C_BYTES = DG_BN * DG_BK / 2;  // eight chunks of 1 KiB
-
 constexpr int DG_CUS = 256;
-constexpr int DG_NT = 2;                       // buffer-load cache policy of the codes: non-temporal
+#ifndef DG_W8
+#define DG_W8 4
+#define DG_DA 2
+#endif
 
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) void* lds_void_t;
+typedef __attribute__((address_space(3))) uint8_t* lds_u8_t;
 typedef __attribute__((address_space(3))) i32x2_t* lds_i32x2_t;
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
+// Raw buffer resource over [base, base + bytes), in scalar registers: loads
+// past the end read zeros.
+__device__ __forceinline__ u32x4_t make_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)base;
+  return u32x4_t{uniform((uint32_t)a), uniform((uint32_t)(a >> 32) & 0xFFFFu), uniform(bytes), 0x00020000u};
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_u8_t)p; }
+
+// 16 bytes per active lane straight to LDS: lane l's at lds + 16 l.  Written
+// as an instruction of its own (it has no result register) so that the
+// compiler, which cannot tell the stages apart, does not make every LDS read
+// wait for every such load; vm_wait does the waiting.  NT: non-temporal, for
+// the codes, which are read once.
+template <bool NT>
+__device__ __forceinline__ void load_lds16(uint32_t lds, u32x4_t rsrc, uint32_t lane_off, uint32_t off) {
+  lds = uniform(lds);
+  off = uniform(off);
+  rsrc = u32x4_t{uniform(rsrc[0]), uniform(rsrc[1]), uniform(rsrc[2]), 0x00020000u};
+  if (NT)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                 :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory");
+}
+
+// At most VM vector loads of this wave are still on their way.
+template <int VM>
+__device__ __forceinline__ void vm_wait() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (15 << 8));
+  asm volatile("" ::: "memory");
 }
 
 // Rows [m0, m0 + rows) of expert e's band, or rows = 0 past the last tile.
@@ -251,7 +283,7 @@ struct DgradArgs {
   Layout L;
   const uint16_t* dy;
   const int32_t* off;
-  int E, NB;            // experts, 256-column groups
+  int E, NB;            // experts, column groups
   const void* pre;      // [M, 2K] gate and up sums, or NULL (no activation)
   int pre_bf16;
   void* dx;
@@ -267,64 +299,74 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// NS groups of four waves share a workgroup; each walks its share of n (in
-// whole stages, the last share padded with empty ones) through LDS of its own,
-// and the first adds up the partial sums in order.
-template <int FMT, int MS, int OCC, int NS>
-__global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
-  // One stage of dy is computed while the next is loaded; codes and scales
-  // run one stage further ahead, so that a stage's first operands are decoded
-  // before the barrier that opens it.
+// W waves take 64 output columns each.  NS groups of W waves share a
+// workgroup; each walks its share of n (in whole stages, the last share padded
+// with empty ones) through LDS of its own, and the first adds up the partial
+// sums in order.
+//
+// Stages.  All operands go straight to LDS.  While stage i is multiplied, dy
+// of stage i + DA and codes and scale words of stage i + 3 are loaded; the
+// operands of stage i + 1 are decoded from its codes, which have landed, and
+// the scale words of stage i + 2 are spread out as f32.
+template <int FMT, int MS, int W, int DA, int OCC, int NS>
+__global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   constexpr int BM = MS * 16;                            // band rows per workgroup
+  constexpr int KCW = W / 2;                             // chunk columns (128 k) per workgroup
   constexpr int A_BYTES = BM * DG_BN * 2;                // dy rows of 128 bytes
-  constexpr int A_LOADS = A_BYTES / 1024 / DG_WAVES;     // 1 KiB loads per wave
+  constexpr int A_LOADS = A_BYTES / 1024 / W;            // 1 KiB loads per wave
+  constexpr int C_BYTES = KCW * DG_BN / 16 * 1024;
   constexpr int H = FMT == 1 ? 2 : 1;                    // scales per 32-block
-  constexpr int S_BYTES = H * DG_BN * (DG_BK / 32) * 4;
-  constexpr int CS_BYTES = DG_C_BYTES + S_BYTES;
-  constexpr int GROUP_BYTES = 2 * A_BYTES + 3 * CS_BYTES;
-  constexpr int PART_BYTES = DG_WAVES * MS * 4 * 64 * 16;   // a group's accumulators
+  constexpr int RECS = FMT == 1 ? W / 4 : 1;             // scale records per 16 n
+  constexpr int R_BYTES = DG_BN / 16 * RECS * 256;       // scale words
+  constexpr int R_WAVE = R_BYTES / W;                    // a wave's share of them
+  constexpr int S_BYTES = H * DG_BN * KCW * 4 * 4;       // the same as f32
+  constexpr int LOADS = A_LOADS + 3;                     // per wave and stage
+  constexpr int GROUP_BYTES = (DA + 1) * A_BYTES + 3 * C_BYTES + 2 * (R_BYTES + S_BYTES);
+  constexpr int PART_BYTES = W * MS * 4 * 64 * 16;       // a group's accumulators
+  static_assert(A_LOADS >= 1 && C_BYTES / 1024 == 2 * W, "whole loads per wave");
   static_assert((NS - 1) * PART_BYTES <= NS * GROUP_BYTES, "the partial sums fit the stages");
   __shared__ __attribute__((aligned(1024))) uint8_t s_all[NS * GROUP_BYTES];
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & (DG_WAVES - 1));
-  const int part = NS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (DG_WAVES * 64)) : 0;
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % W);
+  const int part = NS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (W * 64)) : 0;
   uint8_t* s_dy = s_all + part * GROUP_BYTES;
-  uint8_t* s_cs = s_dy + 2 * A_BYTES;
+  uint8_t* s_codes = s_dy + (DA + 1) * A_BYTES;
+  uint8_t* s_words = s_codes + 3 * C_BYTES;
+  uint8_t* s_scale = s_words + 2 * R_BYTES;
   const int c16 = lane & 15, g = lane >> 4;
   int nb;
   const BandTile tile = find_tile<BM>(p.off, p.E, p.NB, nb);
   if (tile.rows == 0) return;
   const Layout& L = p.L;
   const int N = (int)L.N, K = (int)L.K, KC = (int)L.KC;
-  const int kc0 = nb * 2;                      // first chunk column of the workgroup
-  const int kc2 = wave >> 1;                   // this wave's chunk column
+  const int kc0 = nb * KCW;                    // first chunk column of the workgroup
+  const int kcw = wave >> 1;                   // this wave's chunk column
   const int kb0 = (wave & 1) * 2;              // and first k block in it
 
   // dy rows of the tile: rows past the band do not exist in the range, so
   // they read zeros
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.dy + (int64_t)tile.m0 * N, (uint32_t)tile.rows * N * 2);
+  const u32x4_t ar = make_rsrc(p.dy + (int64_t)tile.m0 * N, (uint32_t)tile.rows * N * 2);
   const int64_t et = (int64_t)tile.e * L.NT;
-  const __amdgpu_buffer_rsrc_t cr = make_rsrc(p.packed + ((et * KC) << 10), (uint32_t)((int64_t)N * K / 2));
-  const __amdgpu_buffer_rsrc_t sr =
-      make_rsrc(p.packed + L.scales_off + et * L.groups * 256, (uint32_t)(L.NT * L.groups * 256));
-  const int rec = FMT == 0 ? kc0 >> 2 : kc0 >> 1;
+  const u32x4_t cr = make_rsrc(p.packed + ((et * KC) << 10), (uint32_t)((int64_t)N * K / 2));
   const int groups = (int)L.groups;
+  const u32x4_t sr = make_rsrc(p.packed + L.scales_off + et * groups * 256, (uint32_t)(L.NT * groups * 256));
 
   // source offsets of this lane's staging loads: 1 KiB (8 rows of 128 bytes)
   // each, lane l landing in row l / 8 at segment l & 7, which holds the row's
   // segment (l & 7) ^ (row / 2 & 7): the 16 rows of a fragment read then fall
   // into 16 different 16-byte bank groups
-  uint32_t avo[A_LOADS], cvo[2];
+  uint32_t avo[A_LOADS];
 #pragma unroll
   for (int j = 0; j < A_LOADS; ++j) {
     const int row = (wave * A_LOADS + j) * 8 + (lane >> 3);
     avo[j] = row < tile.rows ? (uint32_t)row * N * 2 + (((lane & 7) ^ ((row >> 1) & 7)) << 4) : kLaneOob;
   }
-  // chunk column (wave >> 1) of the workgroup, 16-row blocks (wave & 1)*2 + j
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    cvo[j] = kc0 + kc2 < KC ? (uint32_t)((((kb0 + j) * KC + kc0 + kc2) << 10) + lane * 16) : kLaneOob;
+  // the wave's two chunks: its chunk column, 16-row blocks kb0 and kb0 + 1
+  const uint32_t cvo = kc0 + kcw < KC ? (uint32_t)(((kb0 * KC + kc0 + kcw) << 10) + lane * 16) : kLaneOob;
+  // its share of the scale words, a run of R_WAVE bytes of one record
+  const int r_nt = wave * R_WAVE / (RECS * 256), r_in = wave * R_WAVE % (RECS * 256);
+  const uint32_t rvo = (uint32_t)((r_nt * groups + (FMT == 0 ? kc0 >> 2 : kc0 >> 1)) * 256 + r_in + lane * 16);
 
   f32x4_t acc[MS][2][2];
 #pragma unroll
@@ -335,91 +377,93 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   // stages [first, end) of this group; every group runs `steps`
   const int steps = (N / DG_BN + NS - 1) / NS;
   const int first = part * steps, end = min(N / DG_BN, first + steps);
-  // A stage's share of dy, and 2 KiB of codes and 256 bytes of scale words,
-  // per wave: loaded into registers, written to LDS once the stage before is
-  // computed.  Past the last stage the lane offsets lie outside the buffers,
-  // so the loads fetch nothing and return zeros.
-  u32x4_t ra[A_LOADS], rc[2];
-  uint32_t rw;
-  auto load_codes = [&](int i) {
-    const bool live = first + i < end;
-    const uint32_t q = live ? (uint32_t)(first + i) : 0u;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      rc[j] = __builtin_amdgcn_raw_buffer_load_b128(cr, live ? cvo[j] : kLaneOob, (q * (DG_BN / 16) * KC) << 10, DG_NT);
-    rw = __builtin_amdgcn_raw_buffer_load_b32(sr, live ? lane * 4 : kLaneOob,
-                                              ((q * (DG_BN / 16) + wave) * groups + rec) * 256, 0);
-  };
-  auto load_dy = [&](int i) {
+  // Past the last stage the lane offsets lie outside the buffers, so the
+  // loads fetch nothing and write zeros.
+  const uint32_t l_dy = lds_addr(s_dy) + wave * A_LOADS * 1024, l_codes = lds_addr(s_codes) + wave * 2048,
+                 l_words = lds_addr(s_words) + wave * R_WAVE;
+  auto load_dy = [&](int i, uint32_t slot) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) : 0u;
 #pragma unroll
     for (int j = 0; j < A_LOADS; ++j)
-      ra[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, live ? avo[j] : kLaneOob, q * DG_BN * 2, 0);
+      load_lds16<false>(l_dy + slot * A_BYTES + j * 1024, ar, live ? avo[j] : kLaneOob, q * DG_BN * 2);
   };
-  // codes as they lie; the scale word (16-row block `wave`, row c16, k block g
-  // of both chunk columns) as f32, [block][half][n]
-  auto put_codes = [&](uint8_t* st) {
+  auto load_codes = [&](int i, uint32_t slot) {
+    const bool live = first + i < end;
+    const uint32_t q = live ? (uint32_t)(first + i) * (DG_BN / 16) : 0u;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<u32x4_t*>(st + (wave * 2 + j) * 1024 + lane * 16) = rc[j];
-    float* s = reinterpret_cast<float*>(st + DG_C_BYTES) + wave * 16 + c16;
+      load_lds16<true>(l_codes + slot * C_BYTES + j * 1024, cr, live ? cvo : kLaneOob, ((q + j) * KC) << 10);
+    if (lane < R_WAVE / 16)
+      load_lds16<false>(l_words + (i & 1) * R_BYTES, sr, live ? rvo : kLaneOob, q * groups * 256);
+  };
+  // This wave's scale words of stage i as f32, [k block][half][n].
+  auto spread_scales = [&](uint32_t w, int i) {
+    const int d = r_in / 4 % 64 + lane;                  // word of its record: n = d & 15, k block d >> 4
+    float* s = reinterpret_cast<float*>(s_scale + (i & 1) * S_BYTES) + r_nt * 16 + (d & 15);
+    const int kb = d >> 4;
+    if (lane >= R_WAVE / 4) return;
     if (FMT == 0) {
-      s[g * 64] = e8m0_to_f32((rw >> (8 * (kc0 & 3))) & 0xFFu);
-      s[(4 + g) * 64] = e8m0_to_f32((rw >> (8 * (kc0 & 3) + 8)) & 0xFFu);
+#pragma unroll
+      for (int j = 0; j < KCW; ++j) s[(j * 4 + kb) * 64] = e8m0_to_f32((w >> (8 * ((kc0 & 3) + j))) & 0xFFu);
     } else {
-      s[(g * 2) * 64] = e4m3_to_f32<0>(rw);
-      s[(g * 2 + 1) * 64] = e4m3_to_f32<1>(rw);
-      s[((4 + g) * 2) * 64] = e4m3_to_f32<2>(rw);
-      s[((4 + g) * 2 + 1) * 64] = e4m3_to_f32<3>(rw);
+      const int j = r_in / 256 * 2;                      // chunk columns j, j + 1 of the workgroup
+      s[((j * 4 + kb) * 2) * 64] = e4m3_to_f32<0>(w);
+      s[((j * 4 + kb) * 2 + 1) * 64] = e4m3_to_f32<1>(w);
+      s[((j * 4 + 4 + kb) * 2) * 64] = e4m3_to_f32<2>(w);
+      s[((j * 4 + 4 + kb) * 2 + 1) * 64] = e4m3_to_f32<3>(w);
     }
   };
-  auto put_dy = [&](uint8_t* st) {
-#pragma unroll
-    for (int j = 0; j < A_LOADS; ++j)
-      *reinterpret_cast<u32x4_t*>(st + (wave * A_LOADS + j) * 1024 + lane * 16) = ra[j];
+  auto scale_word = [&](int i) {
+    return *reinterpret_cast<const uint32_t*>(s_words + (i & 1) * R_BYTES + wave * R_WAVE + (lane & (R_WAVE / 4 - 1)) * 4);
   };
 
   // Step s (32 n) of a stage: codes and scales of this wave's two k blocks,
   // and the band rows of subtile ms.
-  const uint32_t q_off = (kc2 * 4 + (g >> 1)) * 1024 + kb0 * 256 + (g & 1) * 128 + c16 * 8;
-  const uint32_t s_off = DG_C_BYTES + ((((kc2 * 4 + kb0) * H + (H == 2 ? c16 >> 3 : 0)) * 64 + g * 8) << 2);
+  const uint32_t q_off = (kcw * 4 + (g >> 1)) * 1024 + kb0 * 256 + (g & 1) * 128 + c16 * 8;
+  const uint32_t s_off = (((kcw * 4 + kb0) * H + (H == 2 ? c16 >> 3 : 0)) * 64 + g * 8) << 2;
   const uint32_t a_off = c16 * 128 + ((g ^ ((c16 >> 1) & 7)) << 4);
-  auto raw = [&](const uint8_t* st, int s, RawWeights (&r)[2]) {
+  auto raw = [&](uint32_t slot, int i, int s, RawWeights (&r)[2]) {
+    const uint8_t* st = s_codes + slot * C_BYTES;
+    const uint8_t* sc = s_scale + (i & 1) * S_BYTES;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       r[b].q = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(st + q_off + s * 2048 + b * 256));
-      const f32x4_t* sc = reinterpret_cast<const f32x4_t*>(st + s_off + s * 128 + b * 256 * H);
-      r[b].s[0] = sc[0];
-      r[b].s[1] = sc[1];
+      const f32x4_t* f = reinterpret_cast<const f32x4_t*>(sc + s_off + s * 128 + b * 256 * H);
+      r[b].s[0] = f[0];
+      r[b].s[1] = f[1];
     }
   };
   auto rows = [&](const uint8_t* a, int s, int ms) {
     return *reinterpret_cast<const u32x4_t*>(a + (a_off ^ (s * 64)) + ms * 2048);
   };
+  auto next_slot = [](uint32_t slot, uint32_t n) { return slot + 1 == n ? 0u : slot + 1; };
 
   // The walk of a tile with nsub 16-row subtiles: the operands of a step are
   // decoded among the matrix instructions of the step before.
   auto walk = [&](auto any, auto nsub) {
     constexpr bool any_v = decltype(any)::value;
     constexpr int NSUB = decltype(nsub)::value;
-    uint8_t* c0 = s_cs;
-    uint8_t* c1 = s_cs + CS_BYTES;
-    uint8_t* c2 = s_cs + 2 * CS_BYTES;
-    load_codes(0);
-    load_dy(0);
-    put_codes(c0);
-    load_codes(1);
-    put_dy(s_dy);
-    put_codes(c1);
+    load_codes(0, 0);
+    load_codes(1, 1);
+    load_dy(0, 0);
+    if (DA == 2) load_dy(1, 1);
+    vm_wait<0>();
+    spread_scales(scale_word(0), 0);
+    spread_scales(scale_word(1), 1);
     lds_barrier();
     RawWeights r[2];
     Weights w[2], v[2];
-    raw(c0, 0, r);
+    raw(0, 0, 0, r);
     decode_words<any_v, 0, 8>(r, w);
-    raw(c0, 1, r);
+    raw(0, 0, 1, r);
+    // stage 2's words take stage 0's place, its f32 scales only after every
+    // wave has read stage 0's
+    load_codes(2, 2);
+    lds_barrier();
+    uint32_t sa = 0, sc = 1;                   // LDS slots: dy of stage i, codes of stage i + 1
     for (int i = 0; i < steps; ++i) {
-      const uint8_t* a = s_dy + (i & 1) * A_BYTES;
+      const uint8_t* a = s_dy + sa * A_BYTES;
       u32x4_t x[2];
       auto first_rows = [&](int s) {
         x[0] = rows(a, s, 0);
@@ -427,22 +471,24 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
       };
       first_rows(0);
       __builtin_amdgcn_sched_barrier(0);
-      load_codes(i + 2);
-      load_dy(i + 1);
+      const uint32_t s1 = next_slot(sa, DA + 1), s2 = DA == 2 ? next_slot(s1, DA + 1) : s1;
+      load_dy(i + DA, s2);
+      load_codes(i + 3, next_slot(next_slot(sc, 3), 3));
       __builtin_amdgcn_sched_barrier(0);
       dgrad_step<any_v, NSUB, MS>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 0, ms); },
-                              [&] { first_rows(1); raw(c1, 0, r); }, w, r, v, acc);
+                                  [&] { first_rows(1); raw(sc, i + 1, 0, r); }, w, r, v, acc);
+      vm_wait<LOADS>();                        // all but this step's loads have landed
+      const uint32_t word = scale_word(i + 2);
       dgrad_step<any_v, NSUB, MS>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 1, ms); },
-                              [&] { raw(c1, 1, r); }, v, r, w, acc);
+                                  [&] { raw(sc, i + 1, 1, r); }, v, r, w, acc);
       __builtin_amdgcn_sched_barrier(0);
-      put_dy(s_dy + (~i & 1) * A_BYTES);
-      put_codes(c2);
+      spread_scales(word, i + 2);
+      if (DA == 1) vm_wait<3>();               // dy of the next stage
       lds_barrier();
-      uint8_t* c = c0;
-      c0 = c1;
-      c1 = c2;
-      c2 = c;
+      sa = s1;
+      sc = next_slot(sc, 3);
     }
+    vm_wait<0>();
   };
   auto walk_any = [&](auto any) {
     const int nsub = (tile.rows + 15) >> 4;
@@ -474,6 +520,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
 
   if constexpr (NS > 1) {
     // accumulators of groups 1 .. NS - 1, a float4 per lane and register quad
+    lds_barrier();   // no load is on its way to any group's stages
     f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_all) + (wave * MS * 4) * 64 + lane;
     if (part > 0) {
 #pragma unroll
@@ -487,7 +534,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
       for (int j = 0; j < MS * 4; ++j) acc[j >> 2][(j >> 1) & 1][j & 1] += sum[q * (PART_BYTES / 16) + j * 64];
   }
 
-  if (kc0 + kc2 >= KC) return;
+  if (kc0 + kcw >= KC) return;
   const float post = FMT == 1 ? reinterpret_cast<const float*>(p.packed + L.tscale_off)[tile.e] : 1.0f;
 #pragma unroll
   for (int ms = 0; ms < MS; ++ms) {
@@ -496,7 +543,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
     const int64_t row = tile.m0 + rl;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int col = (kc0 + kc2) * 128 + (kb0 + b) * 32 + g * 8;
+      const int col = (kc0 + kcw) * 128 + (kb0 + b) * 32 + g * 8;
       float v[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -517,11 +564,11 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   }
 }
 
-// The kernel for E experts and M rows: row subtiles of a tile, workgroups (an
-// upper bound: a band of c rows has at most c / BM + 1 tiles), and groups per
-// workgroup.
+// The kernel for E experts and M rows: row subtiles of a tile, 256-column
+// groups, workgroups (an upper bound: a band of c rows has at most c / BM + 1
+// tiles), and groups of waves per workgroup.
 struct DgradPlan {
-  int subtiles, parts;
+  int subtiles, waves, parts;
   int64_t groups;
 };
 
@@ -532,7 +579,9 @@ static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
   // (at 48: 563 against 787 with 32 and 642 with 128), then 128 (at 96: 830
   // against 1,034 with 64)
   pl.subtiles = (int64_t)M <= 24 * (int64_t)E ? 2 : (int64_t)M < 72 * (int64_t)E ? 4 : 8;
-  pl.groups = ((int64_t)M / (16 * pl.subtiles) + (E < M ? E : M)) * ((K + DG_BK - 1) / DG_BK);
+  pl.waves = pl.subtiles == 8 ? DG_W8 : 4;
+  const int cols = 64 * pl.waves;
+  pl.groups = ((int64_t)M / (16 * pl.subtiles) + (E < M ? E : M)) * ((K + cols - 1) / cols);
   pl.parts = 1;
   if (pl.subtiles == 2) {
     // four groups of waves run on a CU at a time (three for NVFP4, by LDS)
@@ -546,9 +595,10 @@ static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
 
 int64_t dgrad_workgroups(int fmt, int32_t E, int32_t K, int32_t M) { return dgrad_plan(fmt, E, K, M).groups; }
 
-template <int FMT, int MS, int OCC, int NS>
-static void launch_dgrad_t(const DgradArgs& a, int64_t groups, hipStream_t stream) {
-  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0, stream, a);
+template <int FMT, int MS, int W, int DA, int OCC, int NS>
+static void launch_dgrad_t(DgradArgs a, int64_t groups, hipStream_t stream) {
+  a.NB = (int)((a.L.K + 64 * W - 1) / (64 * W));
+  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, W, DA, OCC, NS>), dim3((unsigned)groups), dim3(W * 64 * NS), 0, stream, a);
 }
 
 hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
@@ -560,24 +610,23 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
   a.dy = dy;
   a.off = group_offsets;
   a.E = E;
-  a.NB = (K + DG_BK - 1) / DG_BK;
   a.pre = preact;
   a.pre_bf16 = preact_bf16;
   a.dx = dx;
   a.dx_bf16 = dx_bf16;
   const DgradPlan pl = dgrad_plan(fmt, E, K, M);
   if (fmt == 0) {
-    if (pl.subtiles == 8) launch_dgrad_t<0, 8, 2, 1>(a, pl.groups, stream);
-    else if (pl.subtiles == 4) launch_dgrad_t<0, 4, 3, 1>(a, pl.groups, stream);
-    else if (pl.parts == 4) launch_dgrad_t<0, 2, 4, 4>(a, pl.groups, stream);
-    else if (pl.parts == 2) launch_dgrad_t<0, 2, 4, 2>(a, pl.groups, stream);
-    else launch_dgrad_t<0, 2, 4, 1>(a, pl.groups, stream);
+    if (pl.subtiles == 8) launch_dgrad_t<0, 8, DG_W8, DG_DA, 2, 1>(a, pl.groups, stream);
+    else if (pl.subtiles == 4) launch_dgrad_t<0, 4, 4, 1, 3, 1>(a, pl.groups, stream);
+    else if (pl.parts == 4) launch_dgrad_t<0, 2, 4, 1, 4, 4>(a, pl.groups, stream);
+    else if (pl.parts == 2) launch_dgrad_t<0, 2, 4, 1, 4, 2>(a, pl.groups, stream);
+    else launch_dgrad_t<0, 2, 4, 1, 4, 1>(a, pl.groups, stream);
   } else {
-    if (pl.subtiles == 8) launch_dgrad_t<1, 8, 2, 1>(a, pl.groups, stream);
-    else if (pl.subtiles == 4) launch_dgrad_t<1, 4, 3, 1>(a, pl.groups, stream);
-    else if (pl.parts == 3) launch_dgrad_t<1, 2, 3, 3>(a, pl.groups, stream);
-    else if (pl.parts == 2) launch_dgrad_t<1, 2, 3, 2>(a, pl.groups, stream);
-    else launch_dgrad_t<1, 2, 3, 1>(a, pl.groups, stream);
+    if (pl.subtiles == 8) launch_dgrad_t<1, 8, DG_W8, 1, 2, 1>(a, pl.groups, stream);
+    else if (pl.subtiles == 4) launch_dgrad_t<1, 4, 4, 1, 3, 1>(a, pl.groups, stream);
+    else if (pl.parts == 3) launch_dgrad_t<1, 2, 4, 1, 3, 3>(a, pl.groups, stream);
+    else if (pl.parts == 2) launch_dgrad_t<1, 2, 4, 1, 3, 2>(a, pl.groups, stream);
+    else launch_dgrad_t<1, 2, 4, 1, 3, 1>(a, pl.groups, stream);
   }
   return hipGetLastError();
 }
