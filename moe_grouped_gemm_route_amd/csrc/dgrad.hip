@@ -491,21 +491,30 @@ __global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
     vm_wait<0>();
   };
   auto walk_any = [&](auto any) {
+    // (each walk is called from one place, so that it is inlined and the
+    // accumulators stay in registers)
     const int nsub = (tile.rows + 15) >> 4;
-    if constexpr (MS > 2) {
+    if constexpr (MS == 8) {
       switch (nsub) {
         case 1: walk(any, std::integral_constant<int, 1>{}); break;
         case 2: walk(any, std::integral_constant<int, 2>{}); break;
         case 3: walk(any, std::integral_constant<int, 3>{}); break;
         case 4: walk(any, std::integral_constant<int, 4>{}); break;
-        case 5: walk(any, std::integral_constant<int, MS < 5 ? MS : 5>{}); break;
-        case 6: walk(any, std::integral_constant<int, MS < 6 ? MS : 6>{}); break;
-        case 7: walk(any, std::integral_constant<int, MS < 7 ? MS : 7>{}); break;
-        default: walk(any, std::integral_constant<int, MS>{}); break;
+        case 5: walk(any, std::integral_constant<int, 5>{}); break;
+        case 6: walk(any, std::integral_constant<int, 6>{}); break;
+        case 7: walk(any, std::integral_constant<int, 7>{}); break;
+        default: walk(any, std::integral_constant<int, 8>{}); break;
+      }
+    } else if constexpr (MS == 4) {
+      switch (nsub) {
+        case 1: walk(any, std::integral_constant<int, 1>{}); break;
+        case 2: walk(any, std::integral_constant<int, 2>{}); break;
+        case 3: walk(any, std::integral_constant<int, 3>{}); break;
+        default: walk(any, std::integral_constant<int, 4>{}); break;
       }
     } else {
       if (nsub == 1) walk(any, std::integral_constant<int, 1>{});
-      else walk(any, std::integral_constant<int, MS>{});
+      else walk(any, std::integral_constant<int, 2>{});
     }
   };
   bool any = false;
@@ -528,7 +537,7 @@ __global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
     }
     lds_barrier();
     if (part > 0) return;
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < NS - 1; ++q)
 #pragma unroll
       for (int j = 0; j < MS * 4; ++j) acc[j >> 2][(j >> 1) & 1][j & 1] += sum[q * (PART_BYTES / 16) + j * 64];
