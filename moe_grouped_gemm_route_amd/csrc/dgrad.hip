@@ -35,11 +35,9 @@
 namespace moe {
 
 constexpr int DG_BN = 64;                      // n per stage
+constexpr int DG_WAVES = 4;                    // waves per group
+constexpr int DG_KB = 2;                       // k blocks (32 output columns) per wave
 constexpr int DG_CUS = 256;
-#ifndef DG_W8
-#define DG_W8 4
-#define DG_DA 2
-#endif
 
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) uint8_t* lds_u8_t;
@@ -181,9 +179,9 @@ __device__ __forceinline__ void decode_word(const RawWeights& r, Weights& w) {
   }
 }
 
-// Words [LO, HI) of the 2 x 4 words of two k blocks.
+// Words [LO, HI) of the 4 words of each of a wave's k blocks.
 template <bool ANY, int LO, int HI>
-__device__ __forceinline__ void decode_words(const RawWeights (&r)[2], Weights (&w)[2]) {
+__device__ __forceinline__ void decode_words(const RawWeights (&r)[DG_KB], Weights (&w)[DG_KB]) {
   if constexpr (LO < HI) {
     decode_word<ANY, LO % 4>(r[LO / 4], w[LO / 4]);
     decode_words<ANY, LO + 1, HI>(r, w);
@@ -239,43 +237,53 @@ __device__ __forceinline__ void silu_mul_grads(const float (&dh)[8], const float
   }
 }
 
+// N times one matrix instruction and VALU vector instructions behind it.
+template <int N, int VALU>
+__device__ __forceinline__ void interleave() {
+  if constexpr (N > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (VALU > 0) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    interleave<N - 1, VALU>();
+  }
+}
+
 // One 32-n step: the NSUB row subtiles against the operands w, with the next
 // step's operands decoded from r into v on the way.  Each group is a subtile's
-// four matrix instructions, the LDS read of the subtile after next, and a
-// share of the decode, which issues in the shadow of the matrix instructions.
-// The last group has no decode where there are others: it issues the LDS reads
-// that the next step starts with (next).
+// matrix instructions, the LDS read of the subtile after next, and a share of
+// the decode, which issues in the shadow of the matrix instructions.  The last
+// group has no decode where there are others: it issues the LDS reads that the
+// next step starts with (next).
 template <bool ANY, int NSUB, int MAX, int... MS, typename ROWS, typename NEXT>
 __device__ __forceinline__ void dgrad_step(std::integer_sequence<int, MS...>, u32x4_t (&x)[2], ROWS rows, NEXT next,
-                                           const Weights (&w)[2], const RawWeights (&r)[2], Weights (&v)[2],
-                                           f32x4_t (&acc)[MAX][2][2]) {
+                                           const Weights (&w)[DG_KB], const RawWeights (&r)[DG_KB], Weights (&v)[DG_KB],
+                                           f32x4_t (&acc)[MAX][DG_KB][2]) {
   constexpr int DEC = NSUB > 1 ? NSUB - 1 : 1;   // groups that decode
-  auto group = [&](auto mc) {
+  auto group = [&](auto mc) __attribute__((always_inline)) {
     constexpr int ms = decltype(mc)::value;
     const u32x4_t xa = x[ms & 1];
-    acc[ms][0][0] = mfma16(w[0].even, xa, acc[ms][0][0]);
-    acc[ms][0][1] = mfma16(w[0].odd, xa, acc[ms][0][1]);
-    acc[ms][1][0] = mfma16(w[1].even, xa, acc[ms][1][0]);
-    acc[ms][1][1] = mfma16(w[1].odd, xa, acc[ms][1][1]);
+#pragma unroll
+    for (int b = 0; b < DG_KB; ++b) {
+      acc[ms][b][0] = mfma16(w[b].even, xa, acc[ms][b][0]);
+      acc[ms][b][1] = mfma16(w[b].odd, xa, acc[ms][b][1]);
+    }
     if constexpr (ms + 2 < NSUB) x[ms & 1] = rows(ms + 2);
     if constexpr (ms < DEC) {
-      constexpr int LO = 8 * ms / DEC, HI = 8 * (ms + 1) / DEC;
+      constexpr int LO = 4 * DG_KB * ms / DEC, HI = 4 * DG_KB * (ms + 1) / DEC;
       decode_words<ANY, LO, HI>(r, v);
-      constexpr int VALU = (ANY ? 8 : 4) * (HI - LO);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
+      interleave<2 * DG_KB - 1, (ANY ? 8 : 4) * (HI - LO) / (2 * DG_KB)>();
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, VALU / 4, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (ms == NSUB - 1) next();
   };
   (group(std::integral_constant<int, MS>{}), ...);
+}
+
+// f(0), f(1), ... with constants.
+template <int... I, typename F>
+__device__ __forceinline__ void for_each(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
 }
 
 struct DgradArgs {
@@ -299,39 +307,37 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// W waves take 64 output columns each.  NS groups of W waves share a
-// workgroup; each walks its share of n (in whole stages, the last share padded
+// Four waves take 64 output columns each.  NS groups of four waves share a workgroup; each walks its share of n (in whole stages, the last share padded
 // with empty ones) through LDS of its own, and the first adds up the partial
 // sums in order.
 //
 // Stages.  All operands go straight to LDS.  While stage i is multiplied, dy
-// of stage i + DA and codes and scale words of stage i + 3 are loaded; the
+// of stage i + 1 and codes and scale words of stage i + 3 are loaded; the
 // operands of stage i + 1 are decoded from its codes, which have landed, and
 // the scale words of stage i + 2 are spread out as f32.
-template <int FMT, int MS, int W, int DA, int OCC, int NS>
-__global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
+template <int FMT, int MS, int OCC, int NS>
+__global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   constexpr int BM = MS * 16;                            // band rows per workgroup
-  constexpr int KCW = W / 2;                             // chunk columns (128 k) per workgroup
+  constexpr int KB = DG_KB, KCW = DG_KB;                 // chunk columns (128 k) per workgroup
   constexpr int A_BYTES = BM * DG_BN * 2;                // dy rows of 128 bytes
-  constexpr int A_LOADS = A_BYTES / 1024 / W;            // 1 KiB loads per wave
+  constexpr int A_LOADS = A_BYTES / 1024 / DG_WAVES;     // 1 KiB loads per wave
   constexpr int C_BYTES = KCW * DG_BN / 16 * 1024;
   constexpr int H = FMT == 1 ? 2 : 1;                    // scales per 32-block
-  constexpr int RECS = FMT == 1 ? W / 4 : 1;             // scale records per 16 n
+  constexpr int RECS = FMT == 1 ? KCW / 2 : 1;           // scale records per 16 n: a wave's share per stage
   constexpr int R_BYTES = DG_BN / 16 * RECS * 256;       // scale words
-  constexpr int R_WAVE = R_BYTES / W;                    // a wave's share of them
   constexpr int S_BYTES = H * DG_BN * KCW * 4 * 4;       // the same as f32
-  constexpr int LOADS = A_LOADS + 3;                     // per wave and stage
-  constexpr int GROUP_BYTES = (DA + 1) * A_BYTES + 3 * C_BYTES + 2 * (R_BYTES + S_BYTES);
-  constexpr int PART_BYTES = W * MS * 4 * 64 * 16;       // a group's accumulators
-  static_assert(A_LOADS >= 1 && C_BYTES / 1024 == 2 * W, "whole loads per wave");
+  constexpr int LOADS = A_LOADS + KB + 1;                // per wave and stage
+  constexpr int GROUP_BYTES = 2 * A_BYTES + 3 * C_BYTES + 2 * (R_BYTES + S_BYTES);
+  constexpr int PART_BYTES = DG_WAVES * MS * KB * 2 * 64 * 16;   // a group's accumulators
+  static_assert(DG_BN / 16 == DG_WAVES && A_LOADS >= 1, "whole loads per wave");
   static_assert((NS - 1) * PART_BYTES <= NS * GROUP_BYTES, "the partial sums fit the stages");
   __shared__ __attribute__((aligned(1024))) uint8_t s_all[NS * GROUP_BYTES];
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % W);
-  const int part = NS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (W * 64)) : 0;
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % DG_WAVES);
+  const int part = NS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (DG_WAVES * 64)) : 0;
   uint8_t* s_dy = s_all + part * GROUP_BYTES;
-  uint8_t* s_codes = s_dy + (DA + 1) * A_BYTES;
+  uint8_t* s_codes = s_dy + 2 * A_BYTES;
   uint8_t* s_words = s_codes + 3 * C_BYTES;
   uint8_t* s_scale = s_words + 2 * R_BYTES;
   const int c16 = lane & 15, g = lane >> 4;
@@ -341,8 +347,8 @@ __global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   const Layout& L = p.L;
   const int N = (int)L.N, K = (int)L.K, KC = (int)L.KC;
   const int kc0 = nb * KCW;                    // first chunk column of the workgroup
-  const int kcw = wave >> 1;                   // this wave's chunk column
-  const int kb0 = (wave & 1) * 2;              // and first k block in it
+  const int kcw = wave * KB / 4;               // this wave's chunk column
+  const int kb0 = wave * KB % 4;               // and first k block in it
 
   // dy rows of the tile: rows past the band do not exist in the range, so
   // they read zeros
@@ -362,72 +368,78 @@ __global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
     const int row = (wave * A_LOADS + j) * 8 + (lane >> 3);
     avo[j] = row < tile.rows ? (uint32_t)row * N * 2 + (((lane & 7) ^ ((row >> 1) & 7)) << 4) : kLaneOob;
   }
-  // the wave's two chunks: its chunk column, 16-row blocks kb0 and kb0 + 1
+  // the wave's KB code chunks: its chunk column, 16-n blocks kb0, kb0 + 1, ...
   const uint32_t cvo = kc0 + kcw < KC ? (uint32_t)(((kb0 * KC + kc0 + kcw) << 10) + lane * 16) : kLaneOob;
-  // its share of the scale words, a run of R_WAVE bytes of one record
-  const int r_nt = wave * R_WAVE / (RECS * 256), r_in = wave * R_WAVE % (RECS * 256);
-  const uint32_t rvo = (uint32_t)((r_nt * groups + (FMT == 0 ? kc0 >> 2 : kc0 >> 1)) * 256 + r_in + lane * 16);
+  // and its scale words: the records of 16-n block `wave`
+  const uint32_t rvo = (uint32_t)((wave * groups + (FMT == 0 ? kc0 >> 2 : kc0 >> 1)) * 256 + lane * 16);
 
-  f32x4_t acc[MS][2][2];
+  f32x4_t acc[MS][KB][2];
 #pragma unroll
   for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[ms][i >> 1][i & 1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 2 * KB; ++i) acc[ms][i >> 1][i & 1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   // stages [first, end) of this group; every group runs `steps`
   const int steps = (N / DG_BN + NS - 1) / NS;
   const int first = part * steps, end = min(N / DG_BN, first + steps);
   // Past the last stage the lane offsets lie outside the buffers, so the
   // loads fetch nothing and write zeros.
-  const uint32_t l_dy = lds_addr(s_dy) + wave * A_LOADS * 1024, l_codes = lds_addr(s_codes) + wave * 2048,
-                 l_words = lds_addr(s_words) + wave * R_WAVE;
-  auto load_dy = [&](int i, uint32_t slot) {
+  const uint32_t l_dy = lds_addr(s_dy) + wave * A_LOADS * 1024, l_codes = lds_addr(s_codes) + wave * KB * 1024,
+                 l_words = lds_addr(s_words) + wave * RECS * 256;
+  auto load_dy = [&](int i) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) : 0u;
 #pragma unroll
     for (int j = 0; j < A_LOADS; ++j)
-      load_lds16<false>(l_dy + slot * A_BYTES + j * 1024, ar, live ? avo[j] : kLaneOob, q * DG_BN * 2);
+      load_lds16<false>(l_dy + (i & 1) * A_BYTES + j * 1024, ar, live ? avo[j] : kLaneOob, q * DG_BN * 2);
   };
   auto load_codes = [&](int i, uint32_t slot) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) * (DG_BN / 16) : 0u;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < KB; ++j)
       load_lds16<true>(l_codes + slot * C_BYTES + j * 1024, cr, live ? cvo : kLaneOob, ((q + j) * KC) << 10);
-    if (lane < R_WAVE / 16)
+    if (lane < RECS * 16)
       load_lds16<false>(l_words + (i & 1) * R_BYTES, sr, live ? rvo : kLaneOob, q * groups * 256);
   };
-  // This wave's scale words of stage i as f32, [k block][half][n].
-  auto spread_scales = [&](uint32_t w, int i) {
-    const int d = r_in / 4 % 64 + lane;                  // word of its record: n = d & 15, k block d >> 4
-    float* s = reinterpret_cast<float*>(s_scale + (i & 1) * S_BYTES) + r_nt * 16 + (d & 15);
-    const int kb = d >> 4;
-    if (lane >= R_WAVE / 4) return;
+  // This wave's scale words of stage i (n = c16 of 16-n block `wave`, k block
+  // g), from LDS and back to it as f32, [k block][half][n].
+  struct ScaleWords {
+    uint32_t w[RECS];
+  };
+  auto scale_words = [&](int i) {
+    ScaleWords r;
+#pragma unroll
+    for (int u = 0; u < RECS; ++u)
+      r.w[u] = *reinterpret_cast<const uint32_t*>(s_words + (i & 1) * R_BYTES + (wave * RECS + u) * 256 + lane * 4);
+    return r;
+  };
+  auto spread_scales = [&](const ScaleWords& r, int i) {
+    float* s = reinterpret_cast<float*>(s_scale + (i & 1) * S_BYTES) + wave * 16 + c16;
     if (FMT == 0) {
 #pragma unroll
-      for (int j = 0; j < KCW; ++j) s[(j * 4 + kb) * 64] = e8m0_to_f32((w >> (8 * ((kc0 & 3) + j))) & 0xFFu);
+      for (int j = 0; j < KCW; ++j) s[(j * 4 + g) * 64] = e8m0_to_f32((r.w[0] >> (8 * ((kc0 & 3) + j))) & 0xFFu);
     } else {
-      const int j = r_in / 256 * 2;                      // chunk columns j, j + 1 of the workgroup
-      s[((j * 4 + kb) * 2) * 64] = e4m3_to_f32<0>(w);
-      s[((j * 4 + kb) * 2 + 1) * 64] = e4m3_to_f32<1>(w);
-      s[((j * 4 + 4 + kb) * 2) * 64] = e4m3_to_f32<2>(w);
-      s[((j * 4 + 4 + kb) * 2 + 1) * 64] = e4m3_to_f32<3>(w);
+#pragma unroll
+      for (int u = 0; u < RECS; ++u) {
+        s[((u * 8 + g) * 2) * 64] = e4m3_to_f32<0>(r.w[u]);
+        s[((u * 8 + g) * 2 + 1) * 64] = e4m3_to_f32<1>(r.w[u]);
+        s[((u * 8 + 4 + g) * 2) * 64] = e4m3_to_f32<2>(r.w[u]);
+        s[((u * 8 + 4 + g) * 2 + 1) * 64] = e4m3_to_f32<3>(r.w[u]);
+      }
     }
   };
-  auto scale_word = [&](int i) {
-    return *reinterpret_cast<const uint32_t*>(s_words + (i & 1) * R_BYTES + wave * R_WAVE + (lane & (R_WAVE / 4 - 1)) * 4);
-  };
 
-  // Step s (32 n) of a stage: codes and scales of this wave's two k blocks,
+  // Step s (32 n) of a stage: codes and scales of this wave's k blocks,
   // and the band rows of subtile ms.
   const uint32_t q_off = (kcw * 4 + (g >> 1)) * 1024 + kb0 * 256 + (g & 1) * 128 + c16 * 8;
   const uint32_t s_off = (((kcw * 4 + kb0) * H + (H == 2 ? c16 >> 3 : 0)) * 64 + g * 8) << 2;
   const uint32_t a_off = c16 * 128 + ((g ^ ((c16 >> 1) & 7)) << 4);
-  auto raw = [&](uint32_t slot, int i, int s, RawWeights (&r)[2]) {
+  auto raw = [&](uint32_t slot, int i, int s, RawWeights (&r)[KB]) {
     const uint8_t* st = s_codes + slot * C_BYTES;
     const uint8_t* sc = s_scale + (i & 1) * S_BYTES;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < KB; ++b) {
       r[b].q = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(st + q_off + s * 2048 + b * 256));
       const f32x4_t* f = reinterpret_cast<const f32x4_t*>(sc + s_off + s * 128 + b * 256 * H);
       r[b].s[0] = f[0];
@@ -437,33 +449,33 @@ __global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   auto rows = [&](const uint8_t* a, int s, int ms) {
     return *reinterpret_cast<const u32x4_t*>(a + (a_off ^ (s * 64)) + ms * 2048);
   };
-  auto next_slot = [](uint32_t slot, uint32_t n) { return slot + 1 == n ? 0u : slot + 1; };
+  auto next_slot = [](uint32_t slot) { return slot == 2 ? 0u : slot + 1; };
 
   // The walk of a tile with nsub 16-row subtiles: the operands of a step are
-  // decoded among the matrix instructions of the step before.
-  auto walk = [&](auto any, auto nsub) {
+  // decoded among the matrix instructions of the step before.  (Inlined, so
+  // that the accumulators stay in registers.)
+  auto walk = [&](auto any, auto nsub) __attribute__((always_inline)) {
     constexpr bool any_v = decltype(any)::value;
     constexpr int NSUB = decltype(nsub)::value;
     load_codes(0, 0);
     load_codes(1, 1);
-    load_dy(0, 0);
-    if (DA == 2) load_dy(1, 1);
+    load_dy(0);
     vm_wait<0>();
-    spread_scales(scale_word(0), 0);
-    spread_scales(scale_word(1), 1);
+    spread_scales(scale_words(0), 0);
+    spread_scales(scale_words(1), 1);
     lds_barrier();
-    RawWeights r[2];
-    Weights w[2], v[2];
+    RawWeights r[KB];
+    Weights w[KB], v[KB];
     raw(0, 0, 0, r);
-    decode_words<any_v, 0, 8>(r, w);
+    decode_words<any_v, 0, 4 * KB>(r, w);
     raw(0, 0, 1, r);
     // stage 2's words take stage 0's place, its f32 scales only after every
     // wave has read stage 0's
     load_codes(2, 2);
     lds_barrier();
-    uint32_t sa = 0, sc = 1;                   // LDS slots: dy of stage i, codes of stage i + 1
+    uint32_t sc = 1;                           // codes' LDS slot of stage i + 1
     for (int i = 0; i < steps; ++i) {
-      const uint8_t* a = s_dy + sa * A_BYTES;
+      const uint8_t* a = s_dy + (i & 1) * A_BYTES;
       u32x4_t x[2];
       auto first_rows = [&](int s) {
         x[0] = rows(a, s, 0);
@@ -471,28 +483,24 @@ __global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
       };
       first_rows(0);
       __builtin_amdgcn_sched_barrier(0);
-      const uint32_t s1 = next_slot(sa, DA + 1), s2 = DA == 2 ? next_slot(s1, DA + 1) : s1;
-      load_dy(i + DA, s2);
-      load_codes(i + 3, next_slot(next_slot(sc, 3), 3));
+      load_dy(i + 1);
+      load_codes(i + 3, next_slot(next_slot(sc)));
       __builtin_amdgcn_sched_barrier(0);
       dgrad_step<any_v, NSUB, MS>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 0, ms); },
                                   [&] { first_rows(1); raw(sc, i + 1, 0, r); }, w, r, v, acc);
-      vm_wait<LOADS>();                        // all but this step's loads have landed
-      const uint32_t word = scale_word(i + 2);
+      vm_wait<LOADS>();                        // all but this stage's loads have landed
+      const ScaleWords words = scale_words(i + 2);
       dgrad_step<any_v, NSUB, MS>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 1, ms); },
                                   [&] { raw(sc, i + 1, 1, r); }, v, r, w, acc);
       __builtin_amdgcn_sched_barrier(0);
-      spread_scales(word, i + 2);
-      if (DA == 1) vm_wait<3>();               // dy of the next stage
+      spread_scales(words, i + 2);
+      vm_wait<KB + 1>();                       // dy of the next stage has landed
       lds_barrier();
-      sa = s1;
-      sc = next_slot(sc, 3);
+      sc = next_slot(sc);
     }
     vm_wait<0>();
   };
-  auto walk_any = [&](auto any) {
-    // (each walk is called from one place, so that it is inlined and the
-    // accumulators stay in registers)
+  auto walk_any = [&](auto any) __attribute__((always_inline)) {
     const int nsub = (tile.rows + 15) >> 4;
     if constexpr (MS == 8) {
       switch (nsub) {
@@ -530,54 +538,60 @@ __global__ __launch_bounds__(W * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   if constexpr (NS > 1) {
     // accumulators of groups 1 .. NS - 1, a float4 per lane and register quad
     lds_barrier();   // no load is on its way to any group's stages
-    f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_all) + (wave * MS * 4) * 64 + lane;
+    f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_all) + (wave * MS * KB * 2) * 64 + lane;
     if (part > 0) {
 #pragma unroll
-      for (int j = 0; j < MS * 4; ++j) sum[(part - 1) * (PART_BYTES / 16) + j * 64] = acc[j >> 2][(j >> 1) & 1][j & 1];
+      for (int j = 0; j < MS * KB * 2; ++j)
+        sum[(part - 1) * (PART_BYTES / 16) + j * 64] = acc[j / (2 * KB)][j / 2 % KB][j & 1];
     }
     lds_barrier();
     if (part > 0) return;
 #pragma unroll 1
     for (int q = 0; q < NS - 1; ++q)
 #pragma unroll
-      for (int j = 0; j < MS * 4; ++j) acc[j >> 2][(j >> 1) & 1][j & 1] += sum[q * (PART_BYTES / 16) + j * 64];
+      for (int j = 0; j < MS * KB * 2; ++j)
+        acc[j / (2 * KB)][j / 2 % KB][j & 1] += sum[q * (PART_BYTES / 16) + j * 64];
   }
 
   if (kc0 + kcw >= KC) return;
   const float post = FMT == 1 ? reinterpret_cast<const float*>(p.packed + L.tscale_off)[tile.e] : 1.0f;
-#pragma unroll
-  for (int ms = 0; ms < MS; ++ms) {
+  // eight columns of one row: subtile ms, k block b (a fold over constants,
+  // so that the accumulators are never indexed at run time)
+  auto store = [&](auto mc, auto bc) __attribute__((always_inline)) {
+    constexpr int ms = decltype(mc)::value, b = decltype(bc)::value;
     const int rl = ms * 16 + c16;
-    if (rl >= tile.rows) continue;
+    if (rl >= tile.rows) return;
     const int64_t row = tile.m0 + rl;
+    const int col = (kc0 + kcw) * 128 + (kb0 + b) * 32 + g * 8;
+    float v[8];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int col = (kc0 + kcw) * 128 + (kb0 + b) * 32 + g * 8;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = acc[ms][b][0][i] * post;
-        v[2 * i + 1] = acc[ms][b][1][i] * post;
-      }
-      if (p.pre) {
-        float gate[8], up[8], dg[8], du[8];
-        load8(p.pre, p.pre_bf16, row * 2 * K + col, gate);
-        load8(p.pre, p.pre_bf16, row * 2 * K + K + col, up);
-        silu_mul_grads(v, gate, up, dg, du);
-        store8(p.dx, p.dx_bf16, row * 2 * K + col, dg);
-        store8(p.dx, p.dx_bf16, row * 2 * K + K + col, du);
-      } else {
-        store8(p.dx, p.dx_bf16, row * K + col, v);
-      }
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = acc[ms][b][0][i] * post;
+      v[2 * i + 1] = acc[ms][b][1][i] * post;
     }
-  }
+    if (p.pre) {
+      float gate[8], up[8], dg[8], du[8];
+      load8(p.pre, p.pre_bf16, row * 2 * K + col, gate);
+      load8(p.pre, p.pre_bf16, row * 2 * K + K + col, up);
+      silu_mul_grads(v, gate, up, dg, du);
+      store8(p.dx, p.dx_bf16, row * 2 * K + col, dg);
+      store8(p.dx, p.dx_bf16, row * 2 * K + K + col, du);
+    } else {
+      store8(p.dx, p.dx_bf16, row * K + col, v);
+    }
+  };
+  for_each(std::make_integer_sequence<int, MS * KB>{}, [&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+    store(std::integral_constant<int, i / KB>{}, std::integral_constant<int, i % KB>{});
+    __builtin_amdgcn_sched_barrier(0);
+  });
 }
 
-// The kernel for E experts and M rows: row subtiles of a tile, 256-column
-// groups, workgroups (an upper bound: a band of c rows has at most c / BM + 1
-// tiles), and groups of waves per workgroup.
+// The kernel for E experts and M rows: row subtiles of a tile, workgroups (an
+// upper bound: a band of c rows has at most c / BM + 1 tiles), and groups of
+// waves per workgroup.
 struct DgradPlan {
-  int subtiles, waves, parts;
+  int subtiles, parts;
   int64_t groups;
 };
 
@@ -588,8 +602,7 @@ static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
   // (at 48: 563 against 787 with 32 and 642 with 128), then 128 (at 96: 830
   // against 1,034 with 64)
   pl.subtiles = (int64_t)M <= 24 * (int64_t)E ? 2 : (int64_t)M < 72 * (int64_t)E ? 4 : 8;
-  pl.waves = pl.subtiles == 8 ? DG_W8 : 4;
-  const int cols = 64 * pl.waves;
+  const int cols = 128 * DG_KB;
   pl.groups = ((int64_t)M / (16 * pl.subtiles) + (E < M ? E : M)) * ((K + cols - 1) / cols);
   pl.parts = 1;
   if (pl.subtiles == 2) {
@@ -604,10 +617,9 @@ static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
 
 int64_t dgrad_workgroups(int fmt, int32_t E, int32_t K, int32_t M) { return dgrad_plan(fmt, E, K, M).groups; }
 
-template <int FMT, int MS, int W, int DA, int OCC, int NS>
-static void launch_dgrad_t(DgradArgs a, int64_t groups, hipStream_t stream) {
-  a.NB = (int)((a.L.K + 64 * W - 1) / (64 * W));
-  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, W, DA, OCC, NS>), dim3((unsigned)groups), dim3(W * 64 * NS), 0, stream, a);
+template <int FMT, int MS, int OCC, int NS>
+static void launch_dgrad_t(const DgradArgs& a, int64_t groups, hipStream_t stream) {
+  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0, stream, a);
 }
 
 hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
@@ -619,23 +631,24 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
   a.dy = dy;
   a.off = group_offsets;
   a.E = E;
+  a.NB = (K + 128 * DG_KB - 1) / (128 * DG_KB);
   a.pre = preact;
   a.pre_bf16 = preact_bf16;
   a.dx = dx;
   a.dx_bf16 = dx_bf16;
   const DgradPlan pl = dgrad_plan(fmt, E, K, M);
   if (fmt == 0) {
-    if (pl.subtiles == 8) launch_dgrad_t<0, 8, DG_W8, DG_DA, 2, 1>(a, pl.groups, stream);
-    else if (pl.subtiles == 4) launch_dgrad_t<0, 4, 4, 1, 3, 1>(a, pl.groups, stream);
-    else if (pl.parts == 4) launch_dgrad_t<0, 2, 4, 1, 4, 4>(a, pl.groups, stream);
-    else if (pl.parts == 2) launch_dgrad_t<0, 2, 4, 1, 4, 2>(a, pl.groups, stream);
-    else launch_dgrad_t<0, 2, 4, 1, 4, 1>(a, pl.groups, stream);
+    if (pl.subtiles == 8) launch_dgrad_t<0, 8, 2, 1>(a, pl.groups, stream);
+    else if (pl.subtiles == 4) launch_dgrad_t<0, 4, 3, 1>(a, pl.groups, stream);
+    else if (pl.parts == 4) launch_dgrad_t<0, 2, 4, 4>(a, pl.groups, stream);
+    else if (pl.parts == 2) launch_dgrad_t<0, 2, 4, 2>(a, pl.groups, stream);
+    else launch_dgrad_t<0, 2, 4, 1>(a, pl.groups, stream);
   } else {
-    if (pl.subtiles == 8) launch_dgrad_t<1, 8, DG_W8, 1, 2, 1>(a, pl.groups, stream);
-    else if (pl.subtiles == 4) launch_dgrad_t<1, 4, 4, 1, 3, 1>(a, pl.groups, stream);
-    else if (pl.parts == 3) launch_dgrad_t<1, 2, 4, 1, 3, 3>(a, pl.groups, stream);
-    else if (pl.parts == 2) launch_dgrad_t<1, 2, 4, 1, 3, 2>(a, pl.groups, stream);
-    else launch_dgrad_t<1, 2, 4, 1, 3, 1>(a, pl.groups, stream);
+    if (pl.subtiles == 8) launch_dgrad_t<1, 8, 2, 1>(a, pl.groups, stream);
+    else if (pl.subtiles == 4) launch_dgrad_t<1, 4, 3, 1>(a, pl.groups, stream);
+    else if (pl.parts == 3) launch_dgrad_t<1, 2, 3, 3>(a, pl.groups, stream);
+    else if (pl.parts == 2) launch_dgrad_t<1, 2, 3, 2>(a, pl.groups, stream);
+    else launch_dgrad_t<1, 2, 3, 1>(a, pl.groups, stream);
   }
   return hipGetLastError();
 }
