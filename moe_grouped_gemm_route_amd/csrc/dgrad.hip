@@ -85,57 +85,106 @@ struct BandTile {
   int e, m0, rows;
 };
 
-// Tile t of the list "for each expert, its band cut into ceil(rows / BM) even
-// tiles", found
-// by the whole wave from the band offsets: lane l covers experts
-// [l per, l per + per), whose offsets it loads in one batch; a wave prefix sum
-// of the lanes' tile counts picks the lane, which then finds its expert.
-// (E <= 1024, so per <= 16.)
-// The workgroup's tile and its column group nb of NB.  Workgroup ids are dealt
-// round-robin to the 8 XCDs; they are remapped so that each XCD takes a
-// contiguous run of the (tile, column group) list: the column groups of a
-// tile then read its dy rows from one L2.
+// An expert's band of c rows: n even tiles, n - 1 of `share` rows (whole 16-row
+// subtiles) and a last one of the rows left.
+struct BandCut {
+  int c, n, share;
+};
 template <int BM>
+__device__ __forceinline__ BandCut cut_band(int c) {
+  const int n = (c + BM - 1) / BM;
+  return {c, n, n > 0 ? ((c + n - 1) / n + 15) & ~15 : 16};
+}
+// Its tiles of s subtiles.
+__device__ __forceinline__ int tiles_of(const BandCut& b, int s) {
+  return b.n == 0 ? 0 : (b.share == 16 * s ? b.n - 1 : 0) + ((b.c - (b.n - 1) * b.share + 15) >> 4 == s ? 1 : 0);
+}
+
+// The workgroup's tile and its column group nb of NB, found by the whole wave
+// from the band offsets: lane l covers experts [l per, l per + per) (E <= 1024,
+// so per <= 16), whose offsets it loads in one batch.
+//
+// Order.  Workgroup ids are dealt round-robin to the 8 XCDs.  Tiles are dealt
+// to the XCDs in turn, each with all its column groups in a row, so that these
+// read its dy rows from one L2; the groups of the last (tiles mod 8) tiles are
+// spread over all XCDs.  SORTED: tiles run from the largest to the smallest
+// (by subtiles), which fills the last round of workgroups best: w13 at 4,096
+// tokens and w2 (half as many groups) gain what the comment at the kernel says.
+template <int BM, bool SORTED>
 __device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, int E, int NB, int& nb) {
-  constexpr int PER = 16;
+  constexpr int PER = 16, CLASSES = SORTED ? BM / 16 : 1;
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) >> 6;
   const int e0 = lane * per;
   int o[PER + 1];
 #pragma unroll
-  for (int i = 0; i <= PER; ++i) o[i] = (i <= per && e0 + i <= E) ? off[e0 + i] : 0;
-  int mine = 0;
+  for (int i = 0; i <= PER; ++i) o[i] = i <= per ? off[min(e0 + i, E)] : 0;
+  // this lane's tiles by subtiles (SORTED) or all of them
+  int mine[CLASSES] = {};
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (i < per && e0 + i < E) mine += (o[i + 1] - o[i] + BM - 1) / BM;
-  int incl = mine;
+    if (i < per) {
+      const BandCut b = cut_band<BM>(o[i + 1] - o[i]);
+      if constexpr (SORTED) {
+#pragma unroll
+        for (int s = 0; s < CLASSES; ++s) mine[s] += tiles_of(b, s + 1);
+      } else {
+        mine[0] += b.n;
+      }
+    }
+  int total[CLASSES], tiles = 0;
+#pragma unroll
+  for (int s = 0; s < CLASSES; ++s) {
+    total[s] = wave_sum(mine[s]);
+    tiles += total[s];
+  }
+  const int x = blockIdx.x & 7, k = blockIdx.x >> 3;
+  const int whole = (tiles >> 3) * NB;
+  int t;
+  if (k < whole) {
+    t = (k / NB) * 8 + x;
+    nb = k % NB;
+  } else {
+    const int r = (k - whole) * 8 + x;
+    t = (tiles & ~7) + r / NB;
+    nb = r % NB;
+  }
+  BandTile b = {0, 0, 0};
+  if (t >= tiles) return b;
+  // the class that holds tile t, and t's place in it
+  int cls = 0, own = mine[0];
+  if constexpr (SORTED) {
+    bool found = false;
+#pragma unroll
+    for (int s = CLASSES - 1; s >= 0; --s) {
+      if (!found && t < total[s]) {
+        found = true;
+        cls = s;
+        own = mine[s];
+      }
+      if (!found) t -= total[s];
+    }
+  }
+  int incl = own;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int v = __shfl_up(incl, d, 64);
     if (lane >= d) incl += v;
   }
-  const int items = __builtin_amdgcn_readlane(incl, 63) * NB;
-  const int bx = blockIdx.x, x = bx & 7;
-  const int item = x * (items >> 3) + min(x, items & 7) + (bx >> 3);
-  const int t = bx < items ? item / NB : -1;
-  nb = item - t * NB;
-  int left = t - (incl - mine);   // tile t's place among this lane's tiles
-  const uint64_t hit = __ballot(t >= 0 && left >= 0 && left < mine);
-  BandTile b = {0, 0, 0};
-  if (hit == 0) return b;
-  const int src = __ffsll((unsigned long long)hit) - 1;
+  int left = t - (incl - own);    // tile t's place among this lane's tiles
+  const int src = __ffsll((unsigned long long)__ballot(left >= 0 && left < own)) - 1;
   bool found = false;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (i < per && e0 + i < E && !found) {
-      const int c = o[i + 1] - o[i];
-      const int n = (c + BM - 1) / BM;
+    if (i < per && !found) {
+      const BandCut cut = cut_band<BM>(o[i + 1] - o[i]);
+      const int n = SORTED ? tiles_of(cut, cls + 1) : cut.n;
       if (left < n) {
-        // an even share of the band, in whole 16-row subtiles
-        const int share = ((c + n - 1) / n + 15) & ~15;
+        // among tiles of one class, the last one comes last
+        const int j = SORTED && cut.share != 16 * (cls + 1) ? cut.n - 1 : left;
         b.e = e0 + i;
-        b.m0 = o[i] + left * share;
-        b.rows = min(share, c - left * share);
+        b.m0 = o[i] + j * cut.share;
+        b.rows = min(cut.share, cut.c - j * cut.share);
         found = true;
       }
       left -= n;
@@ -208,21 +257,26 @@ __device__ __forceinline__ void store8(void* p, bool bf16, int64_t i, const floa
   }
 }
 
-__device__ __forceinline__ void load8(const void* p, bool bf16, int64_t i, float (&v)[8]) {
-  if (bf16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight values as they lie in memory (PRE 1: bf16, 2: f32), and as f32.
+template <int PRE>
+struct Raw8 {
+  u32x4_t w[PRE];
+};
+
+template <int PRE>
+__device__ __forceinline__ Raw8<PRE> load_raw8(const void* p, int64_t i) {
+  Raw8<PRE> r;
+  const u32x4_t* q = reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint8_t*>(p) + i * (2 * PRE));
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      v[2 * c] = bf16_lo(w[c]);
-      v[2 * c + 1] = bf16_hi(w[c]);
-    }
-  } else {
-    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
+  for (int c = 0; c < PRE; ++c) r.w[c] = q[c];
+  return r;
+}
+
+template <int PRE>
+__device__ __forceinline__ void unpack8(const Raw8<PRE>& r, float (&v)[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    v[c] = PRE == 2 ? __uint_as_float(r.w[(c >> 2) * (PRE - 1)][c & 3]) : c & 1 ? bf16_hi(r.w[0][c >> 1]) : bf16_lo(r.w[0][c >> 1]);
 }
 
 // Gradients of h = silu(g) u for eight columns: dg = dh u s (1 + g (1 - s)),
@@ -342,7 +396,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   uint8_t* s_scale = s_words + 2 * R_BYTES;
   const int c16 = lane & 15, g = lane >> 4;
   int nb;
-  const BandTile tile = find_tile<BM>(p.off, p.E, p.NB, nb);
+  const BandTile tile = find_tile<BM, (MS > 2)>(p.off, p.E, p.NB, nb);
   if (tile.rows == 0) return;
   const Layout& L = p.L;
   const int N = (int)L.N, K = (int)L.K, KC = (int)L.KC;
@@ -555,36 +609,68 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
 
   if (kc0 + kcw >= KC) return;
   const float post = FMT == 1 ? reinterpret_cast<const float*>(p.packed + L.tscale_off)[tile.e] : 1.0f;
-  // eight columns of one row: subtile ms, k block b (a fold over constants,
-  // so that the accumulators are never indexed at run time)
-  auto store = [&](auto mc, auto bc) __attribute__((always_inline)) {
-    constexpr int ms = decltype(mc)::value, b = decltype(bc)::value;
-    const int rl = ms * 16 + c16;
-    if (rl >= tile.rows) return;
-    const int64_t row = tile.m0 + rl;
-    const int col = (kc0 + kcw) * 128 + (kb0 + b) * 32 + g * 8;
-    float v[8];
+  // Unit u = ms * KB + b: eight columns (k block b) of this lane's row of
+  // subtile ms.  Constants all the way, so that the accumulators are never
+  // indexed at run time.
+  const int64_t col0 = (int64_t)(kc0 + kcw) * 128 + kb0 * 32 + g * 8;
+  auto sums = [&](auto uc, float (&v)[8]) __attribute__((always_inline)) {
+    constexpr int u = decltype(uc)::value;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = acc[ms][b][0][i] * post;
-      v[2 * i + 1] = acc[ms][b][1][i] * post;
-    }
-    if (p.pre) {
-      float gate[8], up[8], dg[8], du[8];
-      load8(p.pre, p.pre_bf16, row * 2 * K + col, gate);
-      load8(p.pre, p.pre_bf16, row * 2 * K + K + col, up);
-      silu_mul_grads(v, gate, up, dg, du);
-      store8(p.dx, p.dx_bf16, row * 2 * K + col, dg);
-      store8(p.dx, p.dx_bf16, row * 2 * K + K + col, du);
-    } else {
-      store8(p.dx, p.dx_bf16, row * K + col, v);
+      v[2 * i] = acc[u / KB][u % KB][0][i] * post;
+      v[2 * i + 1] = acc[u / KB][u % KB][1][i] * post;
     }
   };
-  for_each(std::make_integer_sequence<int, MS * KB>{}, [&](auto ic) __attribute__((always_inline)) {
-    constexpr int i = decltype(ic)::value;
-    store(std::integral_constant<int, i / KB>{}, std::integral_constant<int, i % KB>{});
-    __builtin_amdgcn_sched_barrier(0);
-  });
+  if (!p.pre) {
+    for_each(std::make_integer_sequence<int, MS * KB>{}, [&](auto uc) __attribute__((always_inline)) {
+      constexpr int u = decltype(uc)::value;
+      const int rl = u / KB * 16 + c16;
+      float v[8];
+      sums(uc, v);
+      if (rl < tile.rows) store8(p.dx, p.dx_bf16, (int64_t)(tile.m0 + rl) * K + col0 + u % KB * 32, v);
+    });
+    return;
+  }
+  // Through the activation: the gate and up values of G units are loaded while
+  // the G before them are computed (rows past the tile read its last row).
+  auto activation = [&](auto prec) __attribute__((always_inline)) {
+    constexpr int PRE = decltype(prec)::value;
+    constexpr int G = PRE == 1 ? 4 : 2;
+    constexpr int GROUPS = MS * KB / G;
+    Raw8<PRE> gate[2][G], up[2][G];
+    auto load_group = [&](auto jc) __attribute__((always_inline)) {
+      constexpr int j = decltype(jc)::value;
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int u = j * G + i;
+        const int64_t at = (int64_t)(tile.m0 + min(u / KB * 16 + c16, tile.rows - 1)) * 2 * K + col0 + u % KB * 32;
+        gate[j & 1][i] = load_raw8<PRE>(p.pre, at);
+        up[j & 1][i] = load_raw8<PRE>(p.pre, at + K);
+      }
+    };
+    load_group(std::integral_constant<int, 0>{});
+    for_each(std::make_integer_sequence<int, GROUPS>{}, [&](auto jc) __attribute__((always_inline)) {
+      constexpr int j = decltype(jc)::value;
+      if constexpr (j + 1 < GROUPS) load_group(std::integral_constant<int, j + 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+      for_each(std::make_integer_sequence<int, G>{}, [&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value, u = j * G + i;
+        const int rl = u / KB * 16 + c16;
+        float v[8], gt[8], ut[8], dg[8], du[8];
+        sums(std::integral_constant<int, u>{}, v);
+        unpack8<PRE>(gate[j & 1][i], gt);
+        unpack8<PRE>(up[j & 1][i], ut);
+        silu_mul_grads(v, gt, ut, dg, du);
+        if (rl < tile.rows) {
+          const int64_t at = (int64_t)(tile.m0 + rl) * 2 * K + col0 + u % KB * 32;
+          store8(p.dx, p.dx_bf16, at, dg);
+          store8(p.dx, p.dx_bf16, at + K, du);
+        }
+      });
+    });
+  };
+  if (p.pre_bf16) activation(std::integral_constant<int, 1>{});
+  else activation(std::integral_constant<int, 2>{});
 }
 
 // The kernel for E experts and M rows: row subtiles of a tile, workgroups (an
