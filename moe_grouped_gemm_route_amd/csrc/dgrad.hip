@@ -85,59 +85,38 @@ struct BandTile {
   int e, m0, rows;
 };
 
-// An expert's band of c rows: n even tiles, n - 1 of `share` rows (whole 16-row
-// subtiles) and a last one of the rows left.
-struct BandCut {
-  int c, n, share;
-};
-template <int BM>
-__device__ __forceinline__ BandCut cut_band(int c) {
-  const int n = (c + BM - 1) / BM;
-  return {c, n, n > 0 ? ((c + n - 1) / n + 15) & ~15 : 16};
-}
-// Its tiles of s subtiles.
-__device__ __forceinline__ int tiles_of(const BandCut& b, int s) {
-  return b.n == 0 ? 0 : (b.share == 16 * s ? b.n - 1 : 0) + ((b.c - (b.n - 1) * b.share + 15) >> 4 == s ? 1 : 0);
-}
-
 // The workgroup's tile and its column group nb of NB, found by the whole wave
-// from the band offsets: lane l covers experts [l per, l per + per) (E <= 1024,
-// so per <= 16), whose offsets it loads in one batch.
+// from the band offsets.  A band of c rows is cut into ceil(c / BM) even tiles
+// (of whole 16-row subtiles, the last one of the rows left).  Lane l covers
+// experts [l per, l per + per) (E <= 1024, so per <= 16), whose offsets it
+// loads in one batch; a wave prefix sum of the lanes' tile counts picks the
+// lane, which then finds its expert.
 //
-// Order.  Workgroup ids are dealt round-robin to the 8 XCDs.  Tiles are dealt
-// to the XCDs in turn, each with all its column groups in a row, so that these
-// read its dy rows from one L2; the groups of the last (tiles mod 8) tiles are
-// spread over all XCDs.  SORTED: tiles run from the largest to the smallest
-// (by subtiles), which fills the last round of workgroups best: w13 at 4,096
-// tokens and w2 (half as many groups) gain what the comment at the kernel says.
-template <int BM, bool SORTED>
+// Workgroup ids are dealt round-robin to the 8 XCDs.  Tiles are dealt to the
+// XCDs in turn, each with all its column groups in a row, so that these read
+// its dy rows from one L2; the groups of the last (tiles mod 8) tiles are
+// spread over all XCDs.  (Contiguous runs of tiles per XCD, which give one XCD
+// a whole tile more, cost 3 % on w2 at 4,096 tokens.)
+template <int BM>
 __device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, int E, int NB, int& nb) {
-  constexpr int PER = 16, CLASSES = SORTED ? BM / 16 : 1;
+  constexpr int PER = 16;
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) >> 6;
   const int e0 = lane * per;
   int o[PER + 1];
 #pragma unroll
   for (int i = 0; i <= PER; ++i) o[i] = i <= per ? off[min(e0 + i, E)] : 0;
-  // this lane's tiles by subtiles (SORTED) or all of them
-  int mine[CLASSES] = {};
+  int mine = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (i < per) {
-      const BandCut b = cut_band<BM>(o[i + 1] - o[i]);
-      if constexpr (SORTED) {
+    if (i < per) mine += (o[i + 1] - o[i] + BM - 1) / BM;
+  int incl = mine;
 #pragma unroll
-        for (int s = 0; s < CLASSES; ++s) mine[s] += tiles_of(b, s + 1);
-      } else {
-        mine[0] += b.n;
-      }
-    }
-  int total[CLASSES], tiles = 0;
-#pragma unroll
-  for (int s = 0; s < CLASSES; ++s) {
-    total[s] = wave_sum(mine[s]);
-    tiles += total[s];
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += v;
   }
+  const int tiles = __builtin_amdgcn_readlane(incl, 63);
   const int x = blockIdx.x & 7, k = blockIdx.x >> 3;
   const int whole = (tiles >> 3) * NB;
   int t;
@@ -151,40 +130,19 @@ __device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, i
   }
   BandTile b = {0, 0, 0};
   if (t >= tiles) return b;
-  // the class that holds tile t, and t's place in it
-  int cls = 0, own = mine[0];
-  if constexpr (SORTED) {
-    bool found = false;
-#pragma unroll
-    for (int s = CLASSES - 1; s >= 0; --s) {
-      if (!found && t < total[s]) {
-        found = true;
-        cls = s;
-        own = mine[s];
-      }
-      if (!found) t -= total[s];
-    }
-  }
-  int incl = own;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += v;
-  }
-  int left = t - (incl - own);    // tile t's place among this lane's tiles
-  const int src = __ffsll((unsigned long long)__ballot(left >= 0 && left < own)) - 1;
+  int left = t - (incl - mine);   // tile t's place among this lane's tiles
+  const int src = __ffsll((unsigned long long)__ballot(left >= 0 && left < mine)) - 1;
   bool found = false;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (i < per && !found) {
-      const BandCut cut = cut_band<BM>(o[i + 1] - o[i]);
-      const int n = SORTED ? tiles_of(cut, cls + 1) : cut.n;
+      const int c = o[i + 1] - o[i];
+      const int n = (c + BM - 1) / BM;
       if (left < n) {
-        // among tiles of one class, the last one comes last
-        const int j = SORTED && cut.share != 16 * (cls + 1) ? cut.n - 1 : left;
+        const int share = ((c + n - 1) / n + 15) & ~15;
         b.e = e0 + i;
-        b.m0 = o[i] + j * cut.share;
-        b.rows = min(cut.share, cut.c - j * cut.share);
+        b.m0 = o[i] + left * share;
+        b.rows = min(share, c - left * share);
         found = true;
       }
       left -= n;
@@ -396,7 +354,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   uint8_t* s_scale = s_words + 2 * R_BYTES;
   const int c16 = lane & 15, g = lane >> 4;
   int nb;
-  const BandTile tile = find_tile<BM, (MS > 2)>(p.off, p.E, p.NB, nb);
+  const BandTile tile = find_tile<BM>(p.off, p.E, p.NB, nb);
   if (tile.rows == 0) return;
   const Layout& L = p.L;
   const int N = (int)L.N, K = (int)L.K, KC = (int)L.KC;

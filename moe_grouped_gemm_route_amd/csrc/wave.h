@@ -19,11 +19,6 @@ __device__ __forceinline__ uint32_t dpp_or(uint32_t other, uint32_t v) {
 }
 
 template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_or(int other, int v) {
-  return __builtin_amdgcn_update_dpp(other, v, CTRL, ROWS, 0xF, false);
-}
-
-template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_or(float other, float v) {
   return __uint_as_float(dpp_or<CTRL, ROWS>(__float_as_uint(other), __float_as_uint(v)));
 }
