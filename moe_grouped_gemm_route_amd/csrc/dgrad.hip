@@ -593,7 +593,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   // the G before them are computed (rows past the tile read its last row).
   auto activation = [&](auto prec) __attribute__((always_inline)) {
     constexpr int PRE = decltype(prec)::value;
-    constexpr int G = PRE == 1 ? 4 : 2;
+    constexpr int G = PRE == 1 && MS == 8 ? 4 : 2;
     constexpr int GROUPS = MS * KB / G;
     Raw8<PRE> gate[2][G], up[2][G];
     auto load_group = [&](auto jc) __attribute__((always_inline)) {
