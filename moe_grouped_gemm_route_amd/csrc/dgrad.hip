@@ -36,7 +36,6 @@ namespace moe {
 
 constexpr int DG_BN = 64;                      // n per stage
 constexpr int DG_WAVES = 4;                    // waves per group
-constexpr int DG_KB = 2;                       // k blocks (32 output columns) per wave
 constexpr int DG_CUS = 256;
 
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
@@ -90,7 +89,8 @@ struct BandTile {
 // (of whole 16-row subtiles, the last one of the rows left).  Lane l covers
 // experts [l per, l per + per) (E <= 1024, so per <= 16), whose offsets it
 // loads in one batch; a wave prefix sum of the lanes' tile counts picks the
-// lane, which then finds its expert.
+// lane, which then finds its expert.  (Offsets are held to [0, M] and bands to
+// 0 rows, so that no offsets lead outside dy and dx.)
 //
 // Workgroup ids are dealt round-robin to the 8 XCDs.  Tiles are dealt to the
 // XCDs in turn, each with all its column groups in a row, so that these read
@@ -98,18 +98,18 @@ struct BandTile {
 // spread over all XCDs.  (Contiguous runs of tiles per XCD, which give one XCD
 // a whole tile more, cost 3 % on w2 at 4,096 tokens.)
 template <int BM>
-__device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, int E, int NB, int& nb) {
+__device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, int E, int M, int NB, int& nb) {
   constexpr int PER = 16;
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) >> 6;
   const int e0 = lane * per;
   int o[PER + 1];
 #pragma unroll
-  for (int i = 0; i <= PER; ++i) o[i] = i <= per ? off[min(e0 + i, E)] : 0;
+  for (int i = 0; i <= PER; ++i) o[i] = i <= per ? min(max(off[min(e0 + i, E)], 0), M) : 0;
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (i < per) mine += (o[i + 1] - o[i] + BM - 1) / BM;
+    if (i < per) mine += (max(o[i + 1] - o[i], 0) + BM - 1) / BM;
   int incl = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -136,7 +136,7 @@ __device__ __forceinline__ BandTile find_tile(const int32_t* __restrict__ off, i
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (i < per && !found) {
-      const int c = o[i + 1] - o[i];
+      const int c = max(o[i + 1] - o[i], 0);
       const int n = (c + BM - 1) / BM;
       if (left < n) {
         const int share = ((c + n - 1) / n + 15) & ~15;
@@ -186,12 +186,12 @@ __device__ __forceinline__ void decode_word(const RawWeights& r, Weights& w) {
   }
 }
 
-// Words [LO, HI) of the 4 words of each of a wave's k blocks.
-template <bool ANY, int LO, int HI>
-__device__ __forceinline__ void decode_words(const RawWeights (&r)[DG_KB], Weights (&w)[DG_KB]) {
+// Words [LO, HI) of the 4 words of each of a wave's KB k blocks.
+template <bool ANY, int LO, int HI, int KB>
+__device__ __forceinline__ void decode_words(const RawWeights (&r)[KB], Weights (&w)[KB]) {
   if constexpr (LO < HI) {
     decode_word<ANY, LO % 4>(r[LO / 4], w[LO / 4]);
-    decode_words<ANY, LO + 1, HI>(r, w);
+    decode_words<ANY, LO + 1, HI, KB>(r, w);
   }
 }
 
@@ -265,24 +265,24 @@ __device__ __forceinline__ void interleave() {
 // the decode, which issues in the shadow of the matrix instructions.  The last
 // group has no decode where there are others: it issues the LDS reads that the
 // next step starts with (next).
-template <bool ANY, int NSUB, int MAX, int... MS, typename ROWS, typename NEXT>
+template <bool ANY, int NSUB, int MAX, int KB, int... MS, typename ROWS, typename NEXT>
 __device__ __forceinline__ void dgrad_step(std::integer_sequence<int, MS...>, u32x4_t (&x)[2], ROWS rows, NEXT next,
-                                           const Weights (&w)[DG_KB], const RawWeights (&r)[DG_KB], Weights (&v)[DG_KB],
-                                           f32x4_t (&acc)[MAX][DG_KB][2]) {
+                                           const Weights (&w)[KB], const RawWeights (&r)[KB], Weights (&v)[KB],
+                                           f32x4_t (&acc)[MAX][KB][2]) {
   constexpr int DEC = NSUB > 1 ? NSUB - 1 : 1;   // groups that decode
   auto group = [&](auto mc) __attribute__((always_inline)) {
     constexpr int ms = decltype(mc)::value;
     const u32x4_t xa = x[ms & 1];
 #pragma unroll
-    for (int b = 0; b < DG_KB; ++b) {
+    for (int b = 0; b < KB; ++b) {
       acc[ms][b][0] = mfma16(w[b].even, xa, acc[ms][b][0]);
       acc[ms][b][1] = mfma16(w[b].odd, xa, acc[ms][b][1]);
     }
     if constexpr (ms + 2 < NSUB) x[ms & 1] = rows(ms + 2);
     if constexpr (ms < DEC) {
-      constexpr int LO = 4 * DG_KB * ms / DEC, HI = 4 * DG_KB * (ms + 1) / DEC;
-      decode_words<ANY, LO, HI>(r, v);
-      interleave<2 * DG_KB - 1, (ANY ? 8 : 4) * (HI - LO) / (2 * DG_KB)>();
+      constexpr int LO = 4 * KB * ms / DEC, HI = 4 * KB * (ms + 1) / DEC;
+      decode_words<ANY, LO, HI, KB>(r, v);
+      interleave<2 * KB - 1, (ANY ? 8 : 4) * (HI - LO) / (2 * KB)>();
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
@@ -303,7 +303,7 @@ struct DgradArgs {
   Layout L;
   const uint16_t* dy;
   const int32_t* off;
-  int E, NB;            // experts, column groups
+  int E, M, NB;         // experts, rows, column groups
   const void* pre;      // [M, 2K] gate and up sums, or NULL (no activation)
   int pre_bf16;
   void* dx;
@@ -319,7 +319,7 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Four waves take 64 output columns each.  NS groups of four waves share a workgroup; each walks its share of n (in whole stages, the last share padded
+// Four waves take KB k blocks (32 output columns) each.  NS groups of four waves share a workgroup; each walks its share of n (in whole stages, the last share padded
 // with empty ones) through LDS of its own, and the first adds up the partial
 // sums in order.
 //
@@ -327,16 +327,15 @@ __device__ __forceinline__ void lds_barrier() {
 // of stage i + 1 and codes and scale words of stage i + 3 are loaded; the
 // operands of stage i + 1 are decoded from its codes, which have landed, and
 // the scale words of stage i + 2 are spread out as f32.
-template <int FMT, int MS, int OCC, int NS>
+template <int FMT, int MS, int KB, int OCC, int NS>
 __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   constexpr int BM = MS * 16;                            // band rows per workgroup
-  constexpr int KB = DG_KB, KCW = DG_KB;                 // chunk columns (128 k) per workgroup
+  constexpr int KCW = KB;                                // chunk columns (128 k) per workgroup
   constexpr int A_BYTES = BM * DG_BN * 2;                // dy rows of 128 bytes
   constexpr int A_LOADS = A_BYTES / 1024 / DG_WAVES;     // 1 KiB loads per wave
   constexpr int C_BYTES = KCW * DG_BN / 16 * 1024;
   constexpr int H = FMT == 1 ? 2 : 1;                    // scales per 32-block
-  constexpr int RECS = FMT == 1 ? KCW / 2 : 1;           // scale records per 16 n: a wave's share per stage
-  constexpr int R_BYTES = DG_BN / 16 * RECS * 256;       // scale words
+    constexpr int R_BYTES = DG_BN / 16 * 256;              // scale words: a record per 16 n, a wave's share per stage
   constexpr int S_BYTES = H * DG_BN * KCW * 4 * 4;       // the same as f32
   constexpr int LOADS = A_LOADS + KB + 1;                // per wave and stage
   constexpr int GROUP_BYTES = 2 * A_BYTES + 3 * C_BYTES + 2 * (R_BYTES + S_BYTES);
@@ -354,7 +353,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   uint8_t* s_scale = s_words + 2 * R_BYTES;
   const int c16 = lane & 15, g = lane >> 4;
   int nb;
-  const BandTile tile = find_tile<BM>(p.off, p.E, p.NB, nb);
+  const BandTile tile = find_tile<BM>(p.off, p.E, p.M, p.NB, nb);
   if (tile.rows == 0) return;
   const Layout& L = p.L;
   const int N = (int)L.N, K = (int)L.K, KC = (int)L.KC;
@@ -397,7 +396,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   // Past the last stage the lane offsets lie outside the buffers, so the
   // loads fetch nothing and write zeros.
   const uint32_t l_dy = lds_addr(s_dy) + wave * A_LOADS * 1024, l_codes = lds_addr(s_codes) + wave * KB * 1024,
-                 l_words = lds_addr(s_words) + wave * RECS * 256;
+                 l_words = lds_addr(s_words) + wave * 256;
   auto load_dy = [&](int i) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) : 0u;
@@ -411,33 +410,27 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
 #pragma unroll
     for (int j = 0; j < KB; ++j)
       load_lds16<true>(l_codes + slot * C_BYTES + j * 1024, cr, live ? cvo : kLaneOob, ((q + j) * KC) << 10);
-    if (lane < RECS * 16)
+    if (lane < 16)
       load_lds16<false>(l_words + (i & 1) * R_BYTES, sr, live ? rvo : kLaneOob, q * groups * 256);
   };
   // This wave's scale words of stage i (n = c16 of 16-n block `wave`, k block
-  // g), from LDS and back to it as f32, [k block][half][n].
-  struct ScaleWords {
-    uint32_t w[RECS];
+  // g of the record's chunk columns), from LDS and back to it as f32,
+  // [k block][half][n].
+  auto scale_word = [&](int i) {
+    return *reinterpret_cast<const uint32_t*>(s_words + (i & 1) * R_BYTES + wave * 256 + lane * 4);
   };
-  auto scale_words = [&](int i) {
-    ScaleWords r;
-#pragma unroll
-    for (int u = 0; u < RECS; ++u)
-      r.w[u] = *reinterpret_cast<const uint32_t*>(s_words + (i & 1) * R_BYTES + (wave * RECS + u) * 256 + lane * 4);
-    return r;
-  };
-  auto spread_scales = [&](const ScaleWords& r, int i) {
+  auto spread_scales = [&](uint32_t w, int i) {
     float* s = reinterpret_cast<float*>(s_scale + (i & 1) * S_BYTES) + wave * 16 + c16;
     if (FMT == 0) {
 #pragma unroll
-      for (int j = 0; j < KCW; ++j) s[(j * 4 + g) * 64] = e8m0_to_f32((r.w[0] >> (8 * ((kc0 & 3) + j))) & 0xFFu);
+      for (int j = 0; j < KCW; ++j) s[(j * 4 + g) * 64] = e8m0_to_f32((w >> (8 * ((kc0 & 3) + j))) & 0xFFu);
     } else {
-#pragma unroll
-      for (int u = 0; u < RECS; ++u) {
-        s[((u * 8 + g) * 2) * 64] = e4m3_to_f32<0>(r.w[u]);
-        s[((u * 8 + g) * 2 + 1) * 64] = e4m3_to_f32<1>(r.w[u]);
-        s[((u * 8 + 4 + g) * 2) * 64] = e4m3_to_f32<2>(r.w[u]);
-        s[((u * 8 + 4 + g) * 2 + 1) * 64] = e4m3_to_f32<3>(r.w[u]);
+      if (KCW == 1) w >>= 16 * (kc0 & 1);
+      s[(g * 2) * 64] = e4m3_to_f32<0>(w);
+      s[(g * 2 + 1) * 64] = e4m3_to_f32<1>(w);
+      if (KCW == 2) {
+        s[((4 + g) * 2) * 64] = e4m3_to_f32<2>(w);
+        s[((4 + g) * 2 + 1) * 64] = e4m3_to_f32<3>(w);
       }
     }
   };
@@ -473,13 +466,13 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
     load_codes(1, 1);
     load_dy(0);
     vm_wait<0>();
-    spread_scales(scale_words(0), 0);
-    spread_scales(scale_words(1), 1);
+    spread_scales(scale_word(0), 0);
+    spread_scales(scale_word(1), 1);
     lds_barrier();
     RawWeights r[KB];
     Weights w[KB], v[KB];
     raw(0, 0, 0, r);
-    decode_words<any_v, 0, 4 * KB>(r, w);
+    decode_words<any_v, 0, 4 * KB, KB>(r, w);
     raw(0, 0, 1, r);
     // stage 2's words take stage 0's place, its f32 scales only after every
     // wave has read stage 0's
@@ -498,14 +491,14 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
       load_dy(i + 1);
       load_codes(i + 3, next_slot(next_slot(sc)));
       __builtin_amdgcn_sched_barrier(0);
-      dgrad_step<any_v, NSUB, MS>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 0, ms); },
+      dgrad_step<any_v, NSUB, MS, KB>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 0, ms); },
                                   [&] { first_rows(1); raw(sc, i + 1, 0, r); }, w, r, v, acc);
       vm_wait<LOADS>();                        // all but this stage's loads have landed
-      const ScaleWords words = scale_words(i + 2);
-      dgrad_step<any_v, NSUB, MS>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 1, ms); },
+      const uint32_t word = scale_word(i + 2);
+      dgrad_step<any_v, NSUB, MS, KB>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 1, ms); },
                                   [&] { raw(sc, i + 1, 1, r); }, v, r, w, acc);
       __builtin_amdgcn_sched_barrier(0);
-      spread_scales(words, i + 2);
+      spread_scales(word, i + 2);
       vm_wait<KB + 1>();                       // dy of the next stage has landed
       lds_barrier();
       sc = next_slot(sc);
@@ -631,11 +624,11 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   else activation(std::integral_constant<int, 2>{});
 }
 
-// The kernel for E experts and M rows: row subtiles of a tile, workgroups (an
-// upper bound: a band of c rows has at most c / BM + 1 tiles), and groups of
-// waves per workgroup.
+// The kernel for E experts and M rows: row subtiles of a tile, k blocks of a
+// wave (128 columns of a workgroup each), workgroups (an upper bound: a band
+// of c rows has at most c / BM + 1 tiles), and groups of waves per workgroup.
 struct DgradPlan {
-  int subtiles, parts;
+  int subtiles, blocks, parts;
   int64_t groups;
 };
 
@@ -646,24 +639,32 @@ static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
   // (at 48: 563 against 787 with 32 and 642 with 128), then 128 (at 96: 830
   // against 1,034 with 64)
   pl.subtiles = (int64_t)M <= 24 * (int64_t)E ? 2 : (int64_t)M < 72 * (int64_t)E ? 4 : 8;
-  const int cols = 128 * DG_KB;
-  pl.groups = ((int64_t)M / (16 * pl.subtiles) + (E < M ? E : M)) * ((K + cols - 1) / cols);
+  const int64_t tiles = (int64_t)M / (16 * pl.subtiles) + (E < M ? E : M);
+  pl.blocks = 2;
   pl.parts = 1;
+  pl.groups = tiles * ((K + 255) / 256);
   if (pl.subtiles == 2) {
-    // four groups of waves run on a CU at a time (three for NVFP4, by LDS)
-    const int64_t slots = DG_CUS * (fmt == 0 ? 4 : 3);
+    // A CU runs four groups of waves at a time (three for NVFP4, by LDS).  A
+    // step is bound by decoding, so few workgroups are spread first: n over
+    // the groups of a workgroup, then half as many columns over workgroups.
     const int most = fmt == 0 ? 4 : 3;
-    if (pl.groups * most <= slots) pl.parts = most;
-    else if (pl.groups * 2 <= slots) pl.parts = 2;
+    if (pl.groups <= DG_CUS) pl.parts = most;
+    else if (pl.groups * 2 <= DG_CUS * most) pl.parts = 2;
+    if (pl.groups * 2 <= DG_CUS) {
+      pl.blocks = 1;
+      pl.groups = tiles * (K / 128);
+    }
   }
   return pl;
 }
 
 int64_t dgrad_workgroups(int fmt, int32_t E, int32_t K, int32_t M) { return dgrad_plan(fmt, E, K, M).groups; }
 
-template <int FMT, int MS, int OCC, int NS>
-static void launch_dgrad_t(const DgradArgs& a, int64_t groups, hipStream_t stream) {
-  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0, stream, a);
+template <int FMT, int MS, int KB, int OCC, int NS>
+static void launch_dgrad_t(DgradArgs a, int64_t groups, hipStream_t stream) {
+  a.NB = (int)((a.L.K + 128 * KB - 1) / (128 * KB));
+  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, KB, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0, stream,
+                     a);
 }
 
 hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
@@ -675,24 +676,26 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
   a.dy = dy;
   a.off = group_offsets;
   a.E = E;
-  a.NB = (K + 128 * DG_KB - 1) / (128 * DG_KB);
+  a.M = M;
   a.pre = preact;
   a.pre_bf16 = preact_bf16;
   a.dx = dx;
   a.dx_bf16 = dx_bf16;
   const DgradPlan pl = dgrad_plan(fmt, E, K, M);
   if (fmt == 0) {
-    if (pl.subtiles == 8) launch_dgrad_t<0, 8, 2, 1>(a, pl.groups, stream);
-    else if (pl.subtiles == 4) launch_dgrad_t<0, 4, 3, 1>(a, pl.groups, stream);
-    else if (pl.parts == 4) launch_dgrad_t<0, 2, 4, 4>(a, pl.groups, stream);
-    else if (pl.parts == 2) launch_dgrad_t<0, 2, 4, 2>(a, pl.groups, stream);
-    else launch_dgrad_t<0, 2, 4, 1>(a, pl.groups, stream);
+    if (pl.subtiles == 8) launch_dgrad_t<0, 8, 2, 2, 1>(a, pl.groups, stream);
+    else if (pl.subtiles == 4) launch_dgrad_t<0, 4, 2, 3, 1>(a, pl.groups, stream);
+    else if (pl.blocks == 1) launch_dgrad_t<0, 2, 1, 4, 4>(a, pl.groups, stream);
+    else if (pl.parts == 4) launch_dgrad_t<0, 2, 2, 4, 4>(a, pl.groups, stream);
+    else if (pl.parts == 2) launch_dgrad_t<0, 2, 2, 4, 2>(a, pl.groups, stream);
+    else launch_dgrad_t<0, 2, 2, 4, 1>(a, pl.groups, stream);
   } else {
-    if (pl.subtiles == 8) launch_dgrad_t<1, 8, 2, 1>(a, pl.groups, stream);
-    else if (pl.subtiles == 4) launch_dgrad_t<1, 4, 3, 1>(a, pl.groups, stream);
-    else if (pl.parts == 3) launch_dgrad_t<1, 2, 3, 3>(a, pl.groups, stream);
-    else if (pl.parts == 2) launch_dgrad_t<1, 2, 3, 2>(a, pl.groups, stream);
-    else launch_dgrad_t<1, 2, 3, 1>(a, pl.groups, stream);
+    if (pl.subtiles == 8) launch_dgrad_t<1, 8, 2, 2, 1>(a, pl.groups, stream);
+    else if (pl.subtiles == 4) launch_dgrad_t<1, 4, 2, 3, 1>(a, pl.groups, stream);
+    else if (pl.blocks == 1) launch_dgrad_t<1, 2, 1, 3, 3>(a, pl.groups, stream);
+    else if (pl.parts == 3) launch_dgrad_t<1, 2, 2, 3, 3>(a, pl.groups, stream);
+    else if (pl.parts == 2) launch_dgrad_t<1, 2, 2, 3, 2>(a, pl.groups, stream);
+    else launch_dgrad_t<1, 2, 2, 3, 1>(a, pl.groups, stream);
   }
   return hipGetLastError();
 }
