@@ -405,6 +405,80 @@ def test_dgrad_every_band_size(rows):
     close(f64(got), oracle.gmm_dgrad(dy64, off, w), dgrad_bound(dy64, off, w, N), torch.float32)
 
 
+# grids that take each way of sharing the work: 128- and 256-column
+# workgroups, n walked by four (three, NVFP4), two or one group of waves, and
+# 32-, 64- and 128-row tiles; n of one stage, of fewer stages than groups, and
+# of a number no group count divides
+@pytest.mark.parametrize("E,K,rows", [(6, 896, 2), (40, 1024, 1), (100, 1024, 1), (210, 1024, 1), (30, 896, 7),
+                                      (12, 640, 40), (5, 640, 100)])
+@pytest.mark.parametrize("N", [64, 192, 1088])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "nvfp4_pow2"])
+def test_dgrad_every_grid(E, K, rows, N, fmt):
+    rng = np.random.default_rng(E + K + N)
+    counts = np.maximum(0, rows + rng.integers(-rows, rows + 1, size=E))
+    counts[0] = 3 * rows + 30
+    off, M = bands(counts, extra=1)
+    w, packed = make_weights(E, N, K, fmt, seed=E + N)
+    bits = random_dy(M, N, seed=K)
+    dy64 = bf16_bits_to_f64(bits)
+    live = off[-1]
+    out = torch.full((M, K), 9.0, device=DEV)
+    enum = moe.MXFP4 if fmt == "mxfp4" else moe.NVFP4
+    got = moe.moe_gmm_dgrad(packed, enum, E, N, K, to_dev(bits), to_dev(off), M, out=out)
+    close(f64(got)[:live], oracle.gmm_dgrad(dy64, off, w)[:live], dgrad_bound(dy64, off, w, N)[:live], torch.float32)
+    assert bool((out[live:] == 9.0).all())
+
+
+def test_dgrad_offsets_never_lead_outside():
+    # offsets past M, falling and negative ones: bands are cut to the rows that
+    # exist; rows of sound bands come out right and nothing else is touched
+    E, N, K, M = 5, 128, 256, 40
+    w, packed = make_weights(E, N, K, "mxfp4", seed=4)
+    bits = random_dy(M, N, seed=4)
+    good = np.array([0, 10, 20, 30, 40, 40], dtype=np.int32)
+    ref = oracle.gmm_dgrad(bf16_bits_to_f64(bits), good, w)
+    tol = dgrad_bound(bf16_bits_to_f64(bits), good, w, N)
+    pool = torch.full((M + 64, K), 7.0, device=DEV)
+    for bad in ([0, 10, 20, 30, 1 << 30, 1 << 30], [0, 10, 20, 30, 40, 5], [-50, 10, 20, 30, 40, 40]):
+        pool.fill_(7.0)
+        out = pool[:M]
+        moe.moe_gmm_dgrad(packed, moe.MXFP4, E, N, K, to_dev(bits), to_dev(np.array(bad, dtype=np.int32)), M, out=out)
+        close(f64(out), ref, tol, torch.float32)
+        assert bool((pool[M:] == 7.0).all())
+
+
+def test_sizes_past_32_bit_offsets():
+    # more than 2^31 elements (4 GiB of bf16): the last rows come out right
+    T, k, N = 270000, 2, 4096
+    M = T * k
+    pr = torch.arange(M - 1, -1, -1, dtype=torch.int32, device=DEV)       # pair p at row M - 1 - p
+    x = torch.zeros((T, N), dtype=torch.bfloat16, device=DEV)
+    x[0], x[-1] = 1.5, -2.5
+    xs = moe.moe_dispatch(x, pr, k)
+    assert bool((xs[-2:] == 1.5).all()) and bool((xs[:2] == -2.5).all()) and not bool(xs[2:-2].any())
+    dx = moe.moe_dispatch_bwd(xs, pr, k, out_dtype=moe.BF16)
+    assert bool((dx[0] == 3.0).all()) and bool((dx[-1] == -5.0).all())
+    w = torch.full((T, k), 0.5, device=DEV)
+    dy, dw = moe.moe_combine_bwd(x, xs, w, pr, out_dtype=moe.BF16)
+    assert bool((dy[-1] == 0.75).all()) and bool((dy[0] == -1.25).all())
+    assert dw[0].tolist() == [2.25 * N] * 2 and dw[-1].tolist() == [6.25 * N] * 2
+    del dy, dw, dx, xs
+    y = torch.zeros((M, N), dtype=torch.bfloat16, device=DEV)
+    y[-1, : N // 2], y[-1, N // 2:] = 200.0, 0.25
+    h = moe.silu_mul(y, out_dtype=moe.BF16)
+    assert bool((h[-1] == 50.0).all()) and not bool(h[:-1].any())
+    # the product's gradient, through the activation (dx of 2^31 elements)
+    E, n, K = 2, 64, 2048
+    _, packed = make_weights(E, n, K, "mxfp4", seed=6)
+    off = torch.tensor([0, M - 3, M], dtype=torch.int32, device=DEV)
+    dyb = torch.zeros((M, n), dtype=torch.bfloat16, device=DEV)
+    dyb[-1] = 1.0
+    got = moe.moe_gmm_dgrad(packed, moe.MXFP4, E, n, K, dyb, off, M, out_dtype=moe.BF16, act=moe.ACT_SILU_MUL, preact=y)
+    few = moe.moe_gmm_dgrad(packed, moe.MXFP4, E, n, K, dyb[-3:], torch.tensor([0, 0, 3], dtype=torch.int32, device=DEV),
+                            3, out_dtype=moe.BF16, act=moe.ACT_SILU_MUL, preact=y[-3:])
+    assert torch.equal(got[-1], few[-1]) and bool(got[-1].any()) and not bool(got[:-1].any())
+
+
 def test_dgrad_no_rows_and_bad_rows_stay_apart():
     E, N, K = 4, 128, 256
     _, packed = make_weights(E, N, K, "mxfp4", seed=1)
