@@ -322,14 +322,17 @@ def moe_combine(y, topk_weights, pair_row, out_dtype=F32):
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 _OUT = {F32: torch.float32, BF16: torch.bfloat16}
+_SCALARS = {int, float, type(None)}
 
 
 def _float(t, name, ndim):
     """A contiguous float32 or bfloat16 device tensor; returns its dtype enum."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
+    dt = _FLOATS.get(getattr(t, "dtype", None))
+    if dt is None:
         raise MoeGmmError("%s must be a float32 or bfloat16 tensor" % name)
-    _dev(t, t.dtype, name, ndim)
-    return _FLOATS[t.dtype]
+    if not (t.is_cuda and t.is_contiguous() and t.dim() == ndim):
+        _dev(t, t.dtype, name, ndim)
+    return dt
 
 
 def _out(out, shape, dtype, name, like):
@@ -348,18 +351,20 @@ def _out(out, shape, dtype, name, like):
 
 def _launch(fn, tensors, *args):
     """fn(*args, stream) on the device that holds every tensor of tensors (None
-    skipped; a tensor in args stands for its pointer), on that device's current
-    stream."""
+    skipped), on that device's current stream.  A tensor in args stands for its
+    pointer."""
     index = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise MoeGmmError("the tensors must be on one device, got %s and %s" % (tensors[0].device, t.device))
-    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    args = [a if type(a) in _SCALARS or not isinstance(a, torch.Tensor) else a.data_ptr() for a in args]
     if index == torch.cuda.current_device():
-        _check(fn(*args, _raw_stream(index)))
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            _check(fn(*args, _raw_stream(index)))
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _check(status)
 
 
 def topk_gate(logits, k, score=GATE_SOFTMAX, bias=None, renormalize=True, scale=1.0):

@@ -625,6 +625,26 @@ def test_layer_training_step_captured_in_a_graph():
             assert torch.equal(a, b), i
 
 
+def test_parameters_and_views_are_taken_and_strided_ones_refused():
+    # an nn.Parameter router output, a row range of a larger buffer; a column
+    # range or a transposed view is refused, not read wrongly
+    x = torch.nn.Parameter(torch.randn((9, 16), device=DEV))
+    ids, w = moe.topk_gate(x, 2)
+    ids2, w2 = moe.topk_gate(x.detach(), 2)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    big = torch.randn((20, 16), device=DEV)
+    assert torch.equal(moe.silu_mul(big[4:13]), moe.silu_mul(big[4:13].clone()))
+    for bad in (big[:, :8], big.t(), big[::2]):
+        with pytest.raises(moe.MoeGmmError):
+            moe.silu_mul(bad)
+        with pytest.raises(moe.MoeGmmError):
+            moe.topk_gate(bad, 2)
+    # rows that start off a 16-byte boundary
+    flat = torch.randn(4 * 12 + 2, device=DEV)
+    with pytest.raises(moe.MoeGmmError):
+        moe.moe_dispatch(flat[2:].view(4, 12), torch.arange(4, dtype=torch.int32, device=DEV), 1)
+
+
 def test_operators_on_another_stream():
     T, k, E, D, I = 30, 2, 8, 128, 128
     x, logits, bias, packs, _, dout = layer_inputs(T, k, E, D, I, seed=80)
