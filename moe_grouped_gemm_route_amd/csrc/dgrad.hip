@@ -200,10 +200,6 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
                                                  0, 0, 0);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  return (uint32_t)f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16);
-}
-
 __device__ __forceinline__ void store8(void* p, bool bf16, int64_t i, const float (&v)[8]) {
   if (bf16) {
     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) =

@@ -657,3 +657,22 @@ def test_operators_on_another_stream():
     s.synchronize()
     for a, b in zip(got, ref):
         assert torch.equal(a, b)
+
+
+def test_bf16_rounding_of_every_kind_of_value():
+    # dispatch_bwd with k = 1 is a rounding alone: ties to even, the largest
+    # finite values, subnormals, infinities and NaN as torch rounds them
+    rng = np.random.default_rng(90)
+    bits = rng.integers(0, 1 << 32, size=1 << 16, dtype=np.uint64).astype(np.uint32)
+    ties = (rng.integers(0, 1 << 16, size=4096, dtype=np.uint32) << 16) | 0x8000
+    edge = np.array([0, 0x80000000, 1, 0x7FFF, 0x8000, 0x8001, 0x7F7FFFFF, 0xFF7FFFFF, 0x7F7F7FFF, 0x7F7F8000,
+                     0x7F800000, 0xFF800000, 0x7FC00000, 0x7F800001, 0x00800000, 0x007FFFFF], dtype=np.uint32)
+    v = np.concatenate([bits, ties, edge])
+    v = np.concatenate([v, np.zeros(-len(v) % 64, dtype=np.uint32)]).view(np.float32).reshape(-1, 64)
+    x = torch.from_numpy(v.copy()).to(DEV)
+    pr = torch.arange(x.shape[0], dtype=torch.int32, device=DEV)
+    got, ref = moe.moe_dispatch_bwd(x, pr, 1, out_dtype=moe.BF16), x.bfloat16()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    ok = ~torch.isnan(ref)
+    # (0 + -0 is 0 in the sum: compare values)
+    assert torch.equal(got[ok], ref[ok])
