@@ -411,22 +411,25 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   };
   // This wave's scale words of stage i (n = c16 of 16-n block `wave`, k block
   // g of the record's chunk columns), from LDS and back to it as f32,
-  // [k block][half][n].
+  // [k block][half][n]; the high halves' n (NVFP4) are turned by 32, so that
+  // the lanes of the two halves read different banks (the same banks cost
+  // NVFP4 w2 at 256 tokens 16 % of its cycles).
   auto scale_word = [&](int i) {
     return *reinterpret_cast<const uint32_t*>(s_words + (i & 1) * R_BYTES + wave * 256 + lane * 4);
   };
   auto spread_scales = [&](uint32_t w, int i) {
     float* s = reinterpret_cast<float*>(s_scale + (i & 1) * S_BYTES) + wave * 16 + c16;
+    float* hi = s + ((wave ^ 2) - wave) * 16;
     if (FMT == 0) {
 #pragma unroll
       for (int j = 0; j < KCW; ++j) s[(j * 4 + g) * 64] = e8m0_to_f32((w >> (8 * ((kc0 & 3) + j))) & 0xFFu);
     } else {
       if (KCW == 1) w >>= 16 * (kc0 & 1);
       s[(g * 2) * 64] = e4m3_to_f32<0>(w);
-      s[(g * 2 + 1) * 64] = e4m3_to_f32<1>(w);
+      hi[(g * 2 + 1) * 64] = e4m3_to_f32<1>(w);
       if (KCW == 2) {
         s[((4 + g) * 2) * 64] = e4m3_to_f32<2>(w);
-        s[((4 + g) * 2 + 1) * 64] = e4m3_to_f32<3>(w);
+        hi[((4 + g) * 2 + 1) * 64] = e4m3_to_f32<3>(w);
       }
     }
   };
@@ -434,7 +437,9 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   // Step s (32 n) of a stage: codes and scales of this wave's k blocks,
   // and the band rows of subtile ms.
   const uint32_t q_off = (kcw * 4 + (g >> 1)) * 1024 + kb0 * 256 + (g & 1) * 128 + c16 * 8;
-  const uint32_t s_off = (((kcw * 4 + kb0) * H + (H == 2 ? c16 >> 3 : 0)) * 64 + g * 8) << 2;
+  const uint32_t half = H == 2 ? c16 >> 3 : 0;
+  const uint32_t s_off = (((kcw * 4 + kb0) * H + half) * 64 + g * 8) << 2;
+  const uint32_t s_turn = half * 128;
   const uint32_t a_off = c16 * 128 + ((g ^ ((c16 >> 1) & 7)) << 4);
   auto raw = [&](uint32_t slot, int i, int s, RawWeights (&r)[KB]) {
     const uint8_t* st = s_codes + slot * C_BYTES;
@@ -442,7 +447,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
       r[b].q = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(st + q_off + s * 2048 + b * 256));
-      const f32x4_t* f = reinterpret_cast<const f32x4_t*>(sc + s_off + s * 128 + b * 256 * H);
+      const f32x4_t* f = reinterpret_cast<const f32x4_t*>(sc + s_off + ((s * 128) ^ s_turn) + b * 256 * H);
       r[b].s[0] = f[0];
       r[b].s[1] = f[1];
     }
