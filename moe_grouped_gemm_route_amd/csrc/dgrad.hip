@@ -26,6 +26,26 @@
 // lane l of the result holds band row l & 15 and c = 4g .. 4g + 3: together
 // with the even/odd pair, eight consecutive columns, stored as whole 16-byte
 // words.
+//
+// What bounds it, measured (one MI355X, 256 experts top-6):
+//   w13 (4,096 x 4,096), 4,096 tokens: 770-800 us, 1.03-1.07 PFLOP/s of useful
+//     products (a bf16 library product of 8,192^3 reaches 1.39 on this card,
+//     the forward tiled kernel on the same bands 1.0-1.1).  The matrix pipes
+//     are busy 59 % of the time at 1.9 GHz, LDS 30 %, VALU 44 %; time goes with
+//     the power that the code stream, the LDS reads and the decode draw: the
+//     loop without its loads runs in 589 of 815 us, without the decode in 712.
+//   the same at 64 tokens: 287 us, 6.2 TB/s of codes: HBM (6.6 TB/s reads).
+//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 213 us, 4.6
+//     TB/s: the general decode (two multiplies a weight pair more) keeps the
+//     VALU busy 66 % beside the stream.
+//   w13 at 1 token (6 experts): 23 us: the decode of 16 stages a wave, one
+//     after the other, on 192 CUs.
+// Steps that brought it there (w13, 4,096 tokens): one stage, loaded and then
+// computed, 988 us; walks per number of 16-row subtiles, staged one ahead, 915;
+// column groups of a tile on one XCD 881; decode among the matrix instructions
+// 834; direct-to-LDS loads 815; tiles dealt to the XCDs, one convert per bf16
+// pair 788.  Tried and dropped: 512-column workgroups of eight waves (856) or
+// of four waves with 128 columns each (1,249); the largest tiles first (+2 %).
 #include <utility>
 
 #include "common.h"
@@ -403,11 +423,11 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   auto load_codes = [&](int i, uint32_t slot) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) * (DG_BN / 16) : 0u;
+    if (lane < 16)
+      load_lds16<false>(l_words + (i & 1) * R_BYTES, sr, live ? rvo : kLaneOob, q * groups * 256);
 #pragma unroll
     for (int j = 0; j < KB; ++j)
       load_lds16<true>(l_codes + slot * C_BYTES + j * 1024, cr, live ? cvo : kLaneOob, ((q + j) * KC) << 10);
-    if (lane < 16)
-      load_lds16<false>(l_words + (i & 1) * R_BYTES, sr, live ? rvo : kLaneOob, q * groups * 256);
   };
   // This wave's scale words of stage i (n = c16 of 16-n block `wave`, k block
   // g of the record's chunk columns), from LDS and back to it as f32,
