@@ -24,6 +24,7 @@
  *    failure reported by the runtime returns MOE_ERR_HIP.
  *  - bf16 values are passed as uint16_t bit patterns; f32 as float.
  *  - Array shapes are row-major, written [d0, d1, ...].
+ *  - Output buffers overlap neither inputs nor one another.
  */
 #ifndef MOE_GMM_H
 #define MOE_GMM_H
@@ -374,8 +375,8 @@ int moe_combine(const void* y, int y_dtype, const float* topk_weights,
  * ones by ascending index.  Without a bias the logits are compared
  * themselves; with one the sums are compared in f64.
  *   topk_weights[t, j] = scale * s_ej / (renorm ? sum of the chosen s : 1)
- * in f32.  A logit that is -inf or NaN (or an expert whose bias is NaN)
- * masks its expert for that token: it is never chosen and adds nothing to a
+ * in f32.  A logit that is -inf or NaN (or an expert whose bias is -inf or
+ * NaN) masks its expert for that token: it is never chosen and adds nothing to a
  * softmax.  Where fewer than k experts are left, the remaining slots get id
  * -1 and weight 0; moe_route_sort drops such pairs (and counts them).
  *
@@ -502,11 +503,16 @@ int moe_silu_mul(const void* y, int y_dtype, int32_t M, int32_t N, const int32_t
  * dx             out, f32 or bf16 (dx_dtype; RNE).  Rows [group_offsets[E], M)
  *                are not written.
  * Preconditions not checked: group_offsets is non-decreasing with
- * group_offsets[0] = 0 and group_offsets[E] <= M.  Exact-decode domain as
- * moe_gmm.
+ * group_offsets[0] = 0 and group_offsets[E] <= M (offsets that are not lead to
+ * unspecified rows, but to no access outside dy, preact and dx).  Exact-decode
+ * domain as moe_gmm.
  * Limits: K % 128 == 0, N % 64 == 0, E <= 1024, M <= 2^24, N*K/2 and 256*N
- * <= 2^31 - 64 KiB, and a grid of (M/128 + min(E, M)) * ceil(K/256) <=
- * 16,777,215 workgroups; packed 256-byte, dy, preact and dx 16-byte aligned.
+ * <= 2^31 - 64 KiB, and a grid of (M/BM + min(E, M)) * ceil(K/256) <=
+ * 16,777,215 workgroups, with row tiles of BM = 32 rows up to a mean band M/E
+ * of 24, 64 below 72, 128 above; packed 256-byte, dy, preact and dx 16-byte
+ * aligned.
+ * Equal calls return equal bits.  The order of the f32 sums over n depends on
+ * fmt, E, K and M (few rows share n between waves), not on the offsets.
  */
 int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
                   const int32_t* group_offsets, int32_t M, const void* preact, int preact_dtype,
