@@ -511,6 +511,9 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
       __builtin_amdgcn_sched_barrier(0);
       load_dy(i + 1);
       load_codes(i + 3, next_slot(next_slot(sc)));
+      // the waves at their products before those between stages (128-row tiles:
+      // 801 -> 790 us; thin ones lose)
+      if (MS == 8) __builtin_amdgcn_s_setprio(1);
       __builtin_amdgcn_sched_barrier(0);
       dgrad_step<any_v, NSUB, MS, KB>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 0, ms); },
                                   [&] { first_rows(1); raw(sc, i + 1, 0, r); }, w, r, v, acc);
@@ -519,6 +522,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
       dgrad_step<any_v, NSUB, MS, KB>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 1, ms); },
                                   [&] { raw(sc, i + 1, 1, r); }, v, r, w, acc);
       __builtin_amdgcn_sched_barrier(0);
+      if (MS == 8) __builtin_amdgcn_s_setprio(0);
       spread_scales(word, i + 2);
       vm_wait<KB + 1>();                       // dy of the next stage has landed
       lds_barrier();
