@@ -71,6 +71,12 @@ __device__ __forceinline__ u32x4_t make_rsrc(const void* base, uint32_t bytes) {
   return u32x4_t{uniform((uint32_t)a), uniform((uint32_t)(a >> 32) & 0xFFFFu), uniform(bytes), 0x00020000u};
 }
 
+// The same range, or an empty one.
+__device__ __forceinline__ u32x4_t only_if(bool live, u32x4_t rsrc) {
+  rsrc[2] = live ? rsrc[2] : 0u;
+  return rsrc;
+}
+
 __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_u8_t)p; }
 
 // 16 bytes per active lane straight to LDS: lane l's at lds + 16 l.  Written
@@ -409,8 +415,8 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   // stages [first, end) of this group; every group runs `steps`
   const int steps = (N / DG_BN + NS - 1) / NS;
   const int first = part * steps, end = min(N / DG_BN, first + steps);
-  // Past the last stage the lane offsets lie outside the buffers, so the
-  // loads fetch nothing and write zeros.
+  // Past the last stage the buffers are empty, so the loads fetch nothing and
+  // write zeros.
   const uint32_t l_dy = lds_addr(s_dy) + wave * A_LOADS * 1024, l_codes = lds_addr(s_codes) + wave * KB * 1024,
                  l_words = lds_addr(s_words) + wave * 256;
   auto load_dy = [&](int i) {
@@ -418,16 +424,16 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
     const uint32_t q = live ? (uint32_t)(first + i) : 0u;
 #pragma unroll
     for (int j = 0; j < A_LOADS; ++j)
-      load_lds16<false>(l_dy + (i & 1) * A_BYTES + j * 1024, ar, live ? avo[j] : kLaneOob, q * DG_BN * 2);
+      load_lds16<false>(l_dy + (i & 1) * A_BYTES + j * 1024, only_if(live, ar), avo[j], q * DG_BN * 2);
   };
   auto load_codes = [&](int i, uint32_t slot) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) * (DG_BN / 16) : 0u;
     if (lane < 16)
-      load_lds16<false>(l_words + (i & 1) * R_BYTES, sr, live ? rvo : kLaneOob, q * groups * 256);
+      load_lds16<false>(l_words + (i & 1) * R_BYTES, only_if(live, sr), rvo, q * groups * 256);
 #pragma unroll
     for (int j = 0; j < KB; ++j)
-      load_lds16<true>(l_codes + slot * C_BYTES + j * 1024, cr, live ? cvo : kLaneOob, ((q + j) * KC) << 10);
+      load_lds16<true>(l_codes + slot * C_BYTES + j * 1024, only_if(live, cr), cvo, ((q + j) * KC) << 10);
   };
   // This wave's scale words of stage i (n = c16 of 16-n block `wave`, k block
   // g of the record's chunk columns), from LDS and back to it as f32,
