@@ -91,10 +91,10 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, u32x4_t rsrc, uint32_t 
   rsrc = u32x4_t{uniform(rsrc[0]), uniform(rsrc[1]), uniform(rsrc[2]), 0x00020000u};
   if (NT)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
-                 :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory");
+                 :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory");
+                 :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory", "m0");
 }
 
 // At most VM vector loads of this wave are still on their way.
@@ -332,8 +332,8 @@ struct DgradArgs {
   int dx_bf16;
 };
 
-// Ends a step: this wave's LDS operations are done, then the workgroup
-// barrier.  Loads into registers stay in flight.
+// Ends a stage: this wave's LDS operations are done, then the workgroup
+// barrier.  Vector loads stay on their way (vm_wait counts them).
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4));   // vmcnt 63, expcnt 7, lgkmcnt 0
@@ -341,9 +341,10 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Four waves take KB k blocks (32 output columns) each.  NS groups of four waves share a workgroup; each walks its share of n (in whole stages, the last share padded
-// with empty ones) through LDS of its own, and the first adds up the partial
-// sums in order.
+// Four waves take KB k blocks (32 output columns) each.  NS groups of four
+// waves share a workgroup; each walks its share of n (in whole stages, the
+// last share padded with empty ones) through LDS of its own, and the first
+// adds up the partial sums in order.
 //
 // Stages.  All operands go straight to LDS.  While stage i is multiplied, dy
 // of stage i + 1 and codes and scale words of stage i + 3 are loaded; the
@@ -357,7 +358,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   constexpr int A_LOADS = A_BYTES / 1024 / DG_WAVES;     // 1 KiB loads per wave
   constexpr int C_BYTES = KCW * DG_BN / 16 * 1024;
   constexpr int H = FMT == 1 ? 2 : 1;                    // scales per 32-block
-    constexpr int R_BYTES = DG_BN / 16 * 256;              // scale words: a record per 16 n, a wave's share per stage
+  constexpr int R_BYTES = DG_BN / 16 * 256;              // scale words: a record per 16 n, one a wave
   constexpr int S_BYTES = H * DG_BN * KCW * 4 * 4;       // the same as f32
   constexpr int LOADS = A_LOADS + KB + 1;                // per wave and stage
   constexpr int GROUP_BYTES = 2 * A_BYTES + 3 * C_BYTES + 2 * (R_BYTES + S_BYTES);
@@ -438,8 +439,8 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   // This wave's scale words of stage i (n = c16 of 16-n block `wave`, k block
   // g of the record's chunk columns), from LDS and back to it as f32,
   // [k block][half][n]; the high halves' n (NVFP4) are turned by 32, so that
-  // the lanes of the two halves read different banks (the same banks cost
-  // NVFP4 w2 at 256 tokens 16 % of its cycles).
+  // the lanes of the two halves read different banks (NVFP4 w2 at 128 tokens:
+  // 222 -> 216 us).
   auto scale_word = [&](int i) {
     return *reinterpret_cast<const uint32_t*>(s_words + (i & 1) * R_BYTES + wave * 256 + lane * 4);
   };
@@ -665,19 +666,21 @@ struct DgradPlan {
 
 static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
   DgradPlan pl;
-  // by the mean band: 32-row tiles up to 24 rows (w13, 4,096 x 4,096, at 24
+  // By the mean band: 32-row tiles up to 24 rows (w13, 4,096 x 4,096, at 24
   // rows a band: 439 us against 463 with 64-row tiles), 64-row tiles to 72
   // (at 48: 563 against 787 with 32 and 642 with 128), then 128 (at 96: 830
-  // against 1,034 with 64)
+  // against 1,034 with 64).
   pl.subtiles = (int64_t)M <= 24 * (int64_t)E ? 2 : (int64_t)M < 72 * (int64_t)E ? 4 : 8;
   const int64_t tiles = (int64_t)M / (16 * pl.subtiles) + (E < M ? E : M);
   pl.blocks = 2;
   pl.parts = 1;
   pl.groups = tiles * ((K + 255) / 256);
   if (pl.subtiles == 2) {
-    // A CU runs four groups of waves at a time (three for NVFP4, by LDS).  A
-    // step is bound by decoding, so few workgroups are spread first: n over
-    // the groups of a workgroup, then half as many columns over workgroups.
+    // A CU runs four groups of waves at a time (three for NVFP4, by LDS), and
+    // a short grid is bound by how fast a wave decodes its stages.  Where the
+    // groups have room, n is shared by several (w13, 1 token: 50 -> 30 us with
+    // four), and where half the CUs would idle, a workgroup takes 128 columns
+    // (28 -> 23 us).
     const int most = fmt == 0 ? 4 : 3;
     if (pl.groups <= DG_CUS) pl.parts = most;
     else if (pl.groups * 2 <= DG_CUS * most) pl.parts = 2;
