@@ -336,7 +336,7 @@ int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, 
   // offsets, below the lane offset that reads zeros
   if ((int64_t)N * (K / 2) > (int64_t)moe::kLaneOob || (int64_t)N * 256 > (int64_t)moe::kLaneOob) return MOE_ERR_SHAPE;
   if (((uintptr_t)packed & 255) || !aligned16(dy) || !aligned16(dx)) return MOE_ERR_SHAPE;
-  if (moe::dgrad_workgroups(fmt, E, K, M) > kMaxWorkgroups) return MOE_ERR_SHAPE;
+  if (moe::dgrad_workgroups(E, K, M) > kMaxWorkgroups) return MOE_ERR_SHAPE;
   return hip_status(moe::launch_dgrad(static_cast<const uint8_t*>(packed), fmt, E, N, K, dy, group_offsets, M, preact,
                                       preact_dtype == MOE_BF16, dx, dx_dtype == MOE_BF16,
                                       static_cast<hipStream_t>(stream)));

@@ -35,10 +35,10 @@
 //     the power that the code stream, the LDS reads and the decode draw: the
 //     loop without its loads runs in 589 of 815 us, without the decode in 712.
 //   the same at 64 tokens: 287 us, 6.2 TB/s of codes: HBM (6.6 TB/s reads).
-//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 213 us, 4.6
-//     TB/s: the general decode (two multiplies a weight pair more) keeps the
-//     VALU busy 66 % beside the stream.
-//   w13 at 1 token (6 experts): 23 us: the decode of 16 stages a wave, one
+//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 210 us, 4.6
+//     TB/s: the general decode (twice the instructions) keeps the VALU busy
+//     66 % beside the stream.
+//   w13 at 1 token (6 experts): 22 us: the decode of 16 stages a wave, one
 //     after the other, on 192 CUs.
 // Steps that brought it there (w13, 4,096 tokens): one stage, loaded and then
 // computed, 988 us; walks per number of 16-row subtiles, staged one ahead, 915;
@@ -347,10 +347,10 @@ __device__ __forceinline__ void lds_barrier() {
 // adds up the partial sums in order.
 //
 // Stages.  All operands go straight to LDS.  While stage i is multiplied, dy
-// of stage i + 1 and codes and scale words of stage i + 3 are loaded; the
-// operands of stage i + 1 are decoded from its codes, which have landed, and
-// the scale words of stage i + 2 are spread out as f32.
-template <int FMT, int MS, int KB, int OCC, int NS>
+// of stage i + 1, codes of stage i + CR and scale words of stage i + 3 are
+// loaded; the operands of stage i + 1 are decoded from its codes, which have
+// landed, and the scale words of stage i + 2 are spread out as f32.
+template <int FMT, int MS, int KB, int CR, int OCC, int NS>
 __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   constexpr int BM = MS * 16;                            // band rows per workgroup
   constexpr int KCW = KB;                                // chunk columns (128 k) per workgroup
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   constexpr int R_BYTES = DG_BN / 16 * 256;              // scale words: a record per 16 n, one a wave
   constexpr int S_BYTES = H * DG_BN * KCW * 4 * 4;       // the same as f32
   constexpr int LOADS = A_LOADS + KB + 1;                // per wave and stage
-  constexpr int GROUP_BYTES = 2 * A_BYTES + 3 * C_BYTES + 2 * (R_BYTES + S_BYTES);
+  constexpr int GROUP_BYTES = 2 * A_BYTES + CR * C_BYTES + 2 * (R_BYTES + S_BYTES);
   constexpr int PART_BYTES = DG_WAVES * MS * KB * 2 * 64 * 16;   // a group's accumulators
   static_assert(DG_BN / 16 == DG_WAVES && A_LOADS >= 1, "whole loads per wave");
   static_assert((NS - 1) * PART_BYTES <= NS * GROUP_BYTES, "the partial sums fit the stages");
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   const int part = NS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (DG_WAVES * 64)) : 0;
   uint8_t* s_dy = s_all + part * GROUP_BYTES;
   uint8_t* s_codes = s_dy + 2 * A_BYTES;
-  uint8_t* s_words = s_codes + 3 * C_BYTES;
+  uint8_t* s_words = s_codes + CR * C_BYTES;
   uint8_t* s_scale = s_words + 2 * R_BYTES;
   const int c16 = lane & 15, g = lane >> 4;
   int nb;
@@ -427,11 +427,15 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
     for (int j = 0; j < A_LOADS; ++j)
       load_lds16<false>(l_dy + (i & 1) * A_BYTES + j * 1024, only_if(live, ar), avo[j], q * DG_BN * 2);
   };
-  auto load_codes = [&](int i, uint32_t slot) {
+  auto load_words = [&](int i) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) * (DG_BN / 16) : 0u;
     if (lane < 16)
       load_lds16<false>(l_words + (i & 1) * R_BYTES, only_if(live, sr), rvo, q * groups * 256);
+  };
+  auto load_codes = [&](int i, uint32_t slot) {
+    const bool live = first + i < end;
+    const uint32_t q = live ? (uint32_t)(first + i) * (DG_BN / 16) : 0u;
 #pragma unroll
     for (int j = 0; j < KB; ++j)
       load_lds16<true>(l_codes + slot * C_BYTES + j * 1024, only_if(live, cr), cvo, ((q + j) * KC) << 10);
@@ -482,7 +486,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   auto rows = [&](const uint8_t* a, int s, int ms) {
     return *reinterpret_cast<const u32x4_t*>(a + (a_off ^ (s * 64)) + ms * 2048);
   };
-  auto next_slot = [](uint32_t slot) { return slot == 2 ? 0u : slot + 1; };
+  auto next_slot = [](uint32_t slot) { return slot == CR - 1 ? 0u : slot + 1; };
 
   // The walk of a tile with nsub 16-row subtiles: the operands of a step are
   // decoded among the matrix instructions of the step before.  (Inlined, so
@@ -490,6 +494,8 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   auto walk = [&](auto any, auto nsub) __attribute__((always_inline)) {
     constexpr bool any_v = decltype(any)::value;
     constexpr int NSUB = decltype(nsub)::value;
+    load_words(0);
+    load_words(1);
     load_codes(0, 0);
     load_codes(1, 1);
     load_dy(0);
@@ -504,7 +510,8 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
     raw(0, 0, 1, r);
     // stage 2's words take stage 0's place, its f32 scales only after every
     // wave has read stage 0's
-    load_codes(2, 2);
+    load_words(2);
+    if (CR == 3) load_codes(2, 2);
     lds_barrier();
     uint32_t sc = 1;                           // codes' LDS slot of stage i + 1
     for (int i = 0; i < steps; ++i) {
@@ -517,7 +524,9 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
       first_rows(0);
       __builtin_amdgcn_sched_barrier(0);
       load_dy(i + 1);
-      load_codes(i + 3, next_slot(next_slot(sc)));
+      if (CR == 2) load_codes(i + 2, next_slot(sc));
+      load_words(i + 3);
+      if (CR == 3) load_codes(i + 3, next_slot(next_slot(sc)));
       // the waves at their products before those between stages (128-row tiles:
       // 801 -> 790 us; thin ones lose)
       if (MS == 8) __builtin_amdgcn_s_setprio(1);
@@ -531,7 +540,8 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
       __builtin_amdgcn_sched_barrier(0);
       if (MS == 8) __builtin_amdgcn_s_setprio(0);
       spread_scales(word, i + 2);
-      vm_wait<KB + 1>();                       // dy of the next stage has landed
+      // dy of the next stage has landed, and (CR 2) codes of the one after
+      vm_wait<CR == 3 ? KB + 1 : 1>();
       lds_barrier();
       sc = next_slot(sc);
     }
@@ -664,7 +674,7 @@ struct DgradPlan {
   int64_t groups;
 };
 
-static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
+static DgradPlan dgrad_plan(int32_t E, int32_t K, int32_t M) {
   DgradPlan pl;
   // By the mean band: 32-row tiles up to 24 rows (w13, 4,096 x 4,096, at 24
   // rows a band: 439 us against 463 with 64-row tiles), 64-row tiles to 72
@@ -676,14 +686,12 @@ static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
   pl.parts = 1;
   pl.groups = tiles * ((K + 255) / 256);
   if (pl.subtiles == 2) {
-    // A CU runs four groups of waves at a time (three for NVFP4, by LDS), and
-    // a short grid is bound by how fast a wave decodes its stages.  Where the
-    // groups have room, n is shared by several (w13, 1 token: 50 -> 30 us with
-    // four), and where half the CUs would idle, a workgroup takes 128 columns
-    // (28 -> 23 us).
-    const int most = fmt == 0 ? 4 : 3;
-    if (pl.groups <= DG_CUS) pl.parts = most;
-    else if (pl.groups * 2 <= DG_CUS * most) pl.parts = 2;
+    // A CU runs four groups of waves at a time, and a short grid is bound by
+    // how fast a wave decodes its stages.  Where the groups have room, n is
+    // shared by several (w13, 1 token: 50 -> 30 us with four), and where half
+    // the CUs would idle, a workgroup takes 128 columns (28 -> 23 us).
+    if (pl.groups <= DG_CUS) pl.parts = 4;
+    else if (pl.groups <= 2 * DG_CUS) pl.parts = 2;
     if (pl.groups * 2 <= DG_CUS) {
       pl.blocks = 1;
       pl.groups = tiles * (K / 128);
@@ -692,13 +700,27 @@ static DgradPlan dgrad_plan(int fmt, int32_t E, int32_t K, int32_t M) {
   return pl;
 }
 
-int64_t dgrad_workgroups(int fmt, int32_t E, int32_t K, int32_t M) { return dgrad_plan(fmt, E, K, M).groups; }
+int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M) { return dgrad_plan(E, K, M).groups; }
 
 template <int FMT, int MS, int KB, int OCC, int NS>
 static void launch_dgrad_t(DgradArgs a, int64_t groups, hipStream_t stream) {
+  // three stages of codes; two for NVFP4's 32-row tiles, whose f32 scales take
+  // twice the LDS, so that four groups of waves still fit a CU (w2 at 256
+  // tokens 222 -> 210 us)
+  constexpr int CR = FMT == 1 && MS == 2 ? 2 : 3;
   a.NB = (int)((a.L.K + 128 * KB - 1) / (128 * KB));
-  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, KB, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0, stream,
-                     a);
+  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, KB, CR, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0,
+                     stream, a);
+}
+
+template <int FMT>
+static void launch_dgrad_plan(const DgradArgs& a, const DgradPlan& pl, hipStream_t stream) {
+  if (pl.subtiles == 8) launch_dgrad_t<FMT, 8, 2, 2, 1>(a, pl.groups, stream);
+  else if (pl.subtiles == 4) launch_dgrad_t<FMT, 4, 2, 3, 1>(a, pl.groups, stream);
+  else if (pl.blocks == 1) launch_dgrad_t<FMT, 2, 1, 4, 4>(a, pl.groups, stream);
+  else if (pl.parts == 4) launch_dgrad_t<FMT, 2, 2, 4, 4>(a, pl.groups, stream);
+  else if (pl.parts == 2) launch_dgrad_t<FMT, 2, 2, 4, 2>(a, pl.groups, stream);
+  else launch_dgrad_t<FMT, 2, 2, 4, 1>(a, pl.groups, stream);
 }
 
 hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
@@ -715,22 +737,9 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
   a.pre_bf16 = preact_bf16;
   a.dx = dx;
   a.dx_bf16 = dx_bf16;
-  const DgradPlan pl = dgrad_plan(fmt, E, K, M);
-  if (fmt == 0) {
-    if (pl.subtiles == 8) launch_dgrad_t<0, 8, 2, 2, 1>(a, pl.groups, stream);
-    else if (pl.subtiles == 4) launch_dgrad_t<0, 4, 2, 3, 1>(a, pl.groups, stream);
-    else if (pl.blocks == 1) launch_dgrad_t<0, 2, 1, 4, 4>(a, pl.groups, stream);
-    else if (pl.parts == 4) launch_dgrad_t<0, 2, 2, 4, 4>(a, pl.groups, stream);
-    else if (pl.parts == 2) launch_dgrad_t<0, 2, 2, 4, 2>(a, pl.groups, stream);
-    else launch_dgrad_t<0, 2, 2, 4, 1>(a, pl.groups, stream);
-  } else {
-    if (pl.subtiles == 8) launch_dgrad_t<1, 8, 2, 2, 1>(a, pl.groups, stream);
-    else if (pl.subtiles == 4) launch_dgrad_t<1, 4, 2, 3, 1>(a, pl.groups, stream);
-    else if (pl.blocks == 1) launch_dgrad_t<1, 2, 1, 3, 3>(a, pl.groups, stream);
-    else if (pl.parts == 3) launch_dgrad_t<1, 2, 2, 3, 3>(a, pl.groups, stream);
-    else if (pl.parts == 2) launch_dgrad_t<1, 2, 2, 3, 2>(a, pl.groups, stream);
-    else launch_dgrad_t<1, 2, 2, 3, 1>(a, pl.groups, stream);
-  }
+  const DgradPlan pl = dgrad_plan(E, K, M);
+  if (fmt == 0) launch_dgrad_plan<0>(a, pl, stream);
+  else launch_dgrad_plan<1>(a, pl, stream);
   return hipGetLastError();
 }
 

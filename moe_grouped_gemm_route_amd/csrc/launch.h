@@ -118,6 +118,6 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
                         const int32_t* group_offsets, int32_t M, const void* preact, int preact_bf16, void* dx,
                         int dx_bf16, hipStream_t stream);
 // Workgroups that launch_dgrad launches for these sizes.
-int64_t dgrad_workgroups(int fmt, int32_t E, int32_t K, int32_t M);
+int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M);
 
 }  // namespace moe
