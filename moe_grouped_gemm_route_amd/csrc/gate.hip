@@ -3,8 +3,9 @@
 //
 // One wave per token; lane l holds experts l, l + 64, l + 128, ...  The k
 // choices are k rounds of "largest key over the wave, lowest index among
-// equals": the maximum is one DPP reduction, and because a slot's 64 experts
-// are consecutive, the lowest index is the first set bit of the first
+// equals": the keys are unsigned integers in the order of the values, the
+// maximum is one DPP reduction of six instructions, and because a slot's 64
+// experts are consecutive, the lowest index is the first set bit of the first
 // non-empty ballot of (key == maximum), slot by slot.  No shuffle of indices
 // and no LDS.
 //
@@ -96,8 +97,23 @@ __device__ __forceinline__ float chosen_weight(float l, int score, int renorm, f
   return live ? s / z : 0.f;
 }
 
-// KEY is float (no bias: the logits) or double (score + bias).
-template <int VPL, bool BF16, typename KEY>
+// Unsigned keys in the order of the values, 0 for a masked one (below the key
+// of every other value); -0 as +0, so that they tie.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return x > -INFINITY ? u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float order_value(uint32_t key) {
+  return key == 0 ? -INFINITY : __uint_as_float(key ^ ((key >> 31) != 0 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ uint64_t order_key(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  return x > -(double)INFINITY ? u ^ ((uint64_t)((int64_t)u >> 63) | (1ull << 63)) : 0ull;
+}
+
+// BIAS: the keys are score + bias in f64 (64-bit keys in two words, the high
+// one compared first); else the logits.
+template <int VPL, bool BF16, bool BIAS>
 __global__ __launch_bounds__(GATE_WAVES * 64) void gate_kernel(const void* __restrict__ logits,
                                                                const float* __restrict__ bias, int32_t T, int32_t E,
                                                                int32_t k, int score, int renorm, float scale,
@@ -112,12 +128,11 @@ __global__ __launch_bounds__(GATE_WAVES * 64) void gate_kernel(const void* __res
     m = row_max(x);
     z = row_exp_sum(x, m);
   }
-  KEY key[VPL];
-  if constexpr (sizeof(KEY) == 8) {
-    double zd = 0.0, md = 0.0;
-    double p[VPL];
+  uint32_t hi[VPL], lo[BIAS ? VPL : 1];
+  if constexpr (BIAS) {
+    double zd = 0.0, p[VPL];
     if (score == 0) {
-      md = (double)row_max(x);
+      const double md = (double)row_max(x);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         p[i] = x[i] > -INFINITY ? ((double)x[i] == md ? 1.0 : exp((double)x[i] - md)) : 0.0;
@@ -129,39 +144,47 @@ __global__ __launch_bounds__(GATE_WAVES * 64) void gate_kernel(const void* __res
     for (int i = 0; i < VPL; ++i) {
       const int e = i * 64 + lane;
       const double s = score == 0 ? p[i] / zd : 1.0 / (1.0 + exp(-(double)x[i]));
-      key[i] = x[i] > -INFINITY ? s + (double)bias[e] : -(double)INFINITY;
-      if (key[i] != key[i]) key[i] = -(double)INFINITY;   // a NaN bias masks its expert
+      // a NaN bias compares false in order_key and masks its expert
+      const uint64_t key = x[i] > -INFINITY ? order_key(s + (double)bias[e]) : 0ull;
+      hi[i] = (uint32_t)(key >> 32);
+      lo[i] = (uint32_t)key;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = x[i];
+    for (int i = 0; i < VPL; ++i) hi[i] = order_key(x[i]);
   }
 
   int my_id = -1;
-  float my_logit = -INFINITY;
+  uint32_t my_key = 0;
   for (int j = 0; j < k; ++j) {
-    KEY best = key[0];
+    uint32_t best = hi[0], low = 0;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) best = key[i] > best ? key[i] : best;
-    best = wave_max(best);
-    if (!(best > -(KEY)INFINITY)) break;   // uniform: nothing is left to choose
-    int e = -1;
-    float l = -INFINITY;
+    for (int i = 1; i < VPL; ++i) best = max(best, hi[i]);
+    best = wave_max_u32(best);
+    if (best == 0) break;   // uniform: nothing is left to choose
+    if constexpr (BIAS) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const uint64_t hit = __ballot(key[i] == best);
-      if (e < 0 && hit != 0) {
-        const int src = __ffsll((unsigned long long)hit) - 1;
-        e = i * 64 + src;
-        l = read_lane(x[i], src);
-        if (lane == src) key[i] = -(KEY)INFINITY;
-      }
+      for (int i = 0; i < VPL; ++i) low = max(low, hi[i] == best ? lo[i] : 0u);
+      low = wave_max_u32(low);
     }
+    int e = 0;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i) {
+      bool is = hi[i] == best;
+      if constexpr (BIAS) is = is && lo[i] == low;
+      const uint64_t hit = __ballot(is);
+      if (hit != 0) e = i * 64 + __ffsll((unsigned long long)hit) - 1;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) hi[i] = e == i * 64 + lane ? 0u : hi[i];
     if (lane == j) {
       my_id = e;
-      my_logit = l;
+      my_key = best;
     }
   }
+  float my_logit;
+  if constexpr (BIAS) my_logit = my_id >= 0 ? load_logit<BF16>(logits, t * E + my_id) : -INFINITY;
+  else my_logit = order_value(my_key);
   const float w = chosen_weight(my_logit, score, renorm, m, z);
   if (lane < k) {
     ids[t * k + lane] = my_id;
@@ -245,11 +268,11 @@ hipError_t launch_topk_gate(const void* logits, int bf16, const float* bias, int
   for_vpl(E, [&](auto v) {
     constexpr int VPL = decltype(v)::value;
     if (bf16) {
-      if (bias) hipLaunchKernelGGL((gate_kernel<VPL, true, double>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
-      else hipLaunchKernelGGL((gate_kernel<VPL, true, float>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
+      if (bias) hipLaunchKernelGGL((gate_kernel<VPL, true, true>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
+      else hipLaunchKernelGGL((gate_kernel<VPL, true, false>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
     } else {
-      if (bias) hipLaunchKernelGGL((gate_kernel<VPL, false, double>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
-      else hipLaunchKernelGGL((gate_kernel<VPL, false, float>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
+      if (bias) hipLaunchKernelGGL((gate_kernel<VPL, false, true>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
+      else hipLaunchKernelGGL((gate_kernel<VPL, false, false>), grid, block, 0, stream, logits, bias, T, E, k, score, renorm, scale, ids, weights);
     }
   });
   return hipGetLastError();

@@ -66,6 +66,16 @@ __device__ __forceinline__ V wave_max(V v) {
   return read_lane(v, 63);
 }
 
+// The same for unsigned integers, where 0 stands in for a lane without a
+// source and each step folds into one v_max_u32.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+#define MOE_STEP(CTRL, ROWS) v = max(v, dpp_or<CTRL, ROWS>(0u, v));
+  MOE_STEP(0x111, 0xF) MOE_STEP(0x112, 0xF) MOE_STEP(0x114, 0xF) MOE_STEP(0x118, 0xF)
+  MOE_STEP(0x142, 0xA) MOE_STEP(0x143, 0xC)
+#undef MOE_STEP
+  return (uint32_t)read_lane((int)v, 63);
+}
+
 template <typename V>
 __device__ __forceinline__ V wave_sum(V v) {
 #define MOE_STEP(CTRL, ROWS) v += dpp_or<CTRL, ROWS>(V(0), v);
