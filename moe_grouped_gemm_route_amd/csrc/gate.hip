@@ -22,10 +22,11 @@
 //     sigma(l) = e^min(l, 0) / (1 + e^-|l|),
 // and the largest chosen min(l, 0) is subtracted in that exponent.
 //
-// Bound by latency: at 4,096 tokens x 256 experts (bf16) the logits are 2 MB,
-// under a microsecond of HBM; the kernel takes 5.8 us (k rounds of a 64-lane
-// reduction one after the other), 6.9 with a bias (f64 exponentials), the
-// gradient 6.7; the call from Python 8.6-9.6, bound by the host.
+// Bound by latency: at 4,096 tokens x 256 experts top-6 the f32 logits are 4
+// MB, under a microsecond of HBM; the kernel takes 5 us (k rounds of a 64-lane
+// reduction one after the other), 9 with a bias (f64 exponentials), the
+// gradient 4.5 to 6; the call from Python 8.6 to 10, bound by the host.  At
+// 16,384 tokens x 1,024 experts top-16: 54 us, the gradient 17 (134 MB).
 #include "common.h"
 #include "launch.h"
 #include "wave.h"
@@ -193,14 +194,18 @@ __global__ __launch_bounds__(GATE_WAVES * 64) void gate_kernel(const void* __res
 }
 
 // dlogits of one token: lane j < k computes the gradient that reaches the
-// logit of its slot, then every lane adds up the slots that chose its
-// experts, in slot order (a repeated id adds twice).
+// logit of its slot; slots of one expert (a repeated id) are added up in slot
+// order by the first of them, which adds the sum to the expert's place in the
+// row.  The row is put together in LDS: with every lane testing every slot
+// against its own experts instead, 16,384 tokens x 1,024 experts top-16 took
+// 33 us.
 template <int VPL, bool BF16>
 __global__ __launch_bounds__(GATE_WAVES * 64) void gate_bwd_kernel(const void* __restrict__ logits,
                                                                    const int32_t* __restrict__ ids,
                                                                    const float* __restrict__ dweights, int32_t T,
                                                                    int32_t E, int32_t k, int score, int renorm,
                                                                    float scale, void* __restrict__ dlogits) {
+  __shared__ float s_row[GATE_WAVES][VPL * 64];
   const int lane = threadIdx.x & 63;
   const int64_t t = blockIdx.x * (int64_t)GATE_WAVES + (threadIdx.x >> 6);
   if (t >= T) return;
@@ -216,12 +221,17 @@ __global__ __launch_bounds__(GATE_WAVES * 64) void gate_bwd_kernel(const void* _
     }
   }
   const bool dense = score == 0 && !renorm;
-  float x[VPL];
+  float p[VPL];              // the row's exponentials (dense), masked ones 0
   float m = -INFINITY, z = 0.f;
   if (dense) {
-    load_row<VPL, BF16>(logits, t, E, x);
-    m = row_max(x);
-    z = row_exp_sum(x, m);
+    load_row<VPL, BF16>(logits, t, E, p);
+    m = row_max(p);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      p[i] = exp_below(p[i], m);
+      z += p[i];
+    }
+    z = wave_sum(z);
   }
   const float w = chosen_weight(l, score, renorm, m, z);
   // a slot that chose nothing (or a masked expert) has weight 0 whatever its
@@ -231,23 +241,27 @@ __global__ __launch_bounds__(GATE_WAVES * 64) void gate_bwd_kernel(const void* _
   const float mean = score == 0 || renorm ? wave_sum(gl * w) : 0.f;
   float d = live ? w * (gl - (dense ? 0.f : mean)) : 0.f;
   if (score == 1 && live) d *= l >= 0.f ? expf(-l) / (1.f + expf(-l)) : 1.f / (1.f + expf(l));   // 1 - sigma
-  float a[VPL];
+  float total = 0.f;
+  bool first = id >= 0;
+  for (int j = 0; j < k; ++j) {
+    const bool same = read_lane(id, j) == id;
+    if (same) total += read_lane(d, j);
+    if (same && j < lane) first = false;
+  }
+  float* row = s_row[threadIdx.x >> 6];
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    a[i] = dense && x[i] > -INFINITY ? -mean * (exp_below(x[i], m) / z) : 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int e = read_lane(id, j);
-    const float dj = read_lane(d, j);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (e == i * 64 + lane) a[i] += dj;
-  }
+    row[i * 64 + lane] = dense && p[i] > 0.f ? -mean * (p[i] / z) : 0.f;
+  __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
+  if (first) row[id] += total;
+  __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = i * 64 + lane;
+    const float a = row[e];
     if (e < E) {
-      if (BF16) reinterpret_cast<uint16_t*>(dlogits)[t * E + e] = f32_to_bf16_rne(a[i]);
-      else reinterpret_cast<float*>(dlogits)[t * E + e] = a[i];
+      if (BF16) reinterpret_cast<uint16_t*>(dlogits)[t * E + e] = f32_to_bf16_rne(a);
+      else reinterpret_cast<float*>(dlogits)[t * E + e] = a;
     }
   }
 }
