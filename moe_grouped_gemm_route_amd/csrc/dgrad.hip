@@ -28,7 +28,7 @@
 // words.
 //
 // What bounds it, measured (one MI355X, 256 experts top-6):
-//   w13 (4,096 x 4,096), 4,096 tokens: 770-800 us, 1.03-1.07 PFLOP/s of useful
+//   w13 (4,096 x 4,096), 4,096 tokens: 762-813 us, 1.01-1.08 PFLOP/s of useful
 //     products (a bf16 library product of 8,192^3 reaches 1.39 on this card,
 //     the forward tiled kernel on the same bands 1.0-1.1).  The matrix pipes
 //     are busy 59 % of the time at 1.9 GHz, LDS 30 %, VALU 44 %; time goes with
@@ -37,14 +37,14 @@
 //   the same at 64 tokens: 287 us, 6.2 TB/s of codes: HBM (6.6 TB/s reads).
 //   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 210 us, 4.6
 //     TB/s: the general decode (twice the instructions) keeps the VALU busy
-//     66 % beside the stream.
+//     73 % and the matrix pipes 16 %.
 //   w13 at 1 token (6 experts): 22 us: the decode of 16 stages a wave, one
 //     after the other, on 192 CUs.
 // Steps that brought it there (w13, 4,096 tokens): one stage, loaded and then
 // computed, 988 us; walks per number of 16-row subtiles, staged one ahead, 915;
 // column groups of a tile on one XCD 881; decode among the matrix instructions
 // 834; direct-to-LDS loads 815; tiles dealt to the XCDs, one convert per bf16
-// pair 788.  Tried and dropped: 512-column workgroups of eight waves (856) or
+// pair 788; wave priorities, empty ranges past the end 766.  Tried and dropped: 512-column workgroups of eight waves (856) or
 // of four waves with 128 columns each (1,249); the largest tiles first (+2 %).
 #include <utility>
 
