@@ -28,15 +28,16 @@
 // words.
 //
 // What bounds it, measured (one MI355X, 256 experts top-6):
-//   w13 (4,096 x 4,096), 4,096 tokens: 762-813 us, 1.01-1.08 PFLOP/s of useful
+//   w13 (4,096 x 4,096), 4,096 tokens: 762-797 us, 1.04-1.08 PFLOP/s of useful
 //     products (a bf16 library product of 8,192^3 reaches 1.39 on this card,
-//     the forward tiled kernel on the same bands 1.0-1.1).  The matrix pipes
-//     are busy 59 % of the time at 1.9 GHz, LDS 30 %, VALU 44 %; time goes with
-//     the power that the code stream, the LDS reads and the decode draw: the
-//     loop without its loads runs in 589 of 815 us, without the decode in 712.
-//   the same at 64 tokens: 287 us, 6.2 TB/s of codes: HBM (6.6 TB/s reads).
-//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 210 us, 4.6
-//     TB/s: the general decode (twice the instructions) keeps the VALU busy
+//     the forward tiled kernel on the same bands 1.0-1.13).  The matrix pipes
+//     are busy 61 % of the time at 1.9 GHz, LDS 31 %, VALU 43 %; time goes with
+//     the power that the code stream, the LDS reads and the decode draw: of 815
+//     us, before the last steps, the loop without its loads ran in 589, without
+//     the decode in 712.
+//   the same at 64 tokens: 282-288 us, 6.2-6.3 TB/s of codes: HBM (6.6 TB/s reads).
+//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 210-222 us,
+//     4.4-4.6 TB/s: the general decode (twice the instructions) keeps the VALU busy
 //     73 % and the matrix pipes 16 %.
 //   w13 at 1 token (6 experts): 22 us: the decode of 16 stages a wave, one
 //     after the other, on 192 CUs.
@@ -44,8 +45,9 @@
 // computed, 988 us; walks per number of 16-row subtiles, staged one ahead, 915;
 // column groups of a tile on one XCD 881; decode among the matrix instructions
 // 834; direct-to-LDS loads 815; tiles dealt to the XCDs, one convert per bf16
-// pair 788; wave priorities, empty ranges past the end 766.  Tried and dropped: 512-column workgroups of eight waves (856) or
-// of four waves with 128 columns each (1,249); the largest tiles first (+2 %).
+// pair 788; wave priorities 801 -> 790, on another card.  Tried and dropped:
+// 512-column workgroups of eight waves (856) or of four waves with 128 columns
+// each (1,249); the largest tiles first (+2 %).
 #include <utility>
 
 #include "common.h"
