@@ -193,6 +193,16 @@ __global__ __launch_bounds__(GATE_WAVES * 64) void gate_kernel(const void* __res
   }
 }
 
+// Between LDS writes of a wave's lanes and reads of them by other lanes of the
+// wave.  The hardware runs one wave's LDS operations in order; the fences keep
+// the compiler from handing a lane's own store on to its later load, past what
+// another lane wrote in between (a wave barrier alone orders no memory).
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // dlogits of one token: lane j < k computes the gradient that reaches the
 // logit of its slot; slots of one expert (a repeated id) are added up in slot
 // order by the first of them, which adds the sum to the expert's place in the
@@ -252,9 +262,9 @@ __global__ __launch_bounds__(GATE_WAVES * 64) void gate_bwd_kernel(const void* _
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
     row[i * 64 + lane] = dense && p[i] > 0.f ? -mean * (p[i] / z) : 0.f;
-  __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
+  wave_lds_sync();
   if (first) row[id] += total;
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_sync();
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = i * 64 + lane;

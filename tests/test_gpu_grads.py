@@ -676,3 +676,18 @@ def test_bf16_rounding_of_every_kind_of_value():
     ok = ~torch.isnan(ref)
     # (0 + -0 is 0 in the sum: compare values)
     assert torch.equal(got[ok], ref[ok])
+
+
+@pytest.mark.parametrize("E", [64, 200, 256, 1000])
+def test_gate_gradient_reaches_experts_of_every_lane(E):
+    # token t's slots name E - 1 - t, E - 2 - t, ...: an expert's place in the
+    # row belongs to another lane than the slot's, each in turn.  Sigmoid
+    # scores without renormalisation at logits 0: dl = g / 4, exactly.
+    k = 8
+    t = torch.arange(E, device=DEV)
+    ids = ((E - 1 - t[:, None] - torch.arange(k, device=DEV)[None]) % E).int()
+    g = torch.randint(1, 100, (E, k), device=DEV, generator=torch.Generator(DEV).manual_seed(E)).float()
+    x = torch.zeros((E, E), device=DEV)
+    ref = torch.zeros((E, E), device=DEV).scatter_(1, ids.long(), g / 4)
+    got = moe.topk_gate_bwd(x, ids, g, score=moe.GATE_SIGMOID, renormalize=False)
+    assert torch.equal(got, ref)
