@@ -377,8 +377,10 @@ def topk_gate(logits, k, score=GATE_SOFTMAX, bias=None, renormalize=True, scale=
         _dev(bias, torch.float32, "bias", 1)
         if bias.numel() != E:
             raise MoeGmmError("bias must have E entries")
-    ids = logits.new_empty((T, max(0, k)), dtype=torch.int32)
-    weights = logits.new_empty((T, max(0, k)), dtype=torch.float32)
+    if not 1 <= k <= E:
+        raise MoeGmmError("k must be 1 to E")
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
     _launch(library().moe_topk_gate, (logits, bias), logits, dt, bias, T, E, k, score,
             int(bool(renormalize)), float(scale), ids, weights)
     return ids, weights

@@ -691,3 +691,11 @@ def test_gate_gradient_reaches_experts_of_every_lane(E):
     ref = torch.zeros((E, E), device=DEV).scatter_(1, ids.long(), g / 4)
     got = moe.topk_gate_bwd(x, ids, g, score=moe.GATE_SIGMOID, renormalize=False)
     assert torch.equal(got, ref)
+
+
+def test_gate_refuses_k_before_it_allocates():
+    # 2^32 + 2 would be 2 to the C entry and its outputs would not fit anywhere
+    x = torch.zeros((1 << 12, 16), device=DEV)
+    for k in (-1, 0, 17, 1 << 30, (1 << 32) + 2):
+        with pytest.raises(moe.MoeGmmError):
+            moe.topk_gate(x, k)
