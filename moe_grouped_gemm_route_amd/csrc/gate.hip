@@ -26,7 +26,8 @@
 // MB, under a microsecond of HBM; the kernel takes 5 us (k rounds of a 64-lane
 // reduction one after the other), 9 with a bias (f64 exponentials), the
 // gradient 4.5 to 6; the call from Python 8.6 to 10, bound by the host.  At
-// 16,384 tokens x 1,024 experts top-16: 54 us, the gradient 17 (134 MB).
+// 16,384 tokens x 1,024 experts top-16 (67 MB): 33 us, bound by the rounds'
+// instructions, the gradient 17 (134 MB).
 #include "common.h"
 #include "launch.h"
 #include "wave.h"
@@ -155,29 +156,62 @@ __global__ __launch_bounds__(GATE_WAVES * 64) void gate_kernel(const void* __res
     for (int i = 0; i < VPL; ++i) hi[i] = order_key(x[i]);
   }
 
+  // Each lane keeps the largest key of every GR of its registers (and among
+  // equal high words the largest low one), so that a round looks at one group
+  // only: the one that holds the chosen key (1,024 experts top-16: 55 -> 33 us; up
+  // to 256 experts there is one group and nothing changes).  q0 and e are the same
+  // in every lane, so the branches on them are scalar.
+  constexpr int GR = VPL < 4 ? VPL : 4, GROUPS = VPL / GR;
+  uint32_t top[GROUPS], top_lo[BIAS ? GROUPS : 1];
+  auto find_top = [&](int q) __attribute__((always_inline)) {
+    uint32_t h = hi[q * GR], l = 0;
+#pragma unroll
+    for (int i = 1; i < GR; ++i) h = max(h, hi[q * GR + i]);
+    top[q] = h;
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int i = 0; i < GR; ++i) l = max(l, hi[q * GR + i] == h ? lo[q * GR + i] : 0u);
+      top_lo[q] = l;
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < GROUPS; ++q) find_top(q);
+
   int my_id = -1;
   uint32_t my_key = 0;
   for (int j = 0; j < k; ++j) {
-    uint32_t best = hi[0], low = 0;
+    uint32_t best = top[0], low = 0;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) best = max(best, hi[i]);
+    for (int q = 1; q < GROUPS; ++q) best = max(best, top[q]);
     best = wave_max_u32(best);
     if (best == 0) break;   // uniform: nothing is left to choose
     if constexpr (BIAS) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) low = max(low, hi[i] == best ? lo[i] : 0u);
+      for (int q = 0; q < GROUPS; ++q) low = max(low, top[q] == best ? top_lo[q] : 0u);
       low = wave_max_u32(low);
+    }
+    int q0 = GROUPS - 1;                       // the lowest group that holds the key
+#pragma unroll
+    for (int q = GROUPS - 2; q >= 0; --q) {
+      bool is = top[q] == best;
+      if constexpr (BIAS) is = is && top_lo[q] == low;
+      if (__ballot(is) != 0) q0 = q;
     }
     int e = 0;
 #pragma unroll
-    for (int i = VPL - 1; i >= 0; --i) {
-      bool is = hi[i] == best;
-      if constexpr (BIAS) is = is && lo[i] == low;
-      const uint64_t hit = __ballot(is);
-      if (hit != 0) e = i * 64 + __ffsll((unsigned long long)hit) - 1;
-    }
+    for (int q = 0; q < GROUPS; ++q) {
+      if (q != q0) continue;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) hi[i] = e == i * 64 + lane ? 0u : hi[i];
+      for (int i = (q + 1) * GR - 1; i >= q * GR; --i) {
+        bool is = hi[i] == best;
+        if constexpr (BIAS) is = is && lo[i] == low;
+        const uint64_t hit = __ballot(is);
+        if (hit != 0) e = i * 64 + __ffsll((unsigned long long)hit) - 1;
+      }
+#pragma unroll
+      for (int i = q * GR; i < (q + 1) * GR; ++i) hi[i] = e == i * 64 + lane ? 0u : hi[i];
+      find_top(q);
+    }
     if (lane == j) {
       my_id = e;
       my_key = best;

@@ -699,3 +699,24 @@ def test_gate_refuses_k_before_it_allocates():
     for k in (-1, 0, 17, 1 << 30, (1 << 32) + 2):
         with pytest.raises(moe.MoeGmmError):
             moe.topk_gate(x, k)
+
+
+@pytest.mark.parametrize("E", [257, 300, 512, 513, 1000, 1024])
+@pytest.mark.parametrize("biased", [False, True])
+def test_gate_chooses_among_ties_of_many_experts(E, biased):
+    # few values, so that most choices are ties over lanes and registers; rows
+    # with 0, 1, 3 and all experts live.  Sums of different values lie 1e-5 and
+    # more apart, far above an ulp of f64: the ids are exact.
+    rng = np.random.default_rng(E)
+    T, k = 67, 64
+    x = rng.choice([-1.0, 0.0, 0.5, 2.0], size=(T, E), p=[0.4, 0.4, 0.19, 0.01])
+    x[:4] = -np.inf
+    x[1, E - 1] = 0.5
+    x[2, [0, E // 2, E - 2]] = 0.5
+    x[3] = 0.0
+    x = dev(x, torch.float32)
+    b = dev(rng.choice([0.0, 0.1, -0.3], size=E), torch.float32) if biased else None
+    for score, code in (("softmax", moe.GATE_SOFTMAX), ("sigmoid", moe.GATE_SIGMOID)):
+        ids, _ = moe.topk_gate(x, k, score=code, bias=b)
+        rid, _ = oracle.topk_gate(f64(x), k, score, None if b is None else f64(b), True, 1.0)
+        assert np.array_equal(ids.cpu().numpy(), rid), (score, E)
