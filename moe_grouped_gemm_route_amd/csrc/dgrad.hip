@@ -99,11 +99,10 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, u32x4_t rsrc, uint32_t 
                  :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory", "m0");
 }
 
-// At most VM vector loads of this wave are still on their way.
-template <int VM>
+// All vector loads of this wave have landed.
 __device__ __forceinline__ void vm_wait() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (15 << 8));
+  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));   // vmcnt 0, expcnt 7, lgkmcnt 15
   asm volatile("" ::: "memory");
 }
 
@@ -335,7 +334,7 @@ struct DgradArgs {
 };
 
 // Ends a stage: this wave's LDS operations are done, then the workgroup
-// barrier.  Vector loads stay on their way (vm_wait counts them).
+// barrier.  Vector loads are vm_wait's.
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4));   // vmcnt 63, expcnt 7, lgkmcnt 0
@@ -349,10 +348,16 @@ __device__ __forceinline__ void lds_barrier() {
 // adds up the partial sums in order.
 //
 // Stages.  All operands go straight to LDS.  While stage i is multiplied, dy
-// of stage i + 1, codes of stage i + CR and scale words of stage i + 3 are
+// of stage i + 1, codes of stage i + 2 and scale words of stage i + 3 are
 // loaded; the operands of stage i + 1 are decoded from its codes, which have
-// landed, and the scale words of stage i + 2 are spread out as f32.
-template <int FMT, int MS, int KB, int CR, int OCC, int NS>
+// landed, and the scale words of stage i + 2 are spread out as f32.  A stage
+// ends when all loads of the wave have landed, then the barrier.  Counted
+// waits that leave the newest loads on their way (with a third stage of codes)
+// gained 1 % at most on large grids and 1.6 us on small ones; direct-to-LDS
+// loads of 4 bytes have been seen on MI355X to land later than such a count
+// said, so nothing here hangs on their order (370,000 runs with counted waits
+// on loads of 16 bytes gave the bits of the full wait).
+template <int FMT, int MS, int KB, int OCC, int NS>
 __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArgs p) {
   constexpr int BM = MS * 16;                            // band rows per workgroup
   constexpr int KCW = KB;                                // chunk columns (128 k) per workgroup
@@ -362,8 +367,7 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   constexpr int H = FMT == 1 ? 2 : 1;                    // scales per 32-block
   constexpr int R_BYTES = DG_BN / 16 * 256;              // scale words: a record per 16 n, one a wave
   constexpr int S_BYTES = H * DG_BN * KCW * 4 * 4;       // the same as f32
-  constexpr int LOADS = A_LOADS + KB + 1;                // per wave and stage
-  constexpr int GROUP_BYTES = 2 * A_BYTES + CR * C_BYTES + 2 * (R_BYTES + S_BYTES);
+  constexpr int GROUP_BYTES = 2 * A_BYTES + 2 * C_BYTES + 3 * R_BYTES + 2 * S_BYTES;
   constexpr int PART_BYTES = DG_WAVES * MS * KB * 2 * 64 * 16;   // a group's accumulators
   static_assert(DG_BN / 16 == DG_WAVES && A_LOADS >= 1, "whole loads per wave");
   static_assert((NS - 1) * PART_BYTES <= NS * GROUP_BYTES, "the partial sums fit the stages");
@@ -374,8 +378,8 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   const int part = NS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (DG_WAVES * 64)) : 0;
   uint8_t* s_dy = s_all + part * GROUP_BYTES;
   uint8_t* s_codes = s_dy + 2 * A_BYTES;
-  uint8_t* s_words = s_codes + CR * C_BYTES;
-  uint8_t* s_scale = s_words + 2 * R_BYTES;
+  uint8_t* s_words = s_codes + 2 * C_BYTES;
+  uint8_t* s_scale = s_words + 3 * R_BYTES;
   const int c16 = lane & 15, g = lane >> 4;
   int nb;
   const BandTile tile = find_tile<BM>(p.off, p.E, p.M, p.NB, nb);
@@ -429,26 +433,26 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
     for (int j = 0; j < A_LOADS; ++j)
       load_lds16<false>(l_dy + (i & 1) * A_BYTES + j * 1024, only_if(live, ar), avo[j], q * DG_BN * 2);
   };
-  auto load_words = [&](int i) {
+  auto load_words = [&](int i, uint32_t slot) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) * (DG_BN / 16) : 0u;
     if (lane < 16)
-      load_lds16<false>(l_words + (i & 1) * R_BYTES, only_if(live, sr), rvo, q * groups * 256);
+      load_lds16<false>(l_words + slot * R_BYTES, only_if(live, sr), rvo, q * groups * 256);
   };
-  auto load_codes = [&](int i, uint32_t slot) {
+  auto load_codes = [&](int i) {
     const bool live = first + i < end;
     const uint32_t q = live ? (uint32_t)(first + i) * (DG_BN / 16) : 0u;
 #pragma unroll
     for (int j = 0; j < KB; ++j)
-      load_lds16<true>(l_codes + slot * C_BYTES + j * 1024, only_if(live, cr), cvo, ((q + j) * KC) << 10);
+      load_lds16<true>(l_codes + (i & 1) * C_BYTES + j * 1024, only_if(live, cr), cvo, ((q + j) * KC) << 10);
   };
   // This wave's scale words of stage i (n = c16 of 16-n block `wave`, k block
   // g of the record's chunk columns), from LDS and back to it as f32,
   // [k block][half][n]; the high halves' n (NVFP4) are turned by 32, so that
   // the lanes of the two halves read different banks (NVFP4 w2 at 128 tokens:
   // 222 -> 216 us).
-  auto scale_word = [&](int i) {
-    return *reinterpret_cast<const uint32_t*>(s_words + (i & 1) * R_BYTES + wave * 256 + lane * 4);
+  auto scale_word = [&](uint32_t slot) {
+    return *reinterpret_cast<const uint32_t*>(s_words + slot * R_BYTES + wave * 256 + lane * 4);
   };
   auto spread_scales = [&](uint32_t w, int i) {
     float* s = reinterpret_cast<float*>(s_scale + (i & 1) * S_BYTES) + wave * 16 + c16;
@@ -474,8 +478,8 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   const uint32_t s_off = (((kcw * 4 + kb0) * H + half) * 64 + g * 8) << 2;
   const uint32_t s_turn = half * 128;
   const uint32_t a_off = c16 * 128 + ((g ^ ((c16 >> 1) & 7)) << 4);
-  auto raw = [&](uint32_t slot, int i, int s, RawWeights (&r)[KB]) {
-    const uint8_t* st = s_codes + slot * C_BYTES;
+  auto raw = [&](int i, int s, RawWeights (&r)[KB]) {
+    const uint8_t* st = s_codes + (i & 1) * C_BYTES;
     const uint8_t* sc = s_scale + (i & 1) * S_BYTES;
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
@@ -488,7 +492,6 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   auto rows = [&](const uint8_t* a, int s, int ms) {
     return *reinterpret_cast<const u32x4_t*>(a + (a_off ^ (s * 64)) + ms * 2048);
   };
-  auto next_slot = [](uint32_t slot) { return slot == CR - 1 ? 0u : slot + 1; };
 
   // The walk of a tile with nsub 16-row subtiles: the operands of a step are
   // decoded among the matrix instructions of the step before.  (Inlined, so
@@ -496,26 +499,23 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
   auto walk = [&](auto any, auto nsub) __attribute__((always_inline)) {
     constexpr bool any_v = decltype(any)::value;
     constexpr int NSUB = decltype(nsub)::value;
-    load_words(0);
-    load_words(1);
-    load_codes(0, 0);
-    load_codes(1, 1);
+    load_words(0, 0);
+    load_words(1, 1);
+    load_words(2, 2);
+    load_codes(0);
+    load_codes(1);
     load_dy(0);
-    vm_wait<0>();
+    vm_wait();
     spread_scales(scale_word(0), 0);
     spread_scales(scale_word(1), 1);
     lds_barrier();
     RawWeights r[KB];
     Weights w[KB], v[KB];
-    raw(0, 0, 0, r);
+    raw(0, 0, r);
     decode_words<any_v, 0, 4 * KB, KB>(r, w);
-    raw(0, 0, 1, r);
-    // stage 2's words take stage 0's place, its f32 scales only after every
-    // wave has read stage 0's
-    load_words(2);
-    if (CR == 3) load_codes(2, 2);
-    lds_barrier();
-    uint32_t sc = 1;                           // codes' LDS slot of stage i + 1
+    raw(0, 1, r);
+    lds_barrier();                             // stage 0's codes and f32 scales make room
+    uint32_t slot = 0;                         // of the scale words: i mod 3
     for (int i = 0; i < steps; ++i) {
       const uint8_t* a = s_dy + (i & 1) * A_BYTES;
       u32x4_t x[2];
@@ -526,28 +526,24 @@ __global__ __launch_bounds__(DG_WAVES * 64 * NS, OCC) void dgrad_kernel(DgradArg
       first_rows(0);
       __builtin_amdgcn_sched_barrier(0);
       load_dy(i + 1);
-      if (CR == 2) load_codes(i + 2, next_slot(sc));
-      load_words(i + 3);
-      if (CR == 3) load_codes(i + 3, next_slot(next_slot(sc)));
+      load_codes(i + 2);
+      load_words(i + 3, slot);
       // the waves at their products before those between stages (128-row tiles:
       // 801 -> 790 us; thin ones lose)
       if (MS == 8) __builtin_amdgcn_s_setprio(1);
       __builtin_amdgcn_sched_barrier(0);
       dgrad_step<any_v, NSUB, MS, KB>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 0, ms); },
-                                  [&] { first_rows(1); raw(sc, i + 1, 0, r); }, w, r, v, acc);
-      vm_wait<LOADS>();                        // all but this stage's loads have landed
-      const uint32_t word = scale_word(i + 2);
+                                  [&] { first_rows(1); raw(i + 1, 0, r); }, w, r, v, acc);
+      const uint32_t word = scale_word(slot == 0 ? 2 : slot - 1);
       dgrad_step<any_v, NSUB, MS, KB>(std::make_integer_sequence<int, NSUB>{}, x, [&](int ms) { return rows(a, 1, ms); },
-                                  [&] { raw(sc, i + 1, 1, r); }, v, r, w, acc);
+                                  [&] { raw(i + 1, 1, r); }, v, r, w, acc);
       __builtin_amdgcn_sched_barrier(0);
       if (MS == 8) __builtin_amdgcn_s_setprio(0);
       spread_scales(word, i + 2);
-      // dy of the next stage has landed, and (CR 2) codes of the one after
-      vm_wait<CR == 3 ? KB + 1 : 1>();
+      vm_wait();
       lds_barrier();
-      sc = next_slot(sc);
+      slot = slot == 2 ? 0 : slot + 1;
     }
-    vm_wait<0>();
   };
   auto walk_any = [&](auto any) __attribute__((always_inline)) {
     const int nsub = (tile.rows + 15) >> 4;
@@ -706,12 +702,8 @@ int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M) { return dgrad_plan(E,
 
 template <int FMT, int MS, int KB, int OCC, int NS>
 static void launch_dgrad_t(DgradArgs a, int64_t groups, hipStream_t stream) {
-  // three stages of codes; two for NVFP4's 32-row tiles, whose f32 scales take
-  // twice the LDS, so that four groups of waves still fit a CU (w2 at 256
-  // tokens 222 -> 210 us)
-  constexpr int CR = FMT == 1 && MS == 2 ? 2 : 3;
   a.NB = (int)((a.L.K + 128 * KB - 1) / (128 * KB));
-  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, KB, CR, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0,
+  hipLaunchKernelGGL((dgrad_kernel<FMT, MS, KB, OCC, NS>), dim3((unsigned)groups), dim3(DG_WAVES * 64 * NS), 0,
                      stream, a);
 }
 

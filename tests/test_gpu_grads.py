@@ -720,3 +720,24 @@ def test_gate_chooses_among_ties_of_many_experts(E, biased):
         ids, _ = moe.topk_gate(x, k, score=code, bias=b)
         rid, _ = oracle.topk_gate(f64(x), k, score, None if b is None else f64(b), True, 1.0)
         assert np.array_equal(ids.cpu().numpy(), rid), (score, E)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("T,k,N,K", [(700, 4, 320, 1024), (1024, 16, 512, 256)])
+def test_dgrad_many_thin_tiles_stay_right_call_after_call(T, k, N, K, fmt):
+    # 1,024 experts with bands of 0 to 40 rows: short walks, many tiles a CU,
+    # operands that arrive late if any do
+    E = 1024
+    rng = np.random.default_rng(T)
+    off, M = bands(rng.multinomial(T * k, rng.dirichlet(np.full(E, 2.0))))
+    w, packed = make_weights(E, N, K, fmt, seed=T + K)
+    bits = random_dy(M, N, seed=K)
+    dy64 = bf16_bits_to_f64(bits)
+    enum = moe.MXFP4 if fmt == "mxfp4" else moe.NVFP4
+    d, o = to_dev(bits), to_dev(off)
+    first = moe.moe_gmm_dgrad(packed, enum, E, N, K, d, o, M)
+    close(f64(first), oracle.gmm_dgrad(dy64, off, w), dgrad_bound(dy64, off, w, N), torch.float32)
+    other = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(200):
+        other += (moe.moe_gmm_dgrad(packed, enum, E, N, K, d, o, M) != first).sum()
+    assert int(other) == 0
