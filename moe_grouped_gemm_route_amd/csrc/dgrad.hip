@@ -28,18 +28,18 @@
 // words.
 //
 // What bounds it, measured (one MI355X, 256 experts top-6):
-//   w13 (4,096 x 4,096), 4,096 tokens: 762-797 us, 1.04-1.08 PFLOP/s of useful
+//   w13 (4,096 x 4,096), 4,096 tokens: 764-798 us, 1.03-1.08 PFLOP/s of useful
 //     products (a bf16 library product of 8,192^3 reaches 1.39 on this card,
 //     the forward tiled kernel on the same bands 1.0-1.13).  The matrix pipes
-//     are busy 61 % of the time at 1.9 GHz, LDS 31 %, VALU 43 %; time goes with
+//     are busy 61 % of the time at 1.9 GHz, LDS 31 %, VALU 44 %; time goes with
 //     the power that the code stream, the LDS reads and the decode draw: of 815
 //     us, before the last steps, the loop without its loads ran in 589, without
 //     the decode in 712.
-//   the same at 64 tokens: 282-288 us, 6.2-6.3 TB/s of codes: HBM (6.6 TB/s reads).
-//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 210-222 us,
-//     4.4-4.6 TB/s: the general decode (twice the instructions) keeps the VALU busy
+//   the same at 64 tokens: 284-288 us, 6.2-6.3 TB/s of codes: HBM (6.6 TB/s reads).
+//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 207-216 us,
+//     4.5-4.7 TB/s: the general decode (twice the instructions) keeps the VALU busy
 //     73 % and the matrix pipes 16 %.
-//   w13 at 1 token (6 experts): 22 us: the decode of 16 stages a wave, one
+//   w13 at 1 token (6 experts): 23 us: the decode of 16 stages a wave, one
 //     after the other, on 192 CUs.
 // Steps that brought it there (w13, 4,096 tokens): one stage, loaded and then
 // computed, 988 us; walks per number of 16-row subtiles, staged one ahead, 915;
