@@ -86,17 +86,24 @@ __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) { return (uint32_
 // compiler, which cannot tell the stages apart, does not make every LDS read
 // wait for every such load; vm_wait does the waiting.  NT: non-temporal, for
 // the codes, which are read once.
+//
+// A vector memory instruction may read a scalar register only 5 wait states
+// after a vector instruction wrote it, which the hardware does not see to and
+// the compiler does not either around an asm statement.  The v_readfirstlane
+// of uniform() are such writes and can come directly before, so the statement
+// holds the whole distance itself (s_nop 4 is 5 wait states; it also covers
+// the 1 after the write of M0, which the compiler places).
 template <bool NT>
 __device__ __forceinline__ void load_lds16(uint32_t lds, u32x4_t rsrc, uint32_t lane_off, uint32_t off) {
   lds = uniform(lds);
   off = uniform(off);
   rsrc = u32x4_t{uniform(rsrc[0]), uniform(rsrc[1]), uniform(rsrc[2]), 0x00020000u};
   if (NT)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
-                 :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory", "m0");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                 :: "{m0}"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory", "m0");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "{m0}"(lds), "v"(lane_off), "s"(rsrc), "s"(off) : "memory");
 }
 
 // All vector loads of this wave have landed.
