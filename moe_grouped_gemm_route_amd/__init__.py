@@ -337,9 +337,9 @@ def _float(t, name, ndim):
 
 def _out(out, shape, dtype, name, like):
     """out checked, or a new tensor beside `like`; dtype is an F32/BF16 enum or
-    a torch dtype."""
+    its torch dtype."""
     dtype = _OUT.get(dtype, dtype)
-    if not isinstance(dtype, torch.dtype):
+    if dtype not in _FLOATS:
         raise MoeGmmError("the type of %s must be F32 or BF16" % name)
     if out is None:
         return like.new_empty(shape, dtype=dtype)
