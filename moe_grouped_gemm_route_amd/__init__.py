@@ -171,7 +171,7 @@ def route_sort(topk_ids, E, ws=None):
 
 def packed_weight_bytes(fmt, E, N, K):
     n = library().moe_packed_weight_bytes(fmt, E, N, K)
-    if n == 0:
+    if n == 0 or (fmt | E | N | K) >> 31:   # (ctypes passes the low 32 bits)
         raise MoeGmmError("unsupported weight shape E=%d N=%d K=%d" % (E, N, K))
     return n
 
@@ -322,7 +322,8 @@ def moe_combine(y, topk_weights, pair_row, out_dtype=F32):
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 _OUT = {F32: torch.float32, BF16: torch.bfloat16}
-_SCALARS = {int, float, type(None)}
+_Tensor = torch.Tensor
+_I32_MIN, _I32_MAX = -(1 << 31), (1 << 31) - 1
 
 
 def _float(t, name, ndim):
@@ -349,15 +350,22 @@ def _out(out, shape, dtype, name, like):
     return out
 
 
+def _too_wide(a):
+    """A whole number that the C entry's int32 does not hold (ctypes would pass
+    its low 32 bits)."""
+    raise MoeGmmError("%d does not fit 32 bits" % a)
+
+
 def _launch(fn, tensors, *args):
     """fn(*args, stream) on the device that holds every tensor of tensors (None
     skipped), on that device's current stream.  A tensor in args stands for its
-    pointer."""
+    pointer; whole numbers are int32."""
     index = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise MoeGmmError("the tensors must be on one device, got %s and %s" % (tensors[0].device, t.device))
-    args = [a if type(a) in _SCALARS or not isinstance(a, torch.Tensor) else a.data_ptr() for a in args]
+    args = [(a if _I32_MIN <= a <= _I32_MAX else _too_wide(a)) if type(a) is int else
+            a.data_ptr() if isinstance(a, _Tensor) else a for a in args]
     if index == torch.cuda.current_device():
         status = fn(*args, _raw_stream(index))
     else:
@@ -469,7 +477,7 @@ def silu_mul(y, group_offsets=None, out_dtype=F32, out=None):
         _dev(group_offsets, torch.int32, "group_offsets", 1)
         if group_offsets.numel() < 2:
             raise MoeGmmError("group_offsets must have E+1 entries")
-        n_rows = group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1)
+        n_rows = _vp(group_offsets.data_ptr() + 4 * (group_offsets.numel() - 1))
     h = _out(out, (M, N // 2), out_dtype, "out", y)
     _launch(library().moe_silu_mul, (y, group_offsets, h), y, dt, M, N, n_rows, h, _FLOATS[h.dtype])
     return h

@@ -25,3 +25,19 @@ def test_output_types_other_than_f32_and_bf16_are_refused():
     with pytest.raises(moe.MoeGmmError):
         moe.silu_mul(x, out_dtype=torch.float16, out=torch.zeros((4, 4), dtype=torch.float16, device=DEV))
     assert moe.silu_mul(x, out_dtype=torch.bfloat16).dtype == torch.bfloat16
+
+
+def test_sizes_past_32_bits_are_refused():
+    # 2^32 + 8 columns (8 GiB, never touched) are not 8 columns, and 2^32 is not enum 0
+    N = (1 << 32) + 8
+    x = torch.empty((1, N), dtype=torch.bfloat16, device=DEV)
+    pr = torch.zeros(1, dtype=torch.int32, device=DEV)
+    w = torch.ones((1, 1), device=DEV)
+    logits = torch.zeros((2, 8), device=DEV)
+    ids, lw = moe.topk_gate(logits, 2)
+    for call in (lambda: moe.moe_dispatch(x, pr, 1), lambda: moe.moe_dispatch_bwd(x, pr, 1, out_dtype=moe.BF16),
+                 lambda: moe.moe_combine_bwd(x, x, w, pr, out_dtype=moe.BF16),
+                 lambda: moe.silu_mul(x, out_dtype=moe.BF16), lambda: moe.topk_gate(logits, 2, score=1 << 32),
+                 lambda: moe.topk_gate_bwd(logits, ids, lw, score=(1 << 32) + 1)):
+        with pytest.raises(moe.MoeGmmError):
+            call()
