@@ -375,10 +375,13 @@ int moe_combine(const void* y, int y_dtype, const float* topk_weights,
  * ones by ascending index.  Without a bias the logits are compared
  * themselves; with one the sums are compared in f64.
  *   topk_weights[t, j] = scale * s_ej / (renorm ? sum of the chosen s : 1)
- * in f32.  A logit that is -inf or NaN (or an expert whose bias is -inf or
- * NaN) masks its expert for that token: it is never chosen and adds nothing to a
- * softmax.  Where fewer than k experts are left, the remaining slots get id
- * -1 and weight 0; moe_route_sort drops such pairs (and counts them).
+ * in f32.  A logit that is -inf or NaN masks its expert for that token: it is
+ * never chosen and adds nothing to a softmax.  An expert whose bias is -inf or
+ * NaN is never chosen either, but the bias steers the choice alone: the
+ * expert's score stays in the softmax of every token, forward and in the
+ * gradient (which takes no bias).  Where fewer than k experts are left, the
+ * remaining slots get id -1 and weight 0; moe_route_sort drops such pairs (and
+ * counts them).
  *
  * logits         [T, E] f32 or bf16 (dtype).
  * bias           [E] float or NULL.
