@@ -108,6 +108,8 @@ def test_the_check_itself():
     assert run(*first, "s_nop 0", load) == {4}
     assert run(*first, "s_nop 2", load) == {4} and run(*first, "s_nop 3", load) == set()
     assert run("s_mov_b32 m0, s4", load) == {2} and run("s_mov_b32 m0, s4", "s_nop 0", load) == set()
+    fly = functions("f:\n" + load + "\ns_waitcnt vmcnt(1)\ns_barrier\ns_waitcnt vmcnt(0)\ns_barrier\n.Lfunc_end0:")[0]
+    assert loads_at_barriers(fly) == {3}
     assert run("v_cmp_eq_u32_e64 s[2:3], v0, v1", "s_nop 3", load) == {3}
     # around a loop: the write stands behind the load
     assert run(".LBB0_1:", load, "v_readfirstlane_b32 s20, v0", "s_cbranch_scc1 .LBB0_1", "s_endpgm") == {2}
@@ -115,11 +117,42 @@ def test_the_check_itself():
     assert run("v_readfirstlane_b32 s21, v0", "s_mov_b32 s21, s9", "s_mov_b32 m0, s4", "s_nop 0", load) == set()
 
 
-@pytest.mark.parametrize("source", ["dgrad.hip"])
-def test_loads_wait_for_their_scalar_operands(source, tmp_path):
-    out = str(tmp_path / "k.s")
+def loads_at_barriers(body):
+    """Indices of the barriers that some path reaches with a direct-to-LDS load
+    on its way: one after which no s_waitcnt vmcnt(0) has come."""
+    at = {label: i for i, (label, _, _) in enumerate(body) if label}
+    seen, work, bad = set(), [(0, False)], set()
+    while work:
+        i, flying = work.pop()
+        if i >= len(body) or (i, flying) in seen:
+            continue
+        seen.add((i, flying))
+        label, name, ops = body[i]
+        goes = [i + 1]
+        if name:
+            text = " ".join(ops)
+            if name.startswith("buffer_load") and " lds" in " " + text:
+                flying = True
+            elif name == "s_waitcnt" and "vmcnt(0)" in text:
+                flying = False
+            elif name == "s_barrier" and flying:
+                bad.add(i)
+            if name in ("s_endpgm", "s_setpc_b64"):
+                goes = []
+            elif name == "s_branch":
+                goes = [at[ops[0]]]
+            elif name.startswith("s_cbranch"):
+                goes.append(at[ops[0]])
+        work.extend((j, flying) for j in goes)
+    return bad
+
+
+@pytest.fixture(scope="module", params=["dgrad.hip"])
+def kernels(request, tmp_path_factory):
+    """The functions of a source as the build compiles it."""
+    out = str(tmp_path_factory.mktemp("asm") / "k.s")
     cmd = [build.hipcc()] + build.FLAGS + ["-x", "hip", "-S", "--cuda-device-only",
-                                           os.path.join(build.CSRC, source), "-o", out]
+                                           os.path.join(build.CSRC, request.param), "-o", out]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     # M0 in a clobber list is a register that the compiler does not promise to keep
@@ -129,5 +162,14 @@ def test_loads_wait_for_their_scalar_operands(source, tmp_path):
     loads = sum(name is not None and name.startswith("buffer_load") and "lds" in " ".join(ops)
                 for b in bodies for _, name, ops in b)
     assert len(bodies) >= 12 and loads > 0
-    early = [(k, " ".join([b[i][1]] + b[i][2])) for k, b in enumerate(bodies) for i in sorted(short_waits(b))]
-    assert not early, "%d of %d too early: %s" % (len(early), loads, early[:3])
+    return bodies
+
+
+def test_loads_wait_for_their_scalar_operands(kernels):
+    early = [(k, " ".join([b[i][1]] + b[i][2])) for k, b in enumerate(kernels) for i in sorted(short_waits(b))]
+    assert not early, "%d too early: %s" % (len(early), early[:3])
+
+
+def test_no_load_is_on_its_way_at_a_barrier(kernels):
+    assert sum(name == "s_barrier" for b in kernels for _, name, _ in b) > 0
+    assert [(k, i) for k, b in enumerate(kernels) for i in sorted(loads_at_barriers(b))] == []
