@@ -458,6 +458,9 @@ int moe_dispatch_bwd(const void* dxs, int dxs_dtype, const int32_t* pair_row, in
  *
  * dout           [T, N] f32 or bf16 (dout_dtype).
  * y              [rows, N] f32 or bf16 (y_dtype), as given to moe_combine.
+ * pair_row       [T*k] int32; its entries in [0, rows) are distinct, as
+ *                moe_route_sort's are (a row that two pairs name would be
+ *                written twice, with either pair's gradient left in it).
  * topk_weights   [T, k] float.
  * dy             out [rows, N] f32 or bf16 (dy_dtype).
  * dweights       out [T, k] float.
@@ -515,7 +518,7 @@ int moe_silu_mul(const void* y, int y_dtype, int32_t M, int32_t N, const int32_t
  * of 24, 64 below 72, 128 above; packed 256-byte, dy, preact and dx 16-byte
  * aligned.
  * Equal calls return equal bits.  The order of the f32 sums over n depends on
- * fmt, E, K and M (few rows share n between waves), not on the offsets.
+ * E, N, K and M (few rows share n between waves), not on the offsets.
  */
 int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, const uint16_t* dy,
                   const int32_t* group_offsets, int32_t M, const void* preact, int preact_dtype,

@@ -419,9 +419,9 @@ def _pairs(pair_row, k):
 
 
 def moe_dispatch(x, pair_row, k, out=None):
-    """moe_dispatch.  x [T, N] float32 or bfloat16, pair_row [T*k] int32 ->
-    xs [T*k, N] of x's type (or out, [rows, N]); rows no pair names are left
-    as they were."""
+    """moe_dispatch.  x [T, N] float32 or bfloat16, pair_row [T*k] int32 (no
+    row twice) -> xs [T*k, N] of x's type (or out, [rows, N]); rows no pair
+    names are left as they were."""
     dt = _float(x, "x", 2)
     T, N = x.shape
     if _pairs(pair_row, k) != T:
@@ -449,9 +449,9 @@ def moe_dispatch_bwd(dxs, pair_row, k, out_dtype=F32):
 
 def moe_combine_bwd(dout, y, topk_weights, pair_row, out_dtype=F32, out=None):
     """moe_combine_bwd.  dout [T, N] and y [rows, N] float32 or bfloat16,
-    topk_weights [T, k] float32, pair_row [T*k] int32 -> (dy [rows, N],
-    dweights [T, k] float32).  out: a [rows, N] tensor for dy whose rows no
-    pair names are left as they were."""
+    topk_weights [T, k] float32, pair_row [T*k] int32 (no row twice) ->
+    (dy [rows, N], dweights [T, k] float32).  out: a [rows, N] tensor for dy
+    whose rows no pair names are left as they were."""
     gdt = _float(dout, "dout", 2)
     ydt = _float(y, "y", 2)
     _dev(topk_weights, torch.float32, "topk_weights", 2)
