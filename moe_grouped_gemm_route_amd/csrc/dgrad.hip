@@ -28,19 +28,23 @@
 // words.
 //
 // What bounds it, measured (one MI355X, 256 experts top-6):
-//   w13 (4,096 x 4,096), 4,096 tokens: 764-798 us, 1.03-1.08 PFLOP/s of useful
+//   w13 (4,096 x 4,096), 4,096 tokens: 772-797 us, 1.03-1.07 PFLOP/s of useful
 //     products (a bf16 library product of 8,192^3 reaches 1.39 on this card,
-//     the forward tiled kernel on the same bands 1.0-1.13).  The matrix pipes
-//     are busy 61 % of the time at 1.9 GHz, LDS 31 %, VALU 44 %; time goes with
-//     the power that the code stream, the LDS reads and the decode draw: of 815
-//     us, before the last steps, the loop without its loads ran in 589, without
-//     the decode in 712.
-//   the same at 64 tokens: 284-288 us, 6.2-6.3 TB/s of codes: HBM (6.6 TB/s reads).
-//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 207-216 us,
+//     the forward tiled kernel on the same bands, in turn, 731 us to 773).  The
+//     matrix pipes are busy 61 % of the time at 1.9 GHz, LDS 30 %, VALU 44 %;
+//     time goes with the power that the code stream, the LDS reads and the
+//     decode draw: of 815 us, before the last steps, the loop without its loads
+//     ran in 589, without the decode in 712.
+//   the same at 64 tokens: 288-299 us, 6.0-6.2 TB/s of codes: HBM (6.6 TB/s reads).
+//   w2 (4,096 x 2,048) NVFP4 with general scales, 256 tokens Zipf: 209-214 us,
 //     4.5-4.7 TB/s: the general decode (twice the instructions) keeps the VALU busy
-//     73 % and the matrix pipes 16 %.
-//   w13 at 1 token (6 experts): 23 us: the decode of 16 stages a wave, one
-//     after the other, on 192 CUs.
+//     74 % and the matrix pipes 16 %.
+//   w13 at 1 token (6 experts): 23.4 us on 192 CUs, one workgroup each, of which
+//     the loads take 7 (16.5 without them) and the decode 1 (22.8; 14.8 without
+//     both): a stage ends when the loads that it issued itself have landed, 16
+//     times one after the other, and nothing else on the CU covers that.  32
+//     experts of 1,024 x 1,024, 256 tokens top-4: 17.3 us, 13.0 without the
+//     loads, 17.0 without the decode.
 // Steps that brought it there (w13, 4,096 tokens): one stage, loaded and then
 // computed, 988 us; walks per number of 16-row subtiles, staged one ahead, 915;
 // column groups of a tile on one XCD 881; decode among the matrix instructions
@@ -682,9 +686,10 @@ struct DgradPlan {
 static DgradPlan dgrad_plan(int32_t E, int32_t K, int32_t M) {
   DgradPlan pl;
   // By the mean band: 32-row tiles up to 24 rows (w13, 4,096 x 4,096, at 24
-  // rows a band: 439 us against 463 with 64-row tiles), 64-row tiles to 72
-  // (at 48: 563 against 787 with 32 and 642 with 128), then 128 (at 96: 830
-  // against 1,034 with 64).
+  // rows a band: 429 us against 442 with 64-row tiles), 64-row tiles to 72
+  // (at 48: 544 against 802 with 32 and 604 with 128), then 128 (at 96: 775
+  // against 1,034 with 64).  Those are of uniform routing; with Zipf routing
+  // the choice at 24 rows costs 4 % (w2, 4,096 x 2,048: 290 against 277).
   pl.subtiles = (int64_t)M <= 24 * (int64_t)E ? 2 : (int64_t)M < 72 * (int64_t)E ? 4 : 8;
   const int64_t tiles = (int64_t)M / (16 * pl.subtiles) + (E < M ? E : M);
   pl.blocks = 2;

@@ -23,11 +23,13 @@
 // and the largest chosen min(l, 0) is subtracted in that exponent.
 //
 // Bound by latency: at 4,096 tokens x 256 experts top-6 the f32 logits are 4
-// MB, under a microsecond of HBM; the kernel takes 5 us (k rounds of a 64-lane
-// reduction one after the other), 9 with a bias (f64 exponentials), the
-// gradient 4.5 to 6; the call from Python 8.6 to 10, bound by the host.  At
-// 16,384 tokens x 1,024 experts top-16 (67 MB): 33 us, bound by the rounds'
-// instructions, the gradient 17 (134 MB).
+// MB, under a microsecond of HBM; the kernel takes 5.2 us (k rounds of a
+// 64-lane reduction one after the other), 9.0 with a bias (f64 exponentials),
+// the gradient 4.6, or 6.1 where every expert has one (softmax, not
+// renormalised); a call from Python takes 8.1 to 9.9, bound by the host.  At
+// 16,384 tokens x 1,024 experts top-16 (67 MB, 13 us at the copy rate): 33 us,
+// the instructions of 16 rounds of which each serves one token, and the
+// gradient 17 (134 MB).
 #include "common.h"
 #include "launch.h"
 #include "wave.h"

@@ -16,10 +16,11 @@
 // (24,576 x 4,096: 53.2 -> 49.3 us), but not in moe_combine_bwd, whose k waves
 // of a token share its dout row (92 -> 103 us).
 //
-// Measured, bf16, 4,096 tokens top-6, 4,096 columns: dispatch 39 us for 235 MB
-// (6.0 TB/s; a copy of 1 GiB runs at 5.2 on this card), combine_bwd 90 us for
-// 437 MB (4.8), silu_mul 49 us for 302 MB (6.2); dispatch_bwd of f32 rows,
-// 1,237 tokens top-8, 2,560 columns, 19 us for 108 MB (5.6).
+// Measured, bf16, 4,096 tokens top-6, 4,096 columns: dispatch 39-40 us for 235
+// MB (5.9-6.0 TB/s; a torch copy of 1 GiB runs at 5.2 on this card, reads alone
+// at 6.6), combine_bwd 86-90 us for 437 MB (4.9-5.1), silu_mul 49-50 us for 302
+// MB (6.1); dispatch_bwd of f32 rows, 1,237 tokens top-8, 2,560 columns, 19 us
+// for 108 MB (5.6).
 #include "common.h"
 #include "launch.h"
 #include "wave.h"

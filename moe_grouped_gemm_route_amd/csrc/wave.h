@@ -21,8 +21,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 
-// f(a) with a's neighbour as the DPP control CTRL moves it; lanes without a
-// source keep a (the reductions below only use idempotent or masked steps).
+// v of the lane that the DPP control CTRL names; `other` in lanes that have no
+// such source or whose row ROWS leaves out.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp_or(uint32_t other, uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)other, (int)v, CTRL, ROWS, 0xF, false);

@@ -148,6 +148,8 @@ def test_gate_gradient_of_masked_rows_is_zero_or_finite():
         assert not bool(d[3].any())
 
 
+# (the differences of this test are of the oracle's float64 weights;
+# test_gpu_gate_difference takes those of the weights that the GPU returns)
 def test_gate_gradient_is_the_difference():
     # differences of the GPU's own weights (f32: a step of 2^-5 keeps their
     # rounding, 2^-20, and the third-order term, h^2/6 times a third derivative
@@ -406,7 +408,7 @@ def test_dgrad_every_band_size(rows):
 
 
 # grids that take each way of sharing the work: 128- and 256-column
-# workgroups, n walked by four (three, NVFP4), two or one group of waves, and
+# workgroups, n walked by four, two or one group of waves, and
 # 32-, 64- and 128-row tiles; n of one stage, of fewer stages than groups, and
 # of a number no group count divides
 @pytest.mark.parametrize("E,K,rows", [(6, 896, 2), (40, 1024, 1), (100, 1024, 1), (210, 1024, 1), (30, 896, 7),
