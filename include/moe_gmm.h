@@ -525,6 +525,109 @@ int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, 
                   void* dx, int dx_dtype, int act, void* stream);
 
 /*
+ * moe_w4_gemv - a few rows times 4-bit integer weights with group scales.
+ *
+ * The format of integer-quantized checkpoints, for the dense projections and
+ * the shared expert beside the routed ones, and for routed experts at a handful
+ * of tokens (no sort, no pack: the weights are read as they lie).
+ *   W[n, k] = scales[n, k/group] * (code[n, k] - zeros[n, k/group])
+ * The integer differences and the bf16 activations are multiplied exactly; a
+ * group's sum (the codes' and the zero point's part), its product with the scale
+ * and the sum over the groups are f32.  No weight is rounded.
+ *
+ *   topk_ids NULL   y[t, :] = W x[t, :].  E and k must be 1, x_rows = T.
+ *   topk_ids        a row per pair p = t*k + j with e = topk_ids[p]:
+ *                     y[p, :] = W_e x[r, :], r = t where x_rows = T, p where
+ *                     x_rows = T*k.  A pair whose id is outside [0, E) gives a
+ *                     row of zeros.
+ *   topk_weights    with topk_ids: a row per token, summed over its pairs,
+ *                     y[t, :] = sum_j topk_weights[p] * W_e x[r, :]; a pair
+ *                     whose id is outside [0, E) adds nothing, whatever its
+ *                     weight holds.
+ *   act             MOE_ACT_SILU_MUL: rows of N/2, silu(y[:, :N/2]) *
+ *                     y[:, N/2:] of the f32 sums (not with topk_weights:
+ *                     MOE_ERR_UNSUPPORTED).
+ *
+ * codes          [E, N, K/2] uint8: two codes 0 .. 15 per byte, the even K index
+ *                in the low nibble.
+ * scales         [E, N, K/group] f32 or bf16 (scale_dtype).
+ * zeros          [E, N, K/group] uint8 zero points (any byte), or NULL: 8.
+ * group          32, 64, 128 or 256.
+ * x              [x_rows, K] bf16, finite.  (An infinity or NaN makes its row of
+ *                y NaN; other rows do not change.)
+ * topk_ids       [T, k] int32, as moe_topk_gate gives them.
+ * topk_weights   [T, k] float, finite.
+ * y              out, f32 or bf16 (RNE).
+ * Every row is written, whatever T; equal calls return equal bits.  The order of
+ * the f32 sums depends on the sizes and on the form, not on the values.  Meant
+ * for few rows: a dense call reads the weights once per 16 to 64 rows, a routed
+ * one once per pair.
+ * Limits: N <= 2^30, K <= 2^30, K % group == 0, N even with the activation,
+ * E*N*K/2 < 2^40, T <= 2^24, 1 <= k <= 64, T*k <= 2^24; codes and x 16-byte
+ * aligned, scales and y to their type; a grid of rows * N/16 <= 8,388,607.
+ */
+int moe_w4_gemv(const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros, int32_t group,
+                int32_t E, int32_t N, int32_t K, const uint16_t* x, int32_t x_rows, int32_t T,
+                const int32_t* topk_ids, const float* topk_weights, int32_t k, void* y, int y_dtype, int act,
+                void* stream);
+
+/*
+ * moe_gate_up - the dense gated block beside the routed experts (the shared
+ * expert, a dense layer), bf16 weights: both projections, the activation and
+ * the product in one kernel.
+ *   out = x w13^T [M, N],  h[:, j] = silu(out[:, j]) * out[:, N/2 + j]
+ * with silu(z) = z / (1 + e^-z); sums f32, the activation of the f32 sums.
+ *
+ * x              [M, K] bf16.
+ * w13            [N, K] bf16: the N/2 gate rows, then the N/2 up rows.
+ * h              out [M, N/2] f32 or bf16 (h_dtype; RNE).
+ * preact         out [M, N] f32 or bf16 (preact_dtype), may be NULL: the sums,
+ *                gate columns first, as moe_gate_up_bwd and moe_silu_mul take them.
+ * Limits: M <= 2^24, N % 16 == 0, K % 8 == 0, N and K <= 4,194,048,
+ * M*N and M*K < 2^40, M/64 * N/64 and M/64 * K/128 <= 4,194,303; every pointer
+ * 16-byte aligned.
+ * The order of the f32 sums depends on M, N and K.
+ */
+int moe_gate_up(const uint16_t* x, const uint16_t* w13, int32_t M, int32_t N, int32_t K, void* h, int h_dtype,
+                void* preact, int preact_dtype, void* stream);
+
+/*
+ * moe_gate_up_bwd - gradients of moe_gate_up.  With g and u the column halves of
+ * preact and s = 1 / (1 + e^-g):
+ *   d    = [ dh u s (1 + g (1 - s)),  dh g s ]        [M, N]
+ *   dx   = d w13                                      [M, K]
+ *   dw13 = d^T x                                      [N, K]
+ * d is computed in f32.  For a bf16 result it is the product's operand rounded
+ * to bf16 (half a step, as the result's own rounding); for an f32 result it is
+ * kept as the sum of three bf16 values, 24 bits, at three times the products.
+ * (A |d| past the largest bf16, 3.39e38, counts as infinite.)  Sums f32, in a
+ * fixed order; no atomics.
+ *
+ * dh             [M, N/2] f32 or bf16 (dh_dtype).
+ * x, w13         as given to moe_gate_up; x may be NULL without dw13, w13 without
+ *                dx.
+ * preact         [M, N] f32 or bf16 (preact_dtype), as moe_gate_up kept it.
+ * dx             out [M, K] f32 or bf16 (dx_dtype; RNE), or NULL.
+ * dw13           out [N, K] f32 or bf16 (dw_dtype; RNE), or NULL; not both NULL.
+ * ws, ws_bytes   caller-owned device workspace of at least
+ *                moe_gate_up_bwd_workspace_bytes(...) bytes, 256-byte aligned; it
+ *                holds d and the shares of dx's sums, needs no clearing and may
+ *                be reused once the stream has passed this call.
+ * Limits and alignment as moe_gate_up.
+ */
+int moe_gate_up_bwd(const void* dh, int dh_dtype, const uint16_t* x, const uint16_t* w13, const void* preact,
+                    int preact_dtype, int32_t M, int32_t N, int32_t K, void* dx, int dx_dtype, void* dw13,
+                    int dw_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_gate_up_bwd_workspace_bytes - bytes of device workspace that
+ * moe_gate_up_bwd needs (want_dx, want_dw: whether dx and dw13 are given).  0 for
+ * sizes and types that it rejects.
+ */
+size_t moe_gate_up_bwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int want_dx, int dx_dtype, int want_dw,
+                                       int dw_dtype);
+
+/*
  * moe_mxfp4_to_nvfp4 - the lossless MXFP4 -> NVFP4 scale cast.
  *
  * Source: "DeepSeek-V4-Flash-0731-NVFP4", section "The lossless weight cast":

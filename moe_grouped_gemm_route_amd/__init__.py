@@ -20,6 +20,7 @@ __all__ = [
     "mxfp4_quantize", "moe_gmm_w4a4",
     "GATE_SOFTMAX", "GATE_SIGMOID", "topk_gate", "topk_gate_bwd", "moe_dispatch", "moe_dispatch_bwd",
     "moe_combine_bwd", "silu_mul", "moe_gmm_dgrad",
+    "w4_gemv", "gate_up", "gate_up_bwd", "gate_up_bwd_workspace_bytes",
 ]
 
 MXFP4, NVFP4, W_BF16 = 0, 1, 2
@@ -63,6 +64,13 @@ _SIGNATURES = {
     "moe_silu_mul": (ctypes.c_int, [_vp, ctypes.c_int, _i32, _i32, _vp, _vp, ctypes.c_int, _vp]),
     "moe_gmm_dgrad": (ctypes.c_int, [_vp, ctypes.c_int, _i32, _i32, _i32, _vp, _vp, _i32, _vp, ctypes.c_int, _vp,
                                      ctypes.c_int, ctypes.c_int, _vp]),
+    "moe_w4_gemv": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _vp, _vp,
+                                   _i32, _vp, ctypes.c_int, ctypes.c_int, _vp]),
+    "moe_gate_up": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp]),
+    "moe_gate_up_bwd": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, _i32, _i32, _i32, _vp,
+                                       ctypes.c_int, _vp, ctypes.c_int, _vp, _sz, _vp]),
+    "moe_gate_up_bwd_workspace_bytes": (_sz, [_i32, _i32, _i32, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                              ctypes.c_int]),
     "moe_debug_decode": (ctypes.c_int, [_vp, ctypes.c_int, _i32, _i32, _i32, _vp, _vp]),
     "moe_calib_mfma_bf16": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _vp]),
     "moe_calib_hbm_read": (ctypes.c_int, [_vp, _sz, _i32, _vp, _vp]),
@@ -506,6 +514,109 @@ def moe_gmm_dgrad(packed, fmt, E, N, K, dy, group_offsets, M, out_dtype=F32, act
     _launch(library().moe_gmm_dgrad, (packed, db, group_offsets, preact, dx), packed, fmt, E, N, K, db,
             group_offsets, M, preact, pdt, dx, _FLOATS[dx.dtype], act)
     return dx
+
+
+def w4_gemv(codes, scales, x, zeros=None, topk_ids=None, topk_weights=None, out_dtype=F32, act=ACT_NONE, out=None):
+    """moe_w4_gemv: a few rows times 4-bit integer weights with group scales.
+    Dense: codes [N, K/2] uint8, scales [N, K/G] float32 or bfloat16, zeros
+    [N, K/G] uint8 or None (8 everywhere), x bf16 [T, K] -> y [T, N].
+    With topk_ids [T, k] int32: codes [E, N, K/2], scales and zeros [E, N, K/G],
+    x [T, K] or [T*k, K] -> y [T*k, N], a row per pair (zeros for an id outside
+    [0, E)); with topk_weights [T, k] float32 -> y [T, N], a token's rows summed.
+    act=ACT_SILU_MUL: N/2 columns (not with topk_weights)."""
+    routed = topk_ids is not None
+    _dev(codes, torch.uint8, "codes", 3 if routed else 2)
+    sdt = _float(scales, "scales", 3 if routed else 2)
+    xb = _bits16(x, "x")
+    if xb.dim() != 2:
+        raise MoeGmmError("x must be [rows, K]")
+    N, K2 = codes.shape[-2:]
+    rows, K = xb.shape
+    groups = scales.shape[-1]
+    if K != 2 * K2 or scales.shape[:-1] != codes.shape[:-1] or groups < 1 or K % groups:
+        raise MoeGmmError("codes must be [.., N, K/2] and scales [.., N, K/G] for x [rows, K]")
+    if zeros is not None:
+        _dev(zeros, torch.uint8, "zeros", scales.dim())
+        if zeros.shape != scales.shape:
+            raise MoeGmmError("zeros must have the shape of scales")
+    E, T, k, out_rows = 1, rows, 1, rows
+    if routed:
+        _dev(topk_ids, torch.int32, "topk_ids", 2)
+        E = codes.shape[0]
+        T, k = topk_ids.shape
+        out_rows = T * k
+        if rows != T and rows != T * k:
+            raise MoeGmmError("x must have T or T*k rows")
+    if topk_weights is not None:
+        if not routed:
+            raise MoeGmmError("topk_weights go with topk_ids")
+        _dev(topk_weights, torch.float32, "topk_weights", 2)
+        if topk_weights.shape != topk_ids.shape:
+            raise MoeGmmError("topk_weights must be [T, k]")
+        out_rows = T
+    y = _out(out, (out_rows, N // 2 if act == ACT_SILU_MUL else N), out_dtype, "out", scales)
+    _launch(library().moe_w4_gemv, (codes, scales, zeros, xb, topk_ids, topk_weights, y), codes, scales, sdt, zeros,
+            K // groups, E, N, K, xb, rows, T, topk_ids, topk_weights, k, y, _FLOATS[y.dtype], act)
+    return y
+
+
+def _gate_up_shapes(x, w13):
+    """x [M, K] and w13 [N, K] bf16 checked, as 16-bit views."""
+    xb, wb = _bits16(x, "x"), _bits16(w13, "w13")
+    if xb.dim() != 2 or wb.dim() != 2 or xb.shape[1] != wb.shape[1] or wb.shape[0] % 2:
+        raise MoeGmmError("x must be [M, K] and w13 [N, K] with N even")
+    return xb, wb
+
+
+def gate_up(x, w13, out_dtype=F32, preact_dtype=None, out=None, preact=None):
+    """moe_gate_up.  x bf16 [M, K], w13 bf16 [N, K] (gate rows, then up rows) ->
+    h [M, N/2]; with preact_dtype (F32 or BF16), or a preact tensor [M, N] to
+    write, (h, preact): the sums that gate_up_bwd takes."""
+    xb, wb = _gate_up_shapes(x, w13)
+    M, K = xb.shape
+    N = wb.shape[0]
+    h = _out(out, (M, N // 2), out_dtype, "out", xb)
+    if preact is not None or preact_dtype is not None:
+        preact = _out(preact, (M, N), preact.dtype if preact_dtype is None else preact_dtype, "preact", xb)
+    _launch(library().moe_gate_up, (xb, wb, h, preact), xb, wb, M, N, K, h, _FLOATS[h.dtype], preact,
+            F32 if preact is None else _FLOATS[preact.dtype])
+    return h if preact is None else (h, preact)
+
+
+def gate_up_bwd_workspace_bytes(M, N, K, dx_dtype=F32, dw_dtype=F32):
+    """moe_gate_up_bwd_workspace_bytes; a dtype of None: that gradient is not
+    wanted."""
+    if (M | N | K) >> 31:   # (ctypes passes the low 32 bits)
+        return 0
+    return int(library().moe_gate_up_bwd_workspace_bytes(M, N, K, dx_dtype is not None, dx_dtype or 0,
+                                                         dw_dtype is not None, dw_dtype or 0))
+
+
+def gate_up_bwd(dh, x, w13, preact, dx_dtype=F32, dw_dtype=F32, dx=None, dw13=None, ws=None):
+    """moe_gate_up_bwd.  dh [M, N/2] float32 or bfloat16, x and w13 as given to
+    gate_up, the preact it kept -> (dx [M, K], dw13 [N, K]); a dtype of None
+    leaves that gradient out (None in its place).  dx, dw13: tensors to write.
+    ws: a device tensor of at least gate_up_bwd_workspace_bytes, or None to
+    allocate one."""
+    hdt = _float(dh, "dh", 2)
+    pdt = _float(preact, "preact", 2)
+    xb, wb = _gate_up_shapes(x, w13)
+    M, K = xb.shape
+    N = wb.shape[0]
+    if tuple(dh.shape) != (M, N // 2) or tuple(preact.shape) != (M, N):
+        raise MoeGmmError("dh must be [M, N/2] and preact [M, N]")
+    if dx is not None or dx_dtype is not None:
+        dx = _out(dx, (M, K), dx_dtype if dx is None else dx.dtype, "dx", xb)
+    if dw13 is not None or dw_dtype is not None:
+        dw13 = _out(dw13, (N, K), dw_dtype if dw13 is None else dw13.dtype, "dw13", xb)
+    xdt, wdt = (None if t is None else _FLOATS[t.dtype] for t in (dx, dw13))
+    if ws is None:
+        ws = xb.new_empty(max(gate_up_bwd_workspace_bytes(M, N, K, xdt, wdt), 1), dtype=torch.uint8)
+    elif not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise MoeGmmError("ws must be a contiguous CUDA (HIP) tensor")
+    _launch(library().moe_gate_up_bwd, (dh, xb, wb, preact, dx, dw13, ws), dh, hdt, xb, wb, preact, pdt, M, N, K, dx,
+            xdt or 0, dw13, wdt or 0, ws, _sz(ws.numel() * ws.element_size()))
+    return dx, dw13
 
 
 def mxfp4_to_nvfp4(scales):

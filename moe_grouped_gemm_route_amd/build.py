@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoegmm.so")
 
 SOURCES = ["api.cpp", "route_sort.hip", "encode.hip", "gmm.hip", "combine.hip", "gate.hip", "permute.hip", "dgrad.hip",
-           "calib.hip"]
+           "w4.hip", "gateup.hip", "calib.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

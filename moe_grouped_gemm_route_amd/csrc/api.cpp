@@ -66,6 +66,18 @@ int permute_shape(int32_t T, int32_t k, int32_t N, int32_t rows) {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+// Sizes of the dense gate/up block: whole 16-byte words of bf16 in every row of
+// every matrix, and a tile's 256 rows addressed with 32-bit byte offsets below
+// the lane offset that reads zeros.
+int gate_up_shape(int32_t M, int32_t N, int32_t K) {
+  if (M < 1 || M > kMaxRows || N < 16 || N % 16 != 0 || K < 8 || K % 8 != 0) return MOE_ERR_SHAPE;
+  if ((int64_t)N * 512 > 0x7FFE0000ll || (int64_t)K * 512 > 0x7FFE0000ll) return MOE_ERR_SHAPE;
+  if ((int64_t)M * N >= (int64_t(1) << 40) || (int64_t)M * K >= (int64_t(1) << 40)) return MOE_ERR_SHAPE;
+  // workgroups of up to 1,024 work-items, 16 shares of a sum at most
+  if (moe::gate_up_workgroups(M, N, K) > kMaxWorkgroups / 4) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -340,6 +352,74 @@ int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, 
   return hip_status(moe::launch_dgrad(static_cast<const uint8_t*>(packed), fmt, E, N, K, dy, group_offsets, M, preact,
                                       preact_dtype == MOE_BF16, dx, dx_dtype == MOE_BF16,
                                       static_cast<hipStream_t>(stream)));
+}
+
+int moe_w4_gemv(const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros, int32_t group,
+                int32_t E, int32_t N, int32_t K, const uint16_t* x, int32_t x_rows, int32_t T, const int32_t* topk_ids,
+                const float* topk_weights, int32_t k, void* y, int y_dtype, int act, void* stream) {
+  if (!dtype_ok(scale_dtype) || !dtype_ok(y_dtype)) return MOE_ERR_FORMAT;
+  if (act != MOE_ACT_NONE && act != MOE_ACT_SILU_MUL) return MOE_ERR_FORMAT;
+  if (!codes || !scales || !x || !y) return MOE_ERR_NULL;
+  if (topk_weights && !topk_ids) return MOE_ERR_NULL;
+  // a sum of activations is not the activation of a sum
+  if (topk_weights && act != MOE_ACT_NONE) return MOE_ERR_UNSUPPORTED;
+  if (group != 32 && group != 64 && group != 128 && group != 256) return MOE_ERR_SHAPE;
+  if (E < 1 || N < 1 || N > kMaxCols || K < 1 || K > kMaxCols || K % group != 0) return MOE_ERR_SHAPE;
+  if ((int64_t)N * (K / 2) >= kMaxCodeBytes / E) return MOE_ERR_SHAPE;
+  if (act == MOE_ACT_SILU_MUL && N % 2 != 0) return MOE_ERR_SHAPE;
+  if (T < 1 || T > kMaxRows) return MOE_ERR_SHAPE;
+  if (topk_ids) {
+    if (k < 1 || k > 64 || (int64_t)T * k > kMaxRows) return MOE_ERR_SHAPE;
+    // the chunks of a token's experts are counted in 32 bits
+    if ((int64_t)k * (K / 32) > (int64_t(1) << 30)) return MOE_ERR_SHAPE;
+    if (x_rows != T && x_rows != (int64_t)T * k) return MOE_ERR_SHAPE;
+  } else if (E != 1 || k != 1 || x_rows != T) {
+    return MOE_ERR_SHAPE;
+  }
+  if (!aligned16(codes) || !aligned16(x) || ((uintptr_t)scales & (scale_dtype == MOE_BF16 ? 1 : 3)))
+    return MOE_ERR_SHAPE;
+  if (((uintptr_t)y & (y_dtype == MOE_BF16 ? 1 : 3))) return MOE_ERR_SHAPE;
+  // workgroups of up to 512 work-items
+  if (moe::w4_workgroups(N, group, T, k, topk_ids != nullptr, topk_weights != nullptr, act) > kMaxWorkgroups / 2)
+    return MOE_ERR_SHAPE;
+  return hip_status(moe::launch_w4_gemv(codes, scales, scale_dtype == MOE_BF16, zeros, group, E, N, K, x, x_rows != T,
+                                        T, topk_ids, topk_weights, k, y, y_dtype == MOE_BF16, act,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int moe_gate_up(const uint16_t* x, const uint16_t* w13, int32_t M, int32_t N, int32_t K, void* h, int h_dtype,
+                void* preact, int preact_dtype, void* stream) {
+  if (!dtype_ok(h_dtype) || (preact && !dtype_ok(preact_dtype))) return MOE_ERR_FORMAT;
+  if (!x || !w13 || !h) return MOE_ERR_NULL;
+  const int st = gate_up_shape(M, N, K);
+  if (st != MOE_OK) return st;
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(h) || !aligned16(preact)) return MOE_ERR_SHAPE;
+  return hip_status(moe::launch_gate_up(x, w13, M, N, K, h, h_dtype == MOE_BF16, preact, preact_dtype == MOE_BF16,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_gate_up_bwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int want_dx, int dx_dtype, int want_dw,
+                                       int dw_dtype) {
+  if (gate_up_shape(M, N, K) != MOE_OK || !(want_dx || want_dw)) return 0;
+  if ((want_dx && !dtype_ok(dx_dtype)) || (want_dw && !dtype_ok(dw_dtype))) return 0;
+  return (size_t)moe::gate_up_bwd_ws(M, N, K, want_dx != 0, dx_dtype == MOE_BF16, want_dw != 0, dw_dtype == MOE_BF16);
+}
+
+int moe_gate_up_bwd(const void* dh, int dh_dtype, const uint16_t* x, const uint16_t* w13, const void* preact,
+                    int preact_dtype, int32_t M, int32_t N, int32_t K, void* dx, int dx_dtype, void* dw13,
+                    int dw_dtype, void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dh_dtype) || !dtype_ok(preact_dtype)) return MOE_ERR_FORMAT;
+  if ((dx && !dtype_ok(dx_dtype)) || (dw13 && !dtype_ok(dw_dtype))) return MOE_ERR_FORMAT;
+  if (!dh || !preact || !ws || !(dx || dw13) || (dx && !w13) || (dw13 && !x)) return MOE_ERR_NULL;
+  const int st = gate_up_shape(M, N, K);
+  if (st != MOE_OK) return st;
+  if (!aligned16(dh) || !aligned16(preact) || !aligned16(x) || !aligned16(w13) || !aligned16(dx) || !aligned16(dw13))
+    return MOE_ERR_SHAPE;
+  const size_t need = moe_gate_up_bwd_workspace_bytes(M, N, K, dx != nullptr, dx_dtype, dw13 != nullptr, dw_dtype);
+  if (ws_bytes < need || ((uintptr_t)ws & 255)) return MOE_ERR_SHAPE;
+  return hip_status(moe::launch_gate_up_bwd(dh, dh_dtype == MOE_BF16, x, w13, preact, preact_dtype == MOE_BF16, M, N,
+                                            K, dx, dx_dtype == MOE_BF16, dw13, dw_dtype == MOE_BF16, ws,
+                                            static_cast<hipStream_t>(stream)));
 }
 
 int moe_mxfp4_to_nvfp4(const uint8_t* scales, int32_t E, int32_t N, int32_t K,

@@ -1,0 +1,716 @@
+// moe_gate_up and moe_gate_up_bwd: the gated feed-forward block of the tokens'
+// shared expert (or of a dense layer), bf16 weights [N, K] with the gate rows
+// first and the up rows behind them:
+//     [g u] = x w13^T,   h = silu(g) u,   silu(z) = z / (1 + e^-z),
+// and backwards, with s = 1 / (1 + e^-g),
+//     dg = dh u s (1 + g (1 - s)),   du = dh g s,   d = [dg du],
+//     dx = d w13,   dw13 = d^T x.
+//
+// All three products run on one tile kernel, out[i, j] = sum_r A(i, r) B(j, r)
+// on bf16 MFMA with f32 sums.  An operand lies in memory either with r
+// contiguous (x and w13 forwards, d for dx) or with r as the row (w13 for dx;
+// d and x for dw13); the second kind goes to LDS as it lies and is transposed
+// by the reads (ds_read_b64_tr_b16), so nothing is transposed in memory.
+#include "common.h"
+#include "launch.h"
+#include "lds_load.h"
+#include "wave.h"
+
+namespace moe {
+
+constexpr int GU_BK = 64;      // r per stage
+constexpr int GU_CUS = 256;
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t* lds_i16x4_t;
+
+__device__ __forceinline__ f32x4_t gu_mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                 0, 0, 0);
+}
+
+__device__ __forceinline__ float gu_silu(float z) { return z / (1.0f + __expf(-z)); }
+
+__device__ __forceinline__ void gu_store8(void* p, bool bf16, int64_t i, const float (&v)[8]) {
+  if (bf16) {
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  } else {
+    float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The tile kernel
+// ---------------------------------------------------------------------------
+
+struct TileArgs {
+  const uint16_t* a;       // r contiguous: [I, lda]; r as the row: [R, lda]
+  const uint16_t* b;       // likewise with J
+  int64_t lda, ldb;
+  int I, J, R;             // J: columns of out (with GATE: of h)
+  int parts;               // A is the sum of this many matrices, part_stride apart
+  int64_t part_stride;
+  int splits, steps;       // shares of the sum over r, and stages of a share
+  int tiles_i, tiles_j;
+  void* out;               // [I, J]; with splits > 1 f32 [splits, I, J]
+  int out_bf16;
+  void* pre;               // GATE: [I, 2J] sums, or NULL
+  int pre_bf16;
+};
+
+// One operand's tile of DIM rows (or columns) x 64 r in LDS, DIM * 128 bytes.
+//
+// r contiguous: rows of 128 bytes, 16-byte segment c of row q at place
+// c ^ swizzle(q), so that the eight lanes that are served together read eight
+// different segments of the 128 bytes that their rows share in the banks.
+// r as the row: rows of DIM * 2 bytes, segment c of row r at c ^ 4 (r & 3), so
+// that the four rows of a transposing read lie in different 64-byte quarters.
+//
+// The columns of out that two neighbouring 16-column subtiles (PAIR: the B
+// operand) cover are dealt so that a lane's results are eight consecutive ones:
+// subtile s, row q of the operand is column (q >> 2) * 8 + s * 4 + (q & 3) of
+// the pair's 32.
+template <bool RROW, int DIM, int WAVES, bool PAIR>
+struct Operand {
+  static constexpr int BYTES = DIM * GU_BK * 2;
+  static constexpr int LOADS = BYTES / 1024 / WAVES;        // 1 KiB loads of a wave
+  static constexpr int SEGS = RROW ? DIM / 8 : GU_BK / 8;   // 16-byte segments of an LDS row
+  static constexpr int ROWS = 64 / SEGS;                    // LDS rows of a load
+  static_assert(LOADS >= 1 && LOADS * WAVES * 1024 == BYTES, "whole loads per wave");
+  static_assert(!RROW || (DIM >= 128 && DIM <= 512), "rows of 256 bytes at least, a load per two rows at most");
+
+  static __device__ __forceinline__ int swizzle(int row) {
+    return RROW ? (row & 3) << 2 : PAIR ? (row & 3) | ((row >> 3) & 1) << 2 : row & 7;
+  }
+  // LDS row and source segment of this lane in load j of a wave
+  static __device__ __forceinline__ int row(int wave, int j) {
+    return (wave * LOADS + j) * ROWS + (threadIdx.x & 63) / SEGS;
+  }
+  static __device__ __forceinline__ int seg(int row) { return ((threadIdx.x & 63) % SEGS) ^ swizzle(row); }
+
+  // The MFMA operand of 32 r (step ks) and 16 rows: subtile `sub` of the wave's
+  // `base`; lane l holds row l & 15, r = 8 (l >> 4) .. + 7.
+  static __device__ __forceinline__ u32x4_t read(const uint8_t* tile, int base, int sub, int ks) {
+    const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
+    if constexpr (!RROW) {
+      const int r = base + (PAIR ? (sub >> 1) * 32 + (q >> 2) * 8 + (sub & 1) * 4 + (q & 3) : sub * 16 + q);
+      return *reinterpret_cast<const u32x4_t*>(tile + r * 128 + (((ks * 4 + g) ^ swizzle(r)) << 4));
+    } else {
+      // 16 lanes read four r of 16 columns, lane q four columns of row q / 4,
+      // and get one column's four r
+      const int piece = q & 3;
+      const int seg = base / 8 + (PAIR ? (sub >> 1) * 4 + piece : sub * 2 + (piece >> 1));
+      const int half = PAIR ? sub & 1 : piece & 1;
+      u32x4_t v;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = ks * 32 + g * 8 + h * 4 + (q >> 2);
+        const uint8_t* at = tile + r * (DIM * 2) + ((seg ^ swizzle(r)) << 4) + half * 8;
+        const uint2 w = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)at));
+        v[2 * h] = w.x;
+        v[2 * h + 1] = w.y;
+      }
+      return v;
+    }
+  }
+};
+
+// Tile t of the grid, or of a share of it: tiles are dealt to the 8 XCDs
+// (workgroup ids go round them) in contiguous runs, which walk bands of four
+// tile rows column by column, so that the workgroups that run together on an
+// XCD share rows of both operands in its L2.
+__device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& i, int& j) {
+  const int x = id & 7, k = id >> 3;
+  const int per = tiles >> 3, rest = tiles & 7;
+  const int t = x * per + min(x, rest) + k;
+  const int band = t / (4 * tj), in = t - band * 4 * tj;
+  const int h = min(4, ti - band * 4);
+  j = in / h;
+  i = band * 4 + in - j * h;
+}
+
+// WI x WJ waves of SI x SJ 16 x 16 subtiles each, KG such groups of waves that
+// take every KG-th 64 r; two stages.
+//
+// The walk.  A stage's 2 SI operand groups (one A subtile, SJ matrix
+// instructions) run in order; operands are read from LDS two groups ahead.
+// The last quarter of the groups has all of its operands in registers, and the
+// barrier stands before it: there every wave has read the stage to the end and
+// the next stage has landed.  Behind the barrier the loads of the stage after
+// next start into the buffer just read, the next stage's first operands are
+// read, and the last quarter's matrix instructions cover both.  So a stage's
+// loads have a whole stage to land in, and the matrix pipes do not run dry at
+// the barrier.  The wait before it is a full one: direct-to-LDS loads are not
+// counted as still on their way.
+template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, bool GATE, int OCC>
+__global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArgs p) {
+  constexpr int NW = WI * WJ;
+  constexpr int BM = WI * SI * 16, BN = WJ * SJ * 16;
+  typedef Operand<AROW, BM, NW, false> OpA;
+  typedef Operand<BROW, BN, NW, true> OpB;
+  constexpr int SLICE = OpA::BYTES + OpB::BYTES;
+  constexpr int STAGE = KG * SLICE;
+  constexpr int JOIN = (KG - 1) * BM * BN * 4;
+  constexpr int LDS = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
+  static_assert(!GATE || SJ == 4, "a wave holds a pair of gate and a pair of up subtiles");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_all[LDS];
+
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = KG > 1 ? wid / NW : 0;
+  const int wave = wid % NW;
+  const int wi = wave / WJ, wj = wave % WJ;
+
+  const int tiles = p.tiles_i * p.tiles_j;
+  const int split = blockIdx.x / (uint32_t)tiles;
+  int ti, tj;
+  tile_of(blockIdx.x - split * tiles, tiles, p.tiles_i, p.tiles_j, ti, tj);
+  const int i0 = ti * BM;
+  const int j0 = tj * (GATE ? BN / 2 : BN);
+
+  // Source offsets of this lane's loads from the tile's base; lanes outside the
+  // matrix read zeros.
+  uint32_t avo[OpA::LOADS], bvo[OpB::LOADS];
+  int aseg[OpA::LOADS], bseg[OpB::LOADS];
+#pragma unroll
+  for (int j = 0; j < OpA::LOADS; ++j) {
+    const int row = OpA::row(wave, j), seg = OpA::seg(row);
+    aseg[j] = seg * 8;
+    if (AROW) avo[j] = i0 + seg * 8 < p.I ? (uint32_t)(row * p.lda * 2) + seg * 16 : kLaneOob;
+    else avo[j] = i0 + row < p.I ? (uint32_t)(row * p.lda * 2) + seg * 16 : kLaneOob;
+  }
+  bool up[OpB::LOADS];             // GATE: the load's rows are up rows
+#pragma unroll
+  for (int j = 0; j < OpB::LOADS; ++j) {
+    const int row = OpB::row(wave, j), seg = OpB::seg(row);
+    bseg[j] = seg * 8;
+    up[j] = false;
+    if (BROW) {
+      bvo[j] = j0 + seg * 8 < p.J ? (uint32_t)(row * p.ldb * 2) + seg * 16 : kLaneOob;
+    } else if (GATE) {
+      // pairs of 32 rows: gate, up, gate, up ...; a load's eight rows lie in one
+      const int pair = row >> 5, col = (pair >> 1) * 32 + (row & 31);
+      up[j] = (((wave * OpB::LOADS + j) * OpB::ROWS) >> 5) & 1;
+      bvo[j] = j0 + col < p.J ? (uint32_t)(col * p.ldb * 2) + seg * 16 : kLaneOob;
+    } else {
+      bvo[j] = j0 + row < p.J ? (uint32_t)(row * p.ldb * 2) + seg * 16 : kLaneOob;
+    }
+  }
+
+  // The stages of this group: r of `parts` matrices one after the other, each
+  // padded to whole stages; the group's next is KG stages on.
+  const int per_part = (p.R + GU_BK - 1) / GU_BK;
+  int part, at;                     // next stage to load: its part, and stage in it
+  {
+    const int s = split * p.steps * KG + kg;
+    part = s / per_part;
+    at = s - part * per_part;
+  }
+  const uint32_t l0 = lds_addr(s_all) + kg * SLICE;
+  const uint32_t range_a = AROW ? 0 : 0x7FFE0000u;   // lanes outside are marked: the range need not end anywhere
+  auto load = [&](int buf, auto a_or_b) __attribute__((always_inline)) {
+    constexpr bool B = decltype(a_or_b)::value;
+    const bool live = part < p.parts;
+    const int r0 = at * GU_BK;
+    const int left = p.R - r0;      // r of the stage that exist, or more
+    if constexpr (!B) {
+      const uint16_t* base = p.a + part * p.part_stride;
+      base += AROW ? (int64_t)r0 * p.lda + i0 : (int64_t)i0 * p.lda + r0;
+      const uint32_t bytes = AROW ? (uint32_t)((min(left, GU_BK) * p.lda - i0) * 2) : range_a;
+      const u32x4_t rs = only_if(live, make_rsrc(live ? base : p.a, bytes));
+#pragma unroll
+      for (int j = 0; j < OpA::LOADS; ++j) {
+        const uint32_t vo = AROW || aseg[j] < left ? avo[j] : kLaneOob;
+        load_lds16<false>(l0 + buf * STAGE + (wave * OpA::LOADS + j) * 1024, rs, vo, 0);
+      }
+    } else {
+      const uint16_t* base = p.b + (BROW ? (int64_t)r0 * p.ldb + j0 : (int64_t)j0 * p.ldb + r0);
+      const uint32_t bytes = BROW ? (uint32_t)((min(left, GU_BK) * p.ldb - j0) * 2) : 0x7FFE0000u;
+      const u32x4_t rs = only_if(live, make_rsrc(live ? base : p.b, bytes));
+      const u32x4_t ru = GATE ? only_if(live, make_rsrc(live ? base + (int64_t)p.J * p.ldb : p.b, bytes)) : rs;
+#pragma unroll
+      for (int j = 0; j < OpB::LOADS; ++j) {
+        const uint32_t vo = BROW || bseg[j] < left ? bvo[j] : kLaneOob;
+        load_lds16<false>(l0 + buf * STAGE + OpA::BYTES + (wave * OpB::LOADS + j) * 1024, up[j] ? ru : rs, vo, 0);
+      }
+    }
+  };
+  auto advance = [&] {
+    at += KG;
+    while (at >= per_part) {
+      at -= per_part;
+      ++part;
+    }
+  };
+  auto load_stage = [&](int buf) __attribute__((always_inline)) {
+    load(buf, std::false_type{});
+    load(buf, std::true_type{});
+    advance();
+  };
+
+  f32x4_t acc[SI][SJ];
+#pragma unroll
+  for (int a = 0; a < SI; ++a)
+#pragma unroll
+    for (int s = 0; s < SJ; ++s) acc[a][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  constexpr int NQ = 2 * SI;                       // operand groups of a stage
+  constexpr int HOLD = NQ >= 4 ? NQ / 4 : 1;       // behind the barrier
+  constexpr int CA = SI >= 2 ? 2 : 1;              // A operands read a stage ahead
+  u32x4_t fa[NQ], fb[2][SJ];
+  auto read_a = [&](int buf, int q) __attribute__((always_inline)) {
+    fa[q] = OpA::read(s_all + buf * STAGE + kg * SLICE, wi * SI * 16, q % SI, q / SI);
+  };
+  auto read_b = [&](int buf, int ks, int s) __attribute__((always_inline)) {
+    fb[ks][s] = OpB::read(s_all + buf * STAGE + kg * SLICE + OpA::BYTES, wj * SJ * 16, s, ks);
+  };
+  auto mults = [&](int q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < SJ; ++s) acc[q % SI][s] = gu_mfma(fb[q / SI][s], fa[q], acc[q % SI][s]);
+  };
+
+  const int steps = p.steps;
+  load_stage(0);
+  load_stage(1);
+  vm_wait();
+  lds_barrier();
+#pragma unroll
+  for (int s = 0; s < SJ; ++s) read_b(0, 0, s);
+#pragma unroll
+  for (int q = 0; q < CA; ++q) read_a(0, q);
+
+#pragma unroll 1
+  for (int st = 0; st < steps; ++st) {
+    const int buf = st & 1;
+    // reads in the order of need: A of the first half and B of the second
+    // between them, then A of the second; two a group
+    constexpr int READS = NQ - CA + SJ;
+    int done = 0;
+#pragma unroll
+    for (int q = 0; q < NQ - HOLD; ++q) {
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int FRONT = SI - CA;               // A reads of the first half
+      const int upto = q == NQ - HOLD - 1 ? READS : (READS * (q + 1) + NQ - HOLD - 1) / (NQ - HOLD);
+#pragma unroll
+      for (int k = 0; k < READS; ++k) {
+        if (k < done || k >= upto) continue;
+        constexpr int MIX = FRONT < SJ ? FRONT : SJ;
+        if (k < 2 * MIX) {
+          if (k & 1) read_b(buf, 1, k >> 1);
+          else read_a(buf, CA + (k >> 1));
+        } else {
+          const int rest = k - 2 * MIX;            // one of the two is done
+          if (FRONT > SJ) read_a(buf, CA + MIX + rest);
+          else if (rest < SJ - MIX) read_b(buf, 1, MIX + rest);
+          else read_a(buf, SI + rest - (SJ - MIX));
+        }
+      }
+      done = upto;
+      mults(q);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    vm_wait();
+    lds_barrier();
+    u32x4_t na[CA], nb[SJ];
+    {
+      const uint8_t* nx = s_all + (buf ^ 1) * STAGE + kg * SLICE;
+#pragma unroll
+      for (int s = 0; s < SJ; ++s) nb[s] = OpB::read(nx + OpA::BYTES, wj * SJ * 16, s, 0);
+#pragma unroll
+      for (int q = 0; q < CA; ++q) na[q] = OpA::read(nx, wi * SI * 16, q, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = NQ - HOLD; q < NQ; ++q) {
+      mults(q);
+      __builtin_amdgcn_sched_barrier(0);
+      if (q == NQ - HOLD) {
+        load(buf, std::false_type{});
+        if (HOLD == 1) load(buf, std::true_type{});
+      }
+      if (q == NQ - HOLD + 1) load(buf, std::true_type{});
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    advance();
+#pragma unroll
+    for (int s = 0; s < SJ; ++s) fb[0][s] = nb[s];
+#pragma unroll
+    for (int q = 0; q < CA; ++q) fa[q] = na[q];
+  }
+  vm_wait();    // the loads past the last stage land before LDS is used again
+
+  if constexpr (KG > 1) {
+    lds_barrier();
+    f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_all) + wave * SI * SJ * 64 + lane;
+    constexpr int GROUP = NW * SI * SJ * 64;
+    if (kg > 0) {
+#pragma unroll
+      for (int q = 0; q < SI * SJ; ++q) sum[(kg - 1) * GROUP + q * 64] = acc[q / SJ][q % SJ];
+    }
+    lds_barrier();
+    if (kg > 0) return;
+#pragma unroll 1
+    for (int k = 0; k < KG - 1; ++k)
+#pragma unroll
+      for (int q = 0; q < SI * SJ; ++q) acc[q / SJ][q % SJ] += sum[k * GROUP + q * 64];
+  }
+
+  const int c16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int a = 0; a < SI; ++a) {
+    const int row = i0 + wi * SI * 16 + a * 16 + c16;
+    if (row >= p.I) continue;
+    if constexpr (GATE) {
+      const int col = j0 + wj * 32 + g * 8;
+      if (col >= p.J) continue;
+      float gt[8], ut[8], h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        gt[i] = acc[a][i >> 2][i & 3];
+        ut[i] = acc[a][2 + (i >> 2)][i & 3];
+        h[i] = gu_silu(gt[i]) * ut[i];
+      }
+      gu_store8(p.out, p.out_bf16, (int64_t)row * p.J + col, h);
+      if (p.pre) {
+        gu_store8(p.pre, p.pre_bf16, (int64_t)row * 2 * p.J + col, gt);
+        gu_store8(p.pre, p.pre_bf16, (int64_t)row * 2 * p.J + p.J + col, ut);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < SJ / 2; ++c) {
+        const int col = j0 + wj * SJ * 16 + c * 32 + g * 8;
+        if (col >= p.J) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = acc[a][2 * c + (i >> 2)][i & 3];
+        gu_store8(p.out, p.out_bf16, ((int64_t)split * p.I + row) * p.J + col, v);
+      }
+    }
+  }
+}
+
+template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, bool GATE, int OCC>
+static hipError_t launch_tiles(TileArgs a, hipStream_t stream) {
+  constexpr int BM = WI * SI * 16, BN = WJ * SJ * 16, CN = GATE ? BN / 2 : BN;
+  a.tiles_i = (a.I + BM - 1) / BM;
+  a.tiles_j = (a.J + CN - 1) / CN;
+  const int stages = (a.parts * ((a.R + GU_BK - 1) / GU_BK) + KG - 1) / KG;
+  a.steps = (stages + a.splits - 1) / a.splits;
+  const int64_t groups = (int64_t)a.tiles_i * a.tiles_j * a.splits;
+  hipLaunchKernelGGL((gu_tile_kernel<AROW, BROW, WI, WJ, SI, SJ, KG, GATE, OCC>), dim3((unsigned)groups),
+                     dim3(WI * WJ * KG * 64), 0, stream, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the weights stream through registers
+// ---------------------------------------------------------------------------
+
+struct StreamArgs {
+  const uint16_t* x;
+  const uint16_t* w;
+  int64_t K;
+  int M, F;
+  void* h;
+  int h_bf16;
+  void* pre;
+  int pre_bf16;
+};
+
+// A wave takes 16 gate columns and the 16 up columns that belong to them, and
+// its share of K; NB blocks of 16 rows; D chunks of 64 k in flight.
+template <int NB, int D>
+__global__ __launch_bounds__(512) void gu_stream_kernel(StreamArgs p) {
+  __shared__ float s_part[8][NB * 2 * 4][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n16 = lane & 15, g = lane >> 4;
+  const int64_t K = p.K;
+  const int n0 = blockIdx.x * 16;
+  const int n = min(n0 + n16, p.F - 1);
+  const uint16_t* wg = p.w + (int64_t)n * K + g * 8;
+  const uint16_t* wu = wg + (int64_t)p.F * K;
+  const uint16_t* xr[NB];
+  bool on[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    on[b] = b * 16 + n16 < p.M;
+    xr[b] = p.x + (int64_t)(on[b] ? b * 16 + n16 : 0) * K + g * 8;
+  }
+  struct Chunk {
+    u32x4_t w[2][2], x[NB][2];
+  };
+  const int chunks = (int)((K + 63) >> 6);
+  const int share = (chunks + 7) / 8;
+  const int first = wave * share, count = min(share, chunks - first);
+  auto load = [&](int v, Chunk& q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int64_t k = (int64_t)(first + v) * 64 + s * 32;
+      const bool in = k + g * 8 < K;
+      const int64_t at = in ? k : 0;
+      q.w[0][s] = in ? *reinterpret_cast<const u32x4_t*>(wg + at) : u32x4_t{0, 0, 0, 0};
+      q.w[1][s] = in ? *reinterpret_cast<const u32x4_t*>(wu + at) : u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        q.x[b][s] = in && on[b] ? *reinterpret_cast<const u32x4_t*>(xr[b] + at) : u32x4_t{0, 0, 0, 0};
+    }
+  };
+  f32x4_t acc[NB][2];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b][0] = acc[b][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  Chunk ring[D];
+#pragma unroll
+  for (int i = 0; i < D; ++i)
+    if (i < count) load(i, ring[i]);
+  for (int v = 0; v < count; v += D) {
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+      if (v + i < count) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            acc[b][0] = gu_mfma(ring[i].x[b][s], ring[i].w[0][s], acc[b][0]);
+            acc[b][1] = gu_mfma(ring[i].x[b][s], ring[i].w[1][s], acc[b][1]);
+          }
+        if (v + i + D < count) load(v + i + D, ring[i]);
+      }
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_part[wave][b * 8 + i][lane] = acc[b][i >> 2][i & 3];
+  __syncthreads();
+  for (int o = threadIdx.x; o < NB * 4 * 64; o += 512) {
+    const int l = o & 63, i = (o >> 6) & 3, b = o >> 8;
+    const int row = b * 16 + (l >> 4) * 4 + i, col = n0 + (l & 15);
+    if (row >= p.M || col >= p.F) continue;
+    float gt = 0.f, ut = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      gt += s_part[w][b * 8 + i][l];
+      ut += s_part[w][b * 8 + 4 + i][l];
+    }
+    const float h = gu_silu(gt) * ut;
+    const int64_t at = (int64_t)row * p.F + col;
+    if (p.h_bf16) reinterpret_cast<uint16_t*>(p.h)[at] = f32_to_bf16_rne(h);
+    else reinterpret_cast<float*>(p.h)[at] = h;
+    if (p.pre) {
+      const int64_t pa = (int64_t)row * 2 * p.F + col;
+      if (p.pre_bf16) {
+        reinterpret_cast<uint16_t*>(p.pre)[pa] = f32_to_bf16_rne(gt);
+        reinterpret_cast<uint16_t*>(p.pre)[pa + p.F] = f32_to_bf16_rne(ut);
+      } else {
+        reinterpret_cast<float*>(p.pre)[pa] = gt;
+        reinterpret_cast<float*>(p.pre)[pa + p.F] = ut;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The activation's gradient, and sums of shares
+// ---------------------------------------------------------------------------
+
+template <bool BF16>
+__device__ __forceinline__ void gu_load8(const void* p, int64_t i, float (&v)[8]) {
+  if (BF16) {
+    const u32x4_t q = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = c & 1 ? bf16_hi(q[c >> 1]) : bf16_lo(q[c >> 1]);
+  } else {
+    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+    const float4 a = f[0], b = f[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+// v as the sum of PARTS bf16 values: the nearest one, then the nearest one to
+// what is left (24 bits in three).  A value that is not finite is its own first
+// part alone.
+template <int PARTS>
+__device__ __forceinline__ void gu_store_parts(uint16_t* d, int64_t stride, int64_t i, float (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = pack_bf16(v[2 * c], v[2 * c + 1]);
+    *reinterpret_cast<uint4*>(d + q * stride + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (q + 1 < PARTS) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float r = v[c] - (c & 1 ? bf16_hi(w[c >> 1]) : bf16_lo(w[c >> 1]));
+        v[c] = fabsf(r) < 3.0e38f ? r : 0.f;
+      }
+    }
+  }
+}
+
+// d = [dg du] of [M, 2F] sums and dh [M, F], eight columns of each a thread, in
+// bf16 (PARTS 1), or in three bf16 matrices that add up to the f32 value.
+template <bool PBF16, bool HBF16, int PARTS>
+__global__ __launch_bounds__(256) void gu_act_bwd_kernel(const void* __restrict__ pre, const void* __restrict__ dh,
+                                                         int64_t M, int F, uint16_t* __restrict__ d) {
+  const int64_t per = F / 8, total = M * per;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t m = i / per;
+    const int64_t at = m * 2 * F + (i - m * per) * 8;
+    float gt[8], ut[8], hv[8];
+    gu_load8<PBF16>(pre, at, gt);
+    gu_load8<PBF16>(pre, at + F, ut);
+    gu_load8<HBF16>(dh, at - m * F, hv);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float s = 1.0f / (1.0f + __expf(-gt[c]));
+      const float dg = hv[c] * ut[c] * s * (1.0f + gt[c] * (1.0f - s));
+      ut[c] = hv[c] * gt[c] * s;
+      gt[c] = dg;
+    }
+    gu_store_parts<PARTS>(d, M * 2 * F, at, gt);
+    gu_store_parts<PARTS>(d, M * 2 * F, at + F, ut);
+  }
+}
+
+// out = sum of `splits` f32 matrices of n values, in order.
+__global__ __launch_bounds__(256) void gu_join_kernel(const float* __restrict__ part, int splits, int64_t n,
+                                                      void* __restrict__ out, int bf16) {
+  for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 8; i < n;
+       i += (int64_t)gridDim.x * blockDim.x * 8) {
+    float v[8];
+    gu_load8<false>(part, i, v);
+    for (int s = 1; s < splits; ++s) {
+      float w[8];
+      gu_load8<false>(part + s * n, i, w);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] += w[c];
+    }
+    gu_store8(out, bf16, i, v);
+  }
+}
+
+static unsigned gu_grid(int64_t threads) {
+  const int64_t g = (threads + 255) / 256;
+  return (unsigned)(g < (int64_t(1) << 22) ? g : (int64_t(1) << 22));
+}
+
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tiles of 64 x 64 (gate and up: 64 x 32 columns of h), the smallest that any
+// launch takes, times the most shares of a sum.
+int64_t gate_up_workgroups(int32_t M, int32_t N, int32_t K) {
+  const int64_t fwd = ceil_div(M, 64) * ceil_div(N / 2, 32), dx = ceil_div(M, 64) * ceil_div(K, 128);
+  const int64_t dw = ceil_div(N, 128) * ceil_div(K, 128);
+  const int64_t most = fwd > dx ? fwd : dx;
+  return most > dw ? most : dw;
+}
+
+hipError_t launch_gate_up(const uint16_t* x, const uint16_t* w, int32_t M, int32_t N, int32_t K, void* h, int h_bf16,
+                          void* pre, int pre_bf16, hipStream_t stream) {
+  const int F = N / 2;
+  if (M <= 32) {
+    StreamArgs a = {x, w, K, M, F, h, h_bf16, pre, pre_bf16};
+    if (M <= 16) hipLaunchKernelGGL((gu_stream_kernel<1, 4>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((gu_stream_kernel<2, 3>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
+    return hipGetLastError();
+  }
+  TileArgs a = {};
+  a.a = x; a.b = w; a.lda = K; a.ldb = K;
+  a.I = M; a.J = F; a.R = K;
+  a.parts = 1; a.splits = 1;
+  a.out = h; a.out_bf16 = h_bf16; a.pre = pre; a.pre_bf16 = pre_bf16;
+  const int64_t large = ceil_div(M, 256) * ceil_div(F, 128), mid = ceil_div(M, 128) * ceil_div(F, 64);
+  if (large >= GU_CUS / 2) return launch_tiles<false, false, 2, 4, 8, 4, 1, true, 2>(a, stream);
+  if (mid >= GU_CUS) return launch_tiles<false, false, 2, 2, 4, 4, 1, true, 2>(a, stream);
+  return launch_tiles<false, false, 4, 1, 1, 4, 4, true, 4>(a, stream);
+}
+
+// The plan of the gradients: bf16 parts of d, and shares of the sum of dx.
+struct BwdPlan {
+  int parts, splits;
+  int64_t d_bytes, ws_bytes;
+};
+
+static BwdPlan bwd_plan(int32_t M, int32_t N, int32_t K, int want_dx, int dx_bf16, int want_dw, int dw_bf16) {
+  BwdPlan p;
+  p.parts = (want_dx && !dx_bf16) || (want_dw && !dw_bf16) ? 3 : 1;
+  p.d_bytes = ((int64_t)p.parts * M * N * 2 + 255) / 256 * 256;
+  p.splits = 1;
+  if (want_dx) {
+    const int64_t tiles = ceil_div(M, 64) * ceil_div(K, 128);
+    const int64_t stages = ceil_div((dx_bf16 ? 1 : 3) * ceil_div(N, GU_BK), 2);
+    while (p.splits < 16 && tiles * p.splits * 2 <= GU_CUS && stages >= 4 * p.splits) p.splits *= 2;
+  }
+  p.ws_bytes = p.d_bytes + (p.splits > 1 ? (int64_t)p.splits * M * K * 4 : 0);
+  return p;
+}
+
+int64_t gate_up_bwd_ws(int32_t M, int32_t N, int32_t K, int want_dx, int dx_bf16, int want_dw, int dw_bf16) {
+  return bwd_plan(M, N, K, want_dx, dx_bf16, want_dw, dw_bf16).ws_bytes;
+}
+
+template <bool P, bool H>
+static void launch_act_bwd(int parts, const void* pre, const void* dh, int64_t M, int F, uint16_t* d, hipStream_t s) {
+  const dim3 grid(gu_grid(M * (F / 8)));
+  if (parts == 1) hipLaunchKernelGGL((gu_act_bwd_kernel<P, H, 1>), grid, dim3(256), 0, s, pre, dh, M, F, d);
+  else hipLaunchKernelGGL((gu_act_bwd_kernel<P, H, 3>), grid, dim3(256), 0, s, pre, dh, M, F, d);
+}
+
+hipError_t launch_gate_up_bwd(const void* dh, int dh_bf16, const uint16_t* x, const uint16_t* w, const void* pre,
+                              int pre_bf16, int32_t M, int32_t N, int32_t K, void* dx, int dx_bf16, void* dw,
+                              int dw_bf16, void* ws, hipStream_t stream) {
+  const BwdPlan pl = bwd_plan(M, N, K, dx != nullptr, dx_bf16, dw != nullptr, dw_bf16);
+  uint16_t* d = static_cast<uint16_t*>(ws);
+  const int F = N / 2;
+  if (pre_bf16) {
+    if (dh_bf16) launch_act_bwd<true, true>(pl.parts, pre, dh, M, F, d, stream);
+    else launch_act_bwd<true, false>(pl.parts, pre, dh, M, F, d, stream);
+  } else {
+    if (dh_bf16) launch_act_bwd<false, true>(pl.parts, pre, dh, M, F, d, stream);
+    else launch_act_bwd<false, false>(pl.parts, pre, dh, M, F, d, stream);
+  }
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  if (dx) {
+    TileArgs a = {};
+    a.a = d; a.b = w; a.lda = N; a.ldb = K;
+    a.I = M; a.J = K; a.R = N;
+    a.parts = dx_bf16 ? 1 : 3; a.part_stride = (int64_t)M * N;
+    a.splits = pl.splits;
+    a.out = dx; a.out_bf16 = dx_bf16;
+    if (pl.splits > 1) {
+      a.out = static_cast<uint8_t*>(ws) + pl.d_bytes;
+      a.out_bf16 = 0;
+    }
+    const int64_t large = ceil_div(M, 256) * ceil_div(K, 256), mid = ceil_div(M, 128) * ceil_div(K, 128);
+    if (pl.splits == 1 && large >= GU_CUS / 2) err = launch_tiles<false, true, 2, 4, 8, 4, 1, false, 2>(a, stream);
+    else if (pl.splits == 1 && mid >= GU_CUS) err = launch_tiles<false, true, 2, 2, 4, 4, 1, false, 2>(a, stream);
+    else err = launch_tiles<false, true, 2, 2, 2, 4, 2, false, 2>(a, stream);
+    if (err != hipSuccess) return err;
+    if (pl.splits > 1) {
+      const int64_t n = (int64_t)M * K;
+      hipLaunchKernelGGL(gu_join_kernel, dim3(gu_grid(n / 8)), dim3(256), 0, stream, static_cast<const float*>(a.out),
+                         pl.splits, n, dx, dx_bf16);
+      err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
+  }
+  if (dw) {
+    TileArgs a = {};
+    a.a = d; a.b = x; a.lda = N; a.ldb = K;
+    a.I = N; a.J = K; a.R = M;
+    a.parts = dw_bf16 ? 1 : 3; a.part_stride = (int64_t)M * N;
+    a.splits = 1;
+    a.out = dw; a.out_bf16 = dw_bf16;
+    const int64_t large = ceil_div(N, 256) * ceil_div(K, 256);
+    if (large >= GU_CUS / 2) err = launch_tiles<true, true, 2, 4, 8, 4, 1, false, 2>(a, stream);
+    else err = launch_tiles<true, true, 2, 2, 4, 4, 1, false, 2>(a, stream);
+  }
+  return err;
+}
+
+}  // namespace moe

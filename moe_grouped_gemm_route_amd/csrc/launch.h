@@ -120,4 +120,24 @@ hipError_t launch_dgrad(const uint8_t* packed, int fmt, int32_t E, int32_t N, in
 // Workgroups that launch_dgrad launches for these sizes.
 int64_t dgrad_workgroups(int32_t E, int32_t K, int32_t M);
 
+// Rows times 4-bit integer weights with group scales (G a power of two); ids
+// NULL: dense, weights NULL: a row per pair.
+hipError_t launch_w4_gemv(const uint8_t* codes, const void* scales, int scale_bf16, const uint8_t* zeros, int32_t G,
+                          int32_t E, int32_t N, int32_t K, const uint16_t* x, int x_pairs, int32_t T,
+                          const int32_t* ids, const float* weights, int32_t k, void* y, int y_bf16, int act,
+                          hipStream_t stream);
+// Workgroups that launch_w4_gemv launches for these sizes, at most.
+int64_t w4_workgroups(int32_t N, int32_t G, int32_t T, int32_t k, int pairs, int sum, int act);
+
+// The dense gate/up block, and its gradients (dx, dw: NULL where not wanted);
+// the workspace that these need.
+hipError_t launch_gate_up(const uint16_t* x, const uint16_t* w, int32_t M, int32_t N, int32_t K, void* h, int h_bf16,
+                          void* pre, int pre_bf16, hipStream_t stream);
+int64_t gate_up_bwd_ws(int32_t M, int32_t N, int32_t K, int want_dx, int dx_bf16, int want_dw, int dw_bf16);
+hipError_t launch_gate_up_bwd(const void* dh, int dh_bf16, const uint16_t* x, const uint16_t* w, const void* pre,
+                              int pre_bf16, int32_t M, int32_t N, int32_t K, void* dx, int dx_bf16, void* dw,
+                              int dw_bf16, void* ws, hipStream_t stream);
+// Workgroups of the largest launch of either, at most.
+int64_t gate_up_workgroups(int32_t M, int32_t N, int32_t K);
+
 }  // namespace moe

@@ -24,6 +24,9 @@ routed-expert path computes, written from these pages:
 * The router's top-k choice (gate.py) and the gradients of the layer's steps
   (grad.py), which the pages do not cover: the usual definitions and the plain
   derivatives of the steps above.
+* The dense gated block beside the routed experts, its gradients and 4-bit
+  integer weights (dense.py), which the pages name at most: the usual
+  definitions.
 
 It shares no code with the HIP path and imports nothing from it.
 """
@@ -46,3 +49,4 @@ from .combine import combine  # noqa: F401
 from .act import silu, silu_mul  # noqa: F401
 from .gate import topk_gate, topk_gate_bwd, slot_weights  # noqa: F401
 from .grad import dispatch, dispatch_bwd, combine_bwd, gmm_dgrad, silu_mul_bwd  # noqa: F401
+from .dense import w4_weights, w4_gemv, gate_up, gate_up_bwd  # noqa: F401
