@@ -562,7 +562,7 @@ int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, 
  * the f32 sums depends on the sizes and on the form, not on the values.  Meant
  * for few rows: a dense call reads the weights once per 16 to 64 rows, a routed
  * one once per pair.
- * Limits: N <= 2^30, K <= 2^30, K % group == 0, N even with the activation,
+ * Limits: N <= 2^30, K <= 2^23, K % group == 0, N even with the activation,
  * E*N*K/2 < 2^40, T <= 2^24, 1 <= k <= 64, T*k <= 2^24; codes and x 16-byte
  * aligned, scales and y to their type; a grid of rows * N/16 <= 8,388,607.
  */

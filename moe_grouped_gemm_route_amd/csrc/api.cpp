@@ -364,14 +364,13 @@ int moe_w4_gemv(const uint8_t* codes, const void* scales, int scale_dtype, const
   // a sum of activations is not the activation of a sum
   if (topk_weights && act != MOE_ACT_NONE) return MOE_ERR_UNSUPPORTED;
   if (group != 32 && group != 64 && group != 128 && group != 256) return MOE_ERR_SHAPE;
-  if (E < 1 || N < 1 || N > kMaxCols || K < 1 || K > kMaxCols || K % group != 0) return MOE_ERR_SHAPE;
+  // 64 rows of x and 16 columns of codes are addressed with 32-bit byte offsets
+  if (E < 1 || N < 1 || N > kMaxCols || K < 1 || K > (1 << 23) || K % group != 0) return MOE_ERR_SHAPE;
   if ((int64_t)N * (K / 2) >= kMaxCodeBytes / E) return MOE_ERR_SHAPE;
   if (act == MOE_ACT_SILU_MUL && N % 2 != 0) return MOE_ERR_SHAPE;
   if (T < 1 || T > kMaxRows) return MOE_ERR_SHAPE;
   if (topk_ids) {
     if (k < 1 || k > 64 || (int64_t)T * k > kMaxRows) return MOE_ERR_SHAPE;
-    // the chunks of a token's experts are counted in 32 bits
-    if ((int64_t)k * (K / 32) > (int64_t(1) << 30)) return MOE_ERR_SHAPE;
     if (x_rows != T && x_rows != (int64_t)T * k) return MOE_ERR_SHAPE;
   } else if (E != 1 || k != 1 || x_rows != T) {
     return MOE_ERR_SHAPE;

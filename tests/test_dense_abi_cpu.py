@@ -31,15 +31,15 @@ def test_w4_validation(lib):
     for kw in (dict(sdt=2), dict(sdt=-1), dict(odt=2), dict(act=2), dict(act=-1)):
         assert f(**kw) == ERR_FORMAT and r(**kw) == ERR_FORMAT, kw
     for kw in (dict(group=0), dict(group=16), dict(group=48), dict(group=512), dict(group=-32), dict(K=0), dict(K=240),
-               dict(K=-256), dict(N=0), dict(N=-64), dict(N=(1 << 30) + 1), dict(K=(1 << 30) + 32), dict(T=0, rows=0),
+               dict(K=-256), dict(N=0), dict(N=-64), dict(N=(1 << 30) + 1), dict(K=(1 << 23) + 32), dict(T=0, rows=0),
                dict(T=-1, rows=-1), dict(N=65, act=1), dict(codes=B8), dict(x=B8), dict(scales=B2), dict(y=B2),
                dict(scales=B1, sdt=1), dict(y=B1, odt=1), dict(T=(1 << 24) + 1, rows=(1 << 24) + 1),
-               dict(N=1 << 30, K=1 << 12)):
+               dict(N=1 << 30, K=1 << 12), dict(N=1 << 18, K=1 << 23)):
         assert f(**kw) == ERR_SHAPE, kw
     for kw in (dict(E=2), dict(E=0), dict(k=2), dict(k=0), dict(rows=5), dict(rows=8), dict(rows=0)):
         assert f(**kw) == ERR_SHAPE, kw                      # dense: one matrix, a row each
     for kw in (dict(E=0), dict(E=-1), dict(k=0), dict(k=65), dict(rows=5), dict(rows=0), dict(T=1 << 23, rows=1 << 23, k=4),
-               dict(E=1 << 30, N=1 << 12), dict(K=1 << 30, k=64, N=1)):
+               dict(E=1 << 30, N=1 << 12)):
         assert r(**kw) == ERR_SHAPE, kw
     # a grid past the dispatch limit
     assert f(T=1 << 20, rows=1 << 20, N=1 << 20, K=32) == ERR_SHAPE
