@@ -584,7 +584,8 @@ int moe_w4_gemv(const uint8_t* codes, const void* scales, int scale_dtype, const
  * preact         out [M, N] f32 or bf16 (preact_dtype), may be NULL: the sums,
  *                gate columns first, as moe_gate_up_bwd and moe_silu_mul take them.
  * Limits: M <= 2^24, N % 16 == 0, K % 8 == 0, N and K <= 4,194,048,
- * M*N and M*K < 2^40, M/64 * N/64 and M/64 * K/128 <= 4,194,303; every pointer
+ * M*N and M*K < 2^40, M/32 * N/64, M/64 * K/128 and N/128 * K/128 (each
+ * factor rounded up) <= 4,194,303; every pointer
  * 16-byte aligned.
  * The order of the f32 sums depends on M, N and K.
  */

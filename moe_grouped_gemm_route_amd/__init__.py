@@ -516,6 +516,41 @@ def moe_gmm_dgrad(packed, fmt, E, N, K, dy, group_offsets, M, out_dtype=F32, act
     return dx
 
 
+# What a small call costs is its checks: these read each property once.
+_U8, _I32, _F32T, _BF16T, _I16, _U16 = (torch.uint8, torch.int32, torch.float32, torch.bfloat16, torch.int16,
+                                        torch.uint16)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _is(t, dtype, ndim, name):
+    """t checked as a contiguous device tensor."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous()):
+        _dev(t, dtype, name, ndim)
+
+
+def _is_bits16(t, name):
+    """t checked as a contiguous 2-d device tensor of bfloat16 or its 16-bit views."""
+    if not (isinstance(t, _Tensor) and t.dtype is _BF16T and t.is_cuda and t.dim() == 2 and t.is_contiguous()):
+        _dev(t, t.dtype if getattr(t, "dtype", None) in (_BF16T, _I16, _U16) else _BF16T, name, 2)
+
+
+def _one_device(index, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise MoeGmmError("the tensors must be on one device, got cuda:%d and %s" % (index, t.device))
+
+
+def _enqueue(fn, index, args):
+    """fn(*args, stream) on device index, on its current stream."""
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _check(status)
+
+
 def w4_gemv(codes, scales, x, zeros=None, topk_ids=None, topk_weights=None, out_dtype=F32, act=ACT_NONE, out=None):
     """moe_w4_gemv: a few rows times 4-bit integer weights with group scales.
     Dense: codes [N, K/2] uint8, scales [N, K/G] float32 or bfloat16, zeros
@@ -524,62 +559,76 @@ def w4_gemv(codes, scales, x, zeros=None, topk_ids=None, topk_weights=None, out_
     x [T, K] or [T*k, K] -> y [T*k, N], a row per pair (zeros for an id outside
     [0, E)); with topk_weights [T, k] float32 -> y [T, N], a token's rows summed.
     act=ACT_SILU_MUL: N/2 columns (not with topk_weights)."""
-    routed = topk_ids is not None
-    _dev(codes, torch.uint8, "codes", 3 if routed else 2)
-    sdt = _float(scales, "scales", 3 if routed else 2)
-    xb = _bits16(x, "x")
-    if xb.dim() != 2:
-        raise MoeGmmError("x must be [rows, K]")
-    N, K2 = codes.shape[-2:]
-    rows, K = xb.shape
-    groups = scales.shape[-1]
-    if K != 2 * K2 or scales.shape[:-1] != codes.shape[:-1] or groups < 1 or K % groups:
+    nd = 2 if topk_ids is None else 3
+    _is(codes, _U8, nd, "codes")
+    sdt = _float(scales, "scales", nd)
+    _is_bits16(x, "x")
+    lead, slead = codes.shape, scales.shape
+    N, K2 = lead[-2:]
+    rows, K = x.shape
+    groups = slead[-1]
+    if K != 2 * K2 or slead[:-1] != lead[:-1] or groups < 1 or K % groups:
         raise MoeGmmError("codes must be [.., N, K/2] and scales [.., N, K/G] for x [rows, K]")
     if zeros is not None:
-        _dev(zeros, torch.uint8, "zeros", scales.dim())
-        if zeros.shape != scales.shape:
+        _is(zeros, _U8, nd, "zeros")
+        if zeros.shape != slead:
             raise MoeGmmError("zeros must have the shape of scales")
     E, T, k, out_rows = 1, rows, 1, rows
-    if routed:
-        _dev(topk_ids, torch.int32, "topk_ids", 2)
-        E = codes.shape[0]
+    ids = weights = None
+    if topk_ids is not None:
+        _is(topk_ids, _I32, 2, "topk_ids")
+        E = lead[0]
         T, k = topk_ids.shape
         out_rows = T * k
-        if rows != T and rows != T * k:
+        ids = topk_ids.data_ptr()
+        if rows != T and rows != out_rows:
             raise MoeGmmError("x must have T or T*k rows")
     if topk_weights is not None:
-        if not routed:
+        if ids is None:
             raise MoeGmmError("topk_weights go with topk_ids")
-        _dev(topk_weights, torch.float32, "topk_weights", 2)
+        _is(topk_weights, _F32T, 2, "topk_weights")
         if topk_weights.shape != topk_ids.shape:
             raise MoeGmmError("topk_weights must be [T, k]")
         out_rows = T
+        weights = topk_weights.data_ptr()
+    if (E | N | K | rows | T | k) >> 31:
+        _too_wide(max(E, N, K, rows, T, k))
+    index = codes.get_device()
+    _one_device(index, scales, x, zeros, topk_ids, topk_weights, out)
     y = _out(out, (out_rows, N // 2 if act == ACT_SILU_MUL else N), out_dtype, "out", scales)
-    _launch(library().moe_w4_gemv, (codes, scales, zeros, xb, topk_ids, topk_weights, y), codes, scales, sdt, zeros,
-            K // groups, E, N, K, xb, rows, T, topk_ids, topk_weights, k, y, _FLOATS[y.dtype], act)
+    _enqueue(library().moe_w4_gemv, index,
+             (codes.data_ptr(), scales.data_ptr(), sdt, None if zeros is None else zeros.data_ptr(), K // groups, E, N,
+              K, x.data_ptr(), rows, T, ids, weights, k, y.data_ptr(), _FLOATS[y.dtype], act))
     return y
 
 
-def _gate_up_shapes(x, w13):
-    """x [M, K] and w13 [N, K] bf16 checked, as 16-bit views."""
-    xb, wb = _bits16(x, "x"), _bits16(w13, "w13")
-    if xb.dim() != 2 or wb.dim() != 2 or xb.shape[1] != wb.shape[1] or wb.shape[0] % 2:
+def _gate_up_shape(x, w13):
+    """M, N, K of x [M, K] and w13 [N, K] bf16."""
+    _is_bits16(x, "x")
+    _is_bits16(w13, "w13")
+    M, K = x.shape
+    N, K1 = w13.shape
+    if K != K1 or N % 2:
         raise MoeGmmError("x must be [M, K] and w13 [N, K] with N even")
-    return xb, wb
+    if (M | N | K) >> 31:
+        _too_wide(max(M, N, K))
+    return M, N, K
 
 
 def gate_up(x, w13, out_dtype=F32, preact_dtype=None, out=None, preact=None):
     """moe_gate_up.  x bf16 [M, K], w13 bf16 [N, K] (gate rows, then up rows) ->
     h [M, N/2]; with preact_dtype (F32 or BF16), or a preact tensor [M, N] to
     write, (h, preact): the sums that gate_up_bwd takes."""
-    xb, wb = _gate_up_shapes(x, w13)
-    M, K = xb.shape
-    N = wb.shape[0]
-    h = _out(out, (M, N // 2), out_dtype, "out", xb)
+    M, N, K = _gate_up_shape(x, w13)
+    index = x.get_device()
+    _one_device(index, w13, out, preact)
+    h = _out(out, (M, N // 2), out_dtype, "out", x)
+    pre, pdt = None, F32
     if preact is not None or preact_dtype is not None:
-        preact = _out(preact, (M, N), preact.dtype if preact_dtype is None else preact_dtype, "preact", xb)
-    _launch(library().moe_gate_up, (xb, wb, h, preact), xb, wb, M, N, K, h, _FLOATS[h.dtype], preact,
-            F32 if preact is None else _FLOATS[preact.dtype])
+        preact = _out(preact, (M, N), preact.dtype if preact_dtype is None else preact_dtype, "preact", x)
+        pre, pdt = preact.data_ptr(), _FLOATS[preact.dtype]
+    _enqueue(library().moe_gate_up, index,
+             (x.data_ptr(), w13.data_ptr(), M, N, K, h.data_ptr(), _FLOATS[h.dtype], pre, pdt))
     return h if preact is None else (h, preact)
 
 
@@ -588,34 +637,36 @@ def gate_up_bwd_workspace_bytes(M, N, K, dx_dtype=F32, dw_dtype=F32):
     wanted."""
     if (M | N | K) >> 31:   # (ctypes passes the low 32 bits)
         return 0
-    return int(library().moe_gate_up_bwd_workspace_bytes(M, N, K, dx_dtype is not None, dx_dtype or 0,
-                                                         dw_dtype is not None, dw_dtype or 0))
+    return library().moe_gate_up_bwd_workspace_bytes(M, N, K, dx_dtype is not None, dx_dtype or 0,
+                                                     dw_dtype is not None, dw_dtype or 0)
 
 
 def gate_up_bwd(dh, x, w13, preact, dx_dtype=F32, dw_dtype=F32, dx=None, dw13=None, ws=None):
     """moe_gate_up_bwd.  dh [M, N/2] float32 or bfloat16, x and w13 as given to
     gate_up, the preact it kept -> (dx [M, K], dw13 [N, K]); a dtype of None
     leaves that gradient out (None in its place).  dx, dw13: tensors to write.
-    ws: a device tensor of at least gate_up_bwd_workspace_bytes, or None to
-    allocate one."""
+    ws: a device tensor of at least gate_up_bwd_workspace_bytes, 256-byte
+    aligned, or None to allocate one."""
     hdt = _float(dh, "dh", 2)
     pdt = _float(preact, "preact", 2)
-    xb, wb = _gate_up_shapes(x, w13)
-    M, K = xb.shape
-    N = wb.shape[0]
-    if tuple(dh.shape) != (M, N // 2) or tuple(preact.shape) != (M, N):
+    M, N, K = _gate_up_shape(x, w13)
+    if dh.shape != (M, N // 2) or preact.shape != (M, N):
         raise MoeGmmError("dh must be [M, N/2] and preact [M, N]")
+    index = x.get_device()
+    _one_device(index, dh, w13, preact, dx, dw13, ws)
     if dx is not None or dx_dtype is not None:
-        dx = _out(dx, (M, K), dx_dtype if dx is None else dx.dtype, "dx", xb)
+        dx = _out(dx, (M, K), dx_dtype if dx is None else dx.dtype, "dx", x)
     if dw13 is not None or dw_dtype is not None:
-        dw13 = _out(dw13, (N, K), dw_dtype if dw13 is None else dw13.dtype, "dw13", xb)
+        dw13 = _out(dw13, (N, K), dw_dtype if dw13 is None else dw13.dtype, "dw13", x)
     xdt, wdt = (None if t is None else _FLOATS[t.dtype] for t in (dx, dw13))
     if ws is None:
-        ws = xb.new_empty(max(gate_up_bwd_workspace_bytes(M, N, K, xdt, wdt), 1), dtype=torch.uint8)
-    elif not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        ws = x.new_empty(gate_up_bwd_workspace_bytes(M, N, K, xdt, wdt) or 1, dtype=_U8)
+    elif not isinstance(ws, _Tensor) or not ws.is_cuda or not ws.is_contiguous():
         raise MoeGmmError("ws must be a contiguous CUDA (HIP) tensor")
-    _launch(library().moe_gate_up_bwd, (dh, xb, wb, preact, dx, dw13, ws), dh, hdt, xb, wb, preact, pdt, M, N, K, dx,
-            xdt or 0, dw13, wdt or 0, ws, _sz(ws.numel() * ws.element_size()))
+    _enqueue(library().moe_gate_up_bwd, index,
+             (dh.data_ptr(), hdt, x.data_ptr(), w13.data_ptr(), preact.data_ptr(), pdt, M, N, K,
+              None if dx is None else dx.data_ptr(), xdt or 0, None if dw13 is None else dw13.data_ptr(), wdt or 0,
+              ws.data_ptr(), ws.numel() * ws.element_size()))
     return dx, dw13
 
 

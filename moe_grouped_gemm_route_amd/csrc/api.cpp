@@ -73,7 +73,7 @@ int gate_up_shape(int32_t M, int32_t N, int32_t K) {
   if (M < 1 || M > kMaxRows || N < 16 || N % 16 != 0 || K < 8 || K % 8 != 0) return MOE_ERR_SHAPE;
   if ((int64_t)N * 512 > 0x7FFE0000ll || (int64_t)K * 512 > 0x7FFE0000ll) return MOE_ERR_SHAPE;
   if ((int64_t)M * N >= (int64_t(1) << 40) || (int64_t)M * K >= (int64_t(1) << 40)) return MOE_ERR_SHAPE;
-  // workgroups of up to 1,024 work-items, 16 shares of a sum at most
+  // workgroups of up to 1,024 work-items
   if (moe::gate_up_workgroups(M, N, K) > kMaxWorkgroups / 4) return MOE_ERR_SHAPE;
   return MOE_OK;
 }

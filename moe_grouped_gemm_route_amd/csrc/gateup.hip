@@ -51,8 +51,7 @@ struct TileArgs {
   const uint16_t* b;       // likewise with J
   int64_t lda, ldb;
   int I, J, R;             // J: columns of out (with GATE: of h)
-  int parts;               // A is the sum of this many matrices, part_stride apart
-  int64_t part_stride;
+  int64_t part_stride;     // PARTS matrices, this far apart, add up to A
   int splits, steps;       // shares of the sum over r, and stages of a share
   int tiles_i, tiles_j;
   void* out;               // [I, J]; with splits > 1 f32 [splits, I, J]
@@ -133,9 +132,10 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 }
 
 // WI x WJ waves of SI x SJ 16 x 16 subtiles each, KG such groups of waves that
-// take every KG-th 64 r; two stages.
+// take every KG-th 64 r; two stages.  PARTS: A comes as that many bf16 matrices,
+// each multiplied with the same B.
 //
-// The walk.  A stage's 2 SI operand groups (one A subtile, SJ matrix
+// The walk.  A stage's 2 SI PARTS operand groups (one A subtile, SJ matrix
 // instructions) run in order; operands are read from LDS two groups ahead.
 // The last quarter of the groups has all of its operands in registers, and the
 // barrier stands before it: there every wave has read the stage to the end and
@@ -145,13 +145,14 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 // loads have a whole stage to land in, and the matrix pipes do not run dry at
 // the barrier.  The wait before it is a full one: direct-to-LDS loads are not
 // counted as still on their way.
-template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, bool GATE, int OCC>
+template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, int OCC>
 __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArgs p) {
   constexpr int NW = WI * WJ;
   constexpr int BM = WI * SI * 16, BN = WJ * SJ * 16;
   typedef Operand<AROW, BM, NW, false> OpA;
   typedef Operand<BROW, BN, NW, true> OpB;
-  constexpr int SLICE = OpA::BYTES + OpB::BYTES;
+  constexpr int A_BYTES = PARTS * OpA::BYTES;
+  constexpr int SLICE = A_BYTES + OpB::BYTES;
   constexpr int STAGE = KG * SLICE;
   constexpr int JOIN = (KG - 1) * BM * BN * 4;
   constexpr int LDS = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
@@ -200,55 +201,45 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
     }
   }
 
-  // The stages of this group: r of `parts` matrices one after the other, each
-  // padded to whole stages; the group's next is KG stages on.
-  const int per_part = (p.R + GU_BK - 1) / GU_BK;
-  int part, at;                     // next stage to load: its part, and stage in it
-  {
-    const int s = split * p.steps * KG + kg;
-    part = s / per_part;
-    at = s - part * per_part;
-  }
+  // The next stage to load: this group's KG stages on from its last.
+  const int stages = (p.R + GU_BK - 1) / GU_BK;
+  int at = split * p.steps * KG + kg;
   const uint32_t l0 = lds_addr(s_all) + kg * SLICE;
-  const uint32_t range_a = AROW ? 0 : 0x7FFE0000u;   // lanes outside are marked: the range need not end anywhere
-  auto load = [&](int buf, auto a_or_b) __attribute__((always_inline)) {
-    constexpr bool B = decltype(a_or_b)::value;
-    const bool live = part < p.parts;
-    const int r0 = at * GU_BK;
-    const int left = p.R - r0;      // r of the stage that exist, or more
-    if constexpr (!B) {
-      const uint16_t* base = p.a + part * p.part_stride;
-      base += AROW ? (int64_t)r0 * p.lda + i0 : (int64_t)i0 * p.lda + r0;
-      const uint32_t bytes = AROW ? (uint32_t)((min(left, GU_BK) * p.lda - i0) * 2) : range_a;
-      const u32x4_t rs = only_if(live, make_rsrc(live ? base : p.a, bytes));
+  constexpr uint32_t OPEN = 0x7FFE0000u;   // lanes outside are marked: the range need not end anywhere
+  auto load_a = [&](int buf) __attribute__((always_inline)) {
+    const bool live = at < stages;
+    const int r0 = live ? at * GU_BK : 0;
+    const int left = p.R - r0;             // r of the stage that exist, or more
+    const uint32_t bytes = AROW ? (uint32_t)((min(left, GU_BK) * p.lda - i0) * 2) : OPEN;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      const uint16_t* base = p.a + q * p.part_stride + (AROW ? (int64_t)r0 * p.lda + i0 : (int64_t)i0 * p.lda + r0);
+      const u32x4_t rs = only_if(live, make_rsrc(base, bytes));
 #pragma unroll
       for (int j = 0; j < OpA::LOADS; ++j) {
         const uint32_t vo = AROW || aseg[j] < left ? avo[j] : kLaneOob;
-        load_lds16<false>(l0 + buf * STAGE + (wave * OpA::LOADS + j) * 1024, rs, vo, 0);
-      }
-    } else {
-      const uint16_t* base = p.b + (BROW ? (int64_t)r0 * p.ldb + j0 : (int64_t)j0 * p.ldb + r0);
-      const uint32_t bytes = BROW ? (uint32_t)((min(left, GU_BK) * p.ldb - j0) * 2) : 0x7FFE0000u;
-      const u32x4_t rs = only_if(live, make_rsrc(live ? base : p.b, bytes));
-      const u32x4_t ru = GATE ? only_if(live, make_rsrc(live ? base + (int64_t)p.J * p.ldb : p.b, bytes)) : rs;
-#pragma unroll
-      for (int j = 0; j < OpB::LOADS; ++j) {
-        const uint32_t vo = BROW || bseg[j] < left ? bvo[j] : kLaneOob;
-        load_lds16<false>(l0 + buf * STAGE + OpA::BYTES + (wave * OpB::LOADS + j) * 1024, up[j] ? ru : rs, vo, 0);
+        load_lds16<false>(l0 + buf * STAGE + q * OpA::BYTES + (wave * OpA::LOADS + j) * 1024, rs, vo, 0);
       }
     }
   };
-  auto advance = [&] {
-    at += KG;
-    while (at >= per_part) {
-      at -= per_part;
-      ++part;
+  auto load_b = [&](int buf) __attribute__((always_inline)) {
+    const bool live = at < stages;
+    const int r0 = live ? at * GU_BK : 0;
+    const int left = p.R - r0;
+    const uint16_t* base = p.b + (BROW ? (int64_t)r0 * p.ldb + j0 : (int64_t)j0 * p.ldb + r0);
+    const uint32_t bytes = BROW ? (uint32_t)((min(left, GU_BK) * p.ldb - j0) * 2) : OPEN;
+    const u32x4_t rs = only_if(live, make_rsrc(base, bytes));
+    const u32x4_t ru = GATE ? only_if(live, make_rsrc(base + (int64_t)p.J * p.ldb, bytes)) : rs;
+#pragma unroll
+    for (int j = 0; j < OpB::LOADS; ++j) {
+      const uint32_t vo = BROW || bseg[j] < left ? bvo[j] : kLaneOob;
+      load_lds16<false>(l0 + buf * STAGE + A_BYTES + (wave * OpB::LOADS + j) * 1024, up[j] ? ru : rs, vo, 0);
     }
   };
   auto load_stage = [&](int buf) __attribute__((always_inline)) {
-    load(buf, std::false_type{});
-    load(buf, std::true_type{});
-    advance();
+    load_a(buf);
+    load_b(buf);
+    at += KG;
   };
 
   f32x4_t acc[SI][SJ];
@@ -257,19 +248,21 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
 #pragma unroll
     for (int s = 0; s < SJ; ++s) acc[a][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  constexpr int NQ = 2 * SI;                       // operand groups of a stage
+  constexpr int SP = SI * PARTS;
+  constexpr int NQ = 2 * SP;                       // operand groups of a stage
   constexpr int HOLD = NQ >= 4 ? NQ / 4 : 1;       // behind the barrier
-  constexpr int CA = SI >= 2 ? 2 : 1;              // A operands read a stage ahead
+  constexpr int CA = SP >= 2 ? 2 : 1;              // A operands read a stage ahead
   u32x4_t fa[NQ], fb[2][SJ];
   auto read_a = [&](int buf, int q) __attribute__((always_inline)) {
-    fa[q] = OpA::read(s_all + buf * STAGE + kg * SLICE, wi * SI * 16, q % SI, q / SI);
+    fa[q] = OpA::read(s_all + buf * STAGE + kg * SLICE + q % PARTS * OpA::BYTES, wi * SI * 16, q % SP / PARTS, q / SP);
   };
   auto read_b = [&](int buf, int ks, int s) __attribute__((always_inline)) {
-    fb[ks][s] = OpB::read(s_all + buf * STAGE + kg * SLICE + OpA::BYTES, wj * SJ * 16, s, ks);
+    fb[ks][s] = OpB::read(s_all + buf * STAGE + kg * SLICE + A_BYTES, wj * SJ * 16, s, ks);
   };
   auto mults = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < SJ; ++s) acc[q % SI][s] = gu_mfma(fb[q / SI][s], fa[q], acc[q % SI][s]);
+    for (int s = 0; s < SJ; ++s)
+      acc[q % SP / PARTS][s] = gu_mfma(fb[q / SP][s], fa[q], acc[q % SP / PARTS][s]);
   };
 
   const int steps = p.steps;
@@ -292,7 +285,7 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
 #pragma unroll
     for (int q = 0; q < NQ - HOLD; ++q) {
       __builtin_amdgcn_sched_barrier(0);
-      constexpr int FRONT = SI - CA;               // A reads of the first half
+      constexpr int FRONT = SP - CA;               // A reads of the first half
       const int upto = q == NQ - HOLD - 1 ? READS : (READS * (q + 1) + NQ - HOLD - 1) / (NQ - HOLD);
 #pragma unroll
       for (int k = 0; k < READS; ++k) {
@@ -305,7 +298,7 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
           const int rest = k - 2 * MIX;            // one of the two is done
           if (FRONT > SJ) read_a(buf, CA + MIX + rest);
           else if (rest < SJ - MIX) read_b(buf, 1, MIX + rest);
-          else read_a(buf, SI + rest - (SJ - MIX));
+          else read_a(buf, SP + rest - (SJ - MIX));
         }
       }
       done = upto;
@@ -318,9 +311,9 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
     {
       const uint8_t* nx = s_all + (buf ^ 1) * STAGE + kg * SLICE;
 #pragma unroll
-      for (int s = 0; s < SJ; ++s) nb[s] = OpB::read(nx + OpA::BYTES, wj * SJ * 16, s, 0);
+      for (int s = 0; s < SJ; ++s) nb[s] = OpB::read(nx + A_BYTES, wj * SJ * 16, s, 0);
 #pragma unroll
-      for (int q = 0; q < CA; ++q) na[q] = OpA::read(nx, wi * SI * 16, q, 0);
+      for (int q = 0; q < CA; ++q) na[q] = OpA::read(nx + q % PARTS * OpA::BYTES, wi * SI * 16, q / PARTS, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -328,13 +321,13 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
       mults(q);
       __builtin_amdgcn_sched_barrier(0);
       if (q == NQ - HOLD) {
-        load(buf, std::false_type{});
-        if (HOLD == 1) load(buf, std::true_type{});
+        load_a(buf);
+        if (HOLD == 1) load_b(buf);
       }
-      if (q == NQ - HOLD + 1) load(buf, std::true_type{});
+      if (q == NQ - HOLD + 1) load_b(buf);
       __builtin_amdgcn_sched_barrier(0);
     }
-    advance();
+    at += KG;
 #pragma unroll
     for (int s = 0; s < SJ; ++s) fb[0][s] = nb[s];
 #pragma unroll
@@ -392,18 +385,30 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
   }
 }
 
-template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, bool GATE, int OCC>
+template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, int OCC>
 static hipError_t launch_tiles(TileArgs a, hipStream_t stream) {
   constexpr int BM = WI * SI * 16, BN = WJ * SJ * 16, CN = GATE ? BN / 2 : BN;
   a.tiles_i = (a.I + BM - 1) / BM;
   a.tiles_j = (a.J + CN - 1) / CN;
-  const int stages = (a.parts * ((a.R + GU_BK - 1) / GU_BK) + KG - 1) / KG;
+  const int stages = ((a.R + GU_BK - 1) / GU_BK + KG - 1) / KG;
   a.steps = (stages + a.splits - 1) / a.splits;
   const int64_t groups = (int64_t)a.tiles_i * a.tiles_j * a.splits;
-  hipLaunchKernelGGL((gu_tile_kernel<AROW, BROW, WI, WJ, SI, SJ, KG, GATE, OCC>), dim3((unsigned)groups),
+  hipLaunchKernelGGL((gu_tile_kernel<AROW, BROW, WI, WJ, SI, SJ, KG, PARTS, GATE, OCC>), dim3((unsigned)groups),
                      dim3(WI * WJ * KG * 64), 0, stream, a);
   return hipGetLastError();
 }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gu_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+
+// v of the lane that a DPP control names, every lane having one.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+
+constexpr int GS_NT = 2;       // non-temporal: weights are read once
 
 // ---------------------------------------------------------------------------
 // Few rows: the weights stream through registers
@@ -413,100 +418,159 @@ struct StreamArgs {
   const uint16_t* x;
   const uint16_t* w;
   int64_t K;
-  int M, F;
+  int M, F, blocks;        // blocks of 8 columns of h of a workgroup
   void* h;
   int h_bf16;
   void* pre;
   int pre_bf16;
 };
 
-// A wave takes 16 gate columns and the 16 up columns that belong to them, and
-// its share of K; NB blocks of 16 rows; D chunks of 64 k in flight.
-template <int NB, int D>
-__global__ __launch_bounds__(512) void gu_stream_kernel(StreamArgs p) {
-  __shared__ float s_part[8][NB * 2 * 4][64];
+// A tile is 8 gate rows of w13 and the 8 up rows that belong to them, 256 k deep:
+// 8 KiB, loaded by one wave in runs of 512 bytes and turned into the matrix
+// unit's order through LDS of the wave's own (the operand's lanes lie across the
+// rows, 16 bytes each: loaded that way, every lane is a cache access of its own,
+// and the L1 takes one a cycle).  A workgroup's waves share K, in units of 256;
+// blocks of 8 columns of h follow one another.  NB blocks of 16 rows of x, which
+// come along with the tiles; two tiles in flight per wave, or one where 32 rows
+// of x fill the registers.
+constexpr int GS_WAVES = 8;
+
+template <int NB>
+__global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) {
+  constexpr int D = 2;
+  __shared__ __attribute__((aligned(512))) uint8_t s_tile[GS_WAVES][8192];
+  __shared__ float s_part[2][GS_WAVES][NB * 4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
   const int n16 = lane & 15, g = lane >> 4;
-  const int64_t K = p.K;
-  const int n0 = blockIdx.x * 16;
-  const int n = min(n0 + n16, p.F - 1);
-  const uint16_t* wg = p.w + (int64_t)n * K + g * 8;
-  const uint16_t* wu = wg + (int64_t)p.F * K;
-  const uint16_t* xr[NB];
-  bool on[NB];
+  const int K = (int)p.K;
+  const int total = (K + 255) >> 8;
+  const int j0 = blockIdx.x * p.blocks * 8;                 // first column of h
+  const int cols = min(p.blocks * 8, p.F - j0);
+  const int blocks = (cols + 7) >> 3;
+
+  // load i of a tile: rows 2 i and 2 i + 1, a half of the wave each; segment c of
+  // row r at place c ^ r of its 32
+  const int half = lane >> 5, seg = lane & 31;
+  const uint32_t wvo = (uint32_t)half * (uint32_t)(K * 2) + seg * 16;
+  uint8_t* tile = s_tile[wave];
+  uint32_t xvo[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    on[b] = b * 16 + n16 < p.M;
-    xr[b] = p.x + (int64_t)(on[b] ? b * 16 + n16 : 0) * K + g * 8;
-  }
-  struct Chunk {
-    u32x4_t w[2][2], x[NB][2];
+  for (int b = 0; b < NB; ++b) xvo[b] = b * 16 + n16 < p.M ? (uint32_t)((b * 16 + n16) * K * 2 + g * 16) : kLaneOob;
+  const __amdgpu_buffer_rsrc_t xr = gu_rsrc(p.x, (int64_t)p.M * K * 2);
+
+  struct Slot {
+    u32x4_t w[8], x[NB][8];
   };
-  const int chunks = (int)((K + 63) >> 6);
-  const int share = (chunks + 7) / 8;
-  const int first = wave * share, count = min(share, chunks - first);
-  auto load = [&](int v, Chunk& q) __attribute__((always_inline)) {
+  Slot ring[D];
+  int lu = wave, lb = 0;                                    // unit and block of the next load
+  auto load = [&](Slot& q) __attribute__((always_inline)) {
+    const int left = lb < blocks ? (cols - lb * 8) : 0;     // columns from here on
+    const uint16_t* base = p.w + (int64_t)(j0 + lb * 8) * K;
+    const uint32_t bytes = (uint32_t)max(0, min(left, 8)) * (uint32_t)(K * 2);
+    const __amdgpu_buffer_rsrc_t gr = gu_rsrc(base, bytes), ur = gu_rsrc(base + (int64_t)p.F * K, bytes);
+    const uint32_t wo = lu * 256 + seg * 8 < K ? wvo : kLaneOob;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int64_t k = (int64_t)(first + v) * 64 + s * 32;
-      const bool in = k + g * 8 < K;
-      const int64_t at = in ? k : 0;
-      q.w[0][s] = in ? *reinterpret_cast<const u32x4_t*>(wg + at) : u32x4_t{0, 0, 0, 0};
-      q.w[1][s] = in ? *reinterpret_cast<const u32x4_t*>(wu + at) : u32x4_t{0, 0, 0, 0};
+    for (int i = 0; i < 8; ++i)
+      q.w[i] = __builtin_amdgcn_raw_buffer_load_b128(i < 4 ? gr : ur, wo, (i & 3) * K * 4 + lu * 512, GS_NT);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        q.x[b][s] = in && on[b] ? *reinterpret_cast<const u32x4_t*>(xr[b] + at) : u32x4_t{0, 0, 0, 0};
-    }
-  };
-  f32x4_t acc[NB][2];
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-  for (int b = 0; b < NB; ++b) acc[b][0] = acc[b][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  Chunk ring[D];
-#pragma unroll
-  for (int i = 0; i < D; ++i)
-    if (i < count) load(i, ring[i]);
-  for (int v = 0; v < count; v += D) {
-#pragma unroll
-    for (int i = 0; i < D; ++i)
-      if (v + i < count) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            acc[b][0] = gu_mfma(ring[i].x[b][s], ring[i].w[0][s], acc[b][0]);
-            acc[b][1] = gu_mfma(ring[i].x[b][s], ring[i].w[1][s], acc[b][1]);
-          }
-        if (v + i + D < count) load(v + i + D, ring[i]);
+      for (int s = 0; s < 8; ++s) {
+        const uint32_t xo = lu * 256 + s * 32 + g * 8 < K ? xvo[b] : kLaneOob;
+        q.x[b][s] = __builtin_amdgcn_raw_buffer_load_b128(xr, xo, lu * 512 + s * 64, 0);
       }
-  }
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s_part[wave][b * 8 + i][lane] = acc[b][i >> 2][i & 3];
-  __syncthreads();
-  for (int o = threadIdx.x; o < NB * 4 * 64; o += 512) {
-    const int l = o & 63, i = (o >> 6) & 3, b = o >> 8;
-    const int row = b * 16 + (l >> 4) * 4 + i, col = n0 + (l & 15);
-    if (row >= p.M || col >= p.F) continue;
-    float gt = 0.f, ut = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      gt += s_part[w][b * 8 + i][l];
-      ut += s_part[w][b * 8 + 4 + i][l];
+    lu += waves;
+    if (lu >= total) {
+      lu = wave;
+      ++lb;
     }
-    const float h = gu_silu(gt) * ut;
-    const int64_t at = (int64_t)row * p.F + col;
-    if (p.h_bf16) reinterpret_cast<uint16_t*>(p.h)[at] = f32_to_bf16_rne(h);
-    else reinterpret_cast<float*>(p.h)[at] = h;
-    if (p.pre) {
-      const int64_t pa = (int64_t)row * 2 * p.F + col;
-      if (p.pre_bf16) {
-        reinterpret_cast<uint16_t*>(p.pre)[pa] = f32_to_bf16_rne(gt);
-        reinterpret_cast<uint16_t*>(p.pre)[pa + p.F] = f32_to_bf16_rne(ut);
-      } else {
-        reinterpret_cast<float*>(p.pre)[pa] = gt;
-        reinterpret_cast<float*>(p.pre)[pa + p.F] = ut;
+  };
+#pragma unroll
+  for (int i = 0; i < D; ++i) {
+    load(ring[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  f32x4_t acc[NB];
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
+  auto join = [&](int blk) __attribute__((always_inline)) {
+    float (*part)[NB * 4][64] = s_part[blk & 1];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[wave][b * 4 + i][lane] = acc[b][i];
+    clear();
+    lds_barrier();
+    const int live = min(cols - blk * 8, 8);
+    // eight lanes to a column's row: one a wave
+    for (int o = threadIdx.x >> 3; o < NB * 128; o += blockDim.x >> 3) {
+      const int w = threadIdx.x & 7, c = o & 7, row = o >> 3;
+      float gt = 0.f, ut = 0.f;
+      if (w < min(waves, total)) {
+        const float* from = &part[w][(row >> 4) * 4 + (row & 3)][((row >> 2) & 3) * 16 + c];
+        gt = from[0];
+        ut = from[8];
+      }
+      gt += dpp_add<0xB1>(gt), ut += dpp_add<0xB1>(ut);
+      gt += dpp_add<0x4E>(gt), ut += dpp_add<0x4E>(ut);
+      gt += dpp_add<0x141>(gt), ut += dpp_add<0x141>(ut);
+      if (w != 0 || row >= p.M || c >= live) continue;
+      const float h = gu_silu(gt) * ut;
+      const int col = j0 + blk * 8 + c;
+      const int64_t at = (int64_t)row * p.F + col;
+      if (p.h_bf16) reinterpret_cast<uint16_t*>(p.h)[at] = f32_to_bf16_rne(h);
+      else reinterpret_cast<float*>(p.h)[at] = h;
+      if (p.pre) {
+        const int64_t pa = (int64_t)row * 2 * p.F + col;
+        if (p.pre_bf16) {
+          reinterpret_cast<uint16_t*>(p.pre)[pa] = f32_to_bf16_rne(gt);
+          reinterpret_cast<uint16_t*>(p.pre)[pa + p.F] = f32_to_bf16_rne(ut);
+        } else {
+          reinterpret_cast<float*>(p.pre)[pa] = gt;
+          reinterpret_cast<float*>(p.pre)[pa + p.F] = ut;
+        }
+      }
+    }
+  };
+
+  // the tiles of this wave: `per` units of each block.  Every wave takes part in
+  // every join, also where a block's units do not reach it.
+  const int per = wave < total ? (total - wave + waves - 1) / waves : 0;
+  if (per == 0) {
+    for (int b = 0; b < blocks; ++b) join(b);
+    return;
+  }
+  int u = 0, blk = 0;
+  while (blk < blocks) {
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      Slot& q = ring[i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int row = 2 * c + half;
+        *reinterpret_cast<u32x4_t*>(tile + row * 512 + ((seg ^ row) << 4)) = q.w[c];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(tile + n16 * 512 + (((s * 4 + g) ^ n16) << 4));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[b] = gu_mfma(q.x[b][s], w, acc[b]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      load(q);
+      __builtin_amdgcn_sched_barrier(0);
+      if (++u == per) {
+        u = 0;
+        if (blk < blocks) join(blk);
+        ++blk;
       }
     }
   }
@@ -600,52 +664,143 @@ static unsigned gu_grid(int64_t threads) {
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles of 64 x 64 (gate and up: 64 x 32 columns of h), the smallest that any
-// launch takes, times the most shares of a sum.
+// The smallest tiles that a launch takes (shares of a sum add workgroups only
+// where they are few).
 int64_t gate_up_workgroups(int32_t M, int32_t N, int32_t K) {
-  const int64_t fwd = ceil_div(M, 64) * ceil_div(N / 2, 32), dx = ceil_div(M, 64) * ceil_div(K, 128);
+  const int64_t fwd = ceil_div(M, 32) * ceil_div(N / 2, 32), dx = ceil_div(M, 64) * ceil_div(K, 128);
   const int64_t dw = ceil_div(N, 128) * ceil_div(K, 128);
   const int64_t most = fwd > dx ? fwd : dx;
   return most > dw ? most : dw;
+}
+
+// The tile kernel's instances, and what a stage of 64 r costs them when all the
+// workgroups that fit the CUs run (us, from 4,096 x 4,096 products; a stage of KG
+// groups counts KG).  A product takes the instance, and the shares of its sum,
+// of the least estimate: whole rounds of workgroups, and for shares the sums
+// written, read and added at 4.5 TB/s in one more launch.  The sides measured, us:
+//   gate/up, K 4,096, 2,048 columns of h: 64 rows 32 x 64 tiles 19.8, 64 x 64 22.7,
+//     128 x 128 38.5; 256 rows 64 x 64 23.7, 128 x 128 39.7; 1,024 rows 128 x 128
+//     43.8, 128 x 256 64, 64 x 64 over 64; 2,048 rows 128 x 256 67.8, 256 x 256
+//     89.9; 4,096 rows 256 x 256 109.8, 128 x 256 131.2
+//   dx of 1,237 rows (2,560 columns, sum over 2,832): 128 x 128 36.8, 256 x 256
+//     in four shares 37.5 and their sum
+//   dw13 of 2,832 x 2,560 over 1,237 rows: 256 x 128 28.5, 256 x 256 39.7
+struct TileConfig {
+  int bm, bn, kg, fit;    // rows, columns (gate and up: of w13), groups, workgroups that run at once
+  float stage;
+};
+
+struct TilePlan {
+  int config, splits;
+};
+
+template <int COUNT>
+static TilePlan tile_plan(const TileConfig (&configs)[COUNT], int gate, int64_t I, int64_t J, int64_t R,
+                          int most_splits) {
+  TilePlan best = {0, 1};
+  float least = 0.f;
+  for (int c = 0; c < COUNT; ++c) {
+    const TileConfig& t = configs[c];
+    const int64_t tiles = ceil_div(I, t.bm) * ceil_div(J, gate ? t.bn / 2 : t.bn);
+    const int64_t stages = ceil_div(ceil_div(R, GU_BK), t.kg);
+    for (int splits = 1; splits <= most_splits && splits <= stages; splits *= 2) {
+      if (splits > 1 && tiles * splits > 2 * t.fit) break;
+      float us = (float)ceil_div(tiles * splits, t.fit) * (3.f + (float)(ceil_div(stages, splits) * t.kg) * t.stage);
+      if (splits > 1) us += 4.f + (float)splits * (float)I * (float)J * (8.f / 4.5e6f);
+      if (least == 0.f || us < least) {
+        least = us;
+        best = {c, splits};
+      }
+    }
+  }
+  return best;
+}
+
+static const TileConfig kForward[] = {{256, 256, 1, 256, 1.65f}, {128, 256, 1, 256, 1.f}, {128, 128, 2, 256, .6f},
+                                      {64, 64, 4, 256, .3f}, {32, 64, 4, 256, .25f}};
+static const TileConfig kDx[] = {{256, 256, 1, 256, 1.7f}, {128, 256, 1, 256, .97f}, {128, 128, 2, 256, .6f},
+                                 {64, 128, 1, 768, .7f}};
+static const TileConfig kDx3[] = {{128, 256, 1, 256, 2.2f}, {64, 256, 1, 256, 1.25f}, {64, 128, 1, 512, 1.3f}};
+static const TileConfig kDw[] = {{256, 256, 1, 256, 1.7f}, {256, 128, 1, 256, 1.02f}, {128, 128, 2, 256, .6f}};
+static const TileConfig kDw3[] = {{128, 256, 1, 256, 2.3f}};
+constexpr int GU_SPLITS = 16;
+
+static hipError_t launch_forward(int config, const TileArgs& a, hipStream_t s) {
+  switch (config) {
+    case 0: return launch_tiles<false, false, 2, 4, 8, 4, 1, 1, true, 2>(a, s);
+    case 1: return launch_tiles<false, false, 2, 4, 4, 4, 1, 1, true, 2>(a, s);
+    case 2: return launch_tiles<false, false, 2, 2, 4, 4, 2, 1, true, 2>(a, s);
+    case 3: return launch_tiles<false, false, 4, 1, 1, 4, 4, 1, true, 4>(a, s);
+    default: return launch_tiles<false, false, 2, 1, 1, 4, 4, 1, true, 2>(a, s);
+  }
+}
+
+static hipError_t launch_dx(int parts, int config, const TileArgs& a, hipStream_t s) {
+  if (parts == 1) switch (config) {
+    case 0: return launch_tiles<false, true, 2, 4, 8, 4, 1, 1, false, 2>(a, s);
+    case 1: return launch_tiles<false, true, 2, 4, 4, 4, 1, 1, false, 2>(a, s);
+    case 2: return launch_tiles<false, true, 2, 2, 4, 4, 2, 1, false, 2>(a, s);
+    default: return launch_tiles<false, true, 2, 2, 2, 4, 1, 1, false, 3>(a, s);
+  }
+  switch (config) {
+    case 0: return launch_tiles<false, true, 2, 4, 4, 4, 1, 3, false, 2>(a, s);
+    case 1: return launch_tiles<false, true, 2, 4, 2, 4, 1, 3, false, 2>(a, s);
+    default: return launch_tiles<false, true, 2, 2, 2, 4, 1, 3, false, 2>(a, s);
+  }
+}
+
+static hipError_t launch_dw(int parts, int config, const TileArgs& a, hipStream_t s) {
+  if (parts == 3) return launch_tiles<true, true, 2, 4, 4, 4, 1, 3, false, 2>(a, s);
+  switch (config) {
+    case 0: return launch_tiles<true, true, 2, 4, 8, 4, 1, 1, false, 2>(a, s);
+    case 1: return launch_tiles<true, true, 4, 2, 4, 4, 1, 1, false, 2>(a, s);
+    default: return launch_tiles<true, true, 2, 2, 4, 4, 2, 1, false, 2>(a, s);
+  }
 }
 
 hipError_t launch_gate_up(const uint16_t* x, const uint16_t* w, int32_t M, int32_t N, int32_t K, void* h, int h_bf16,
                           void* pre, int pre_bf16, hipStream_t stream) {
   const int F = N / 2;
   if (M <= 32) {
-    StreamArgs a = {x, w, K, M, F, h, h_bf16, pre, pre_bf16};
-    if (M <= 16) hipLaunchKernelGGL((gu_stream_kernel<1, 4>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((gu_stream_kernel<2, 3>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
+    const int all = (F + 7) / 8, per = (all + GU_CUS - 1) / GU_CUS;
+    StreamArgs a = {x, w, K, M, F, per, h, h_bf16, pre, pre_bf16};
+    const int units = (K + 255) / 256, waves = units < GS_WAVES ? units : GS_WAVES;
+    const dim3 grid((all + per - 1) / per), block(waves * 64);
+    if (M <= 16) hipLaunchKernelGGL(gu_stream_kernel<1>, grid, block, 0, stream, a);
+    else hipLaunchKernelGGL(gu_stream_kernel<2>, grid, block, 0, stream, a);
     return hipGetLastError();
   }
   TileArgs a = {};
   a.a = x; a.b = w; a.lda = K; a.ldb = K;
   a.I = M; a.J = F; a.R = K;
-  a.parts = 1; a.splits = 1;
+  a.splits = 1;
   a.out = h; a.out_bf16 = h_bf16; a.pre = pre; a.pre_bf16 = pre_bf16;
-  const int64_t large = ceil_div(M, 256) * ceil_div(F, 128), mid = ceil_div(M, 128) * ceil_div(F, 64);
-  if (large >= GU_CUS / 2) return launch_tiles<false, false, 2, 4, 8, 4, 1, true, 2>(a, stream);
-  if (mid >= GU_CUS) return launch_tiles<false, false, 2, 2, 4, 4, 1, true, 2>(a, stream);
-  return launch_tiles<false, false, 4, 1, 1, 4, 4, true, 4>(a, stream);
+  return launch_forward(tile_plan(kForward, 1, M, F, K, 1).config, a, stream);
 }
 
-// The plan of the gradients: bf16 parts of d, and shares of the sum of dx.
+// The plan of the gradients: bf16 parts of d, and each product's instance and
+// shares, whose f32 sums lie behind d (dx's are added up before dw13's begin).
 struct BwdPlan {
-  int parts, splits;
+  int parts;
+  TilePlan dx, dw;
   int64_t d_bytes, ws_bytes;
 };
 
 static BwdPlan bwd_plan(int32_t M, int32_t N, int32_t K, int want_dx, int dx_bf16, int want_dw, int dw_bf16) {
-  BwdPlan p;
+  BwdPlan p = {};
   p.parts = (want_dx && !dx_bf16) || (want_dw && !dw_bf16) ? 3 : 1;
   p.d_bytes = ((int64_t)p.parts * M * N * 2 + 255) / 256 * 256;
-  p.splits = 1;
+  int64_t sums = 0;
   if (want_dx) {
-    const int64_t tiles = ceil_div(M, 64) * ceil_div(K, 128);
-    const int64_t stages = ceil_div((dx_bf16 ? 1 : 3) * ceil_div(N, GU_BK), 2);
-    while (p.splits < 16 && tiles * p.splits * 2 <= GU_CUS && stages >= 4 * p.splits) p.splits *= 2;
+    p.dx = dx_bf16 ? tile_plan(kDx, 0, M, K, N, GU_SPLITS) : tile_plan(kDx3, 0, M, K, N, GU_SPLITS);
+    if (p.dx.splits > 1) sums = (int64_t)p.dx.splits * M * K * 4;
   }
-  p.ws_bytes = p.d_bytes + (p.splits > 1 ? (int64_t)p.splits * M * K * 4 : 0);
+  if (want_dw) {
+    p.dw = dw_bf16 ? tile_plan(kDw, 0, N, K, M, GU_SPLITS) : tile_plan(kDw3, 0, N, K, M, GU_SPLITS);
+    const int64_t bytes = p.dw.splits > 1 ? (int64_t)p.dw.splits * N * K * 4 : 0;
+    sums = bytes > sums ? bytes : sums;
+  }
+  p.ws_bytes = p.d_bytes + sums;
   return p;
 }
 
@@ -675,40 +830,31 @@ hipError_t launch_gate_up_bwd(const void* dh, int dh_bf16, const uint16_t* x, co
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
+  float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.d_bytes);
+  // out of the product, or of its shares
+  auto product = [&](TileArgs a, const TilePlan& t, bool is_dx, int parts, void* out, int out_bf16) {
+    a.part_stride = (int64_t)M * N;
+    a.splits = t.splits;
+    a.out = t.splits > 1 ? sums : out;
+    a.out_bf16 = t.splits > 1 ? 0 : out_bf16;
+    hipError_t e = is_dx ? launch_dx(parts, t.config, a, stream) : launch_dw(parts, t.config, a, stream);
+    if (e != hipSuccess || t.splits == 1) return e;
+    const int64_t n = (int64_t)a.I * a.J;
+    hipLaunchKernelGGL(gu_join_kernel, dim3(gu_grid(n / 8)), dim3(256), 0, stream, sums, t.splits, n, out, out_bf16);
+    return hipGetLastError();
+  };
   if (dx) {
     TileArgs a = {};
     a.a = d; a.b = w; a.lda = N; a.ldb = K;
     a.I = M; a.J = K; a.R = N;
-    a.parts = dx_bf16 ? 1 : 3; a.part_stride = (int64_t)M * N;
-    a.splits = pl.splits;
-    a.out = dx; a.out_bf16 = dx_bf16;
-    if (pl.splits > 1) {
-      a.out = static_cast<uint8_t*>(ws) + pl.d_bytes;
-      a.out_bf16 = 0;
-    }
-    const int64_t large = ceil_div(M, 256) * ceil_div(K, 256), mid = ceil_div(M, 128) * ceil_div(K, 128);
-    if (pl.splits == 1 && large >= GU_CUS / 2) err = launch_tiles<false, true, 2, 4, 8, 4, 1, false, 2>(a, stream);
-    else if (pl.splits == 1 && mid >= GU_CUS) err = launch_tiles<false, true, 2, 2, 4, 4, 1, false, 2>(a, stream);
-    else err = launch_tiles<false, true, 2, 2, 2, 4, 2, false, 2>(a, stream);
+    err = product(a, pl.dx, true, dx_bf16 ? 1 : 3, dx, dx_bf16);
     if (err != hipSuccess) return err;
-    if (pl.splits > 1) {
-      const int64_t n = (int64_t)M * K;
-      hipLaunchKernelGGL(gu_join_kernel, dim3(gu_grid(n / 8)), dim3(256), 0, stream, static_cast<const float*>(a.out),
-                         pl.splits, n, dx, dx_bf16);
-      err = hipGetLastError();
-      if (err != hipSuccess) return err;
-    }
   }
   if (dw) {
     TileArgs a = {};
     a.a = d; a.b = x; a.lda = N; a.ldb = K;
     a.I = N; a.J = K; a.R = M;
-    a.parts = dw_bf16 ? 1 : 3; a.part_stride = (int64_t)M * N;
-    a.splits = 1;
-    a.out = dw; a.out_bf16 = dw_bf16;
-    const int64_t large = ceil_div(N, 256) * ceil_div(K, 256);
-    if (large >= GU_CUS / 2) err = launch_tiles<true, true, 2, 4, 8, 4, 1, false, 2>(a, stream);
-    else err = launch_tiles<true, true, 2, 2, 4, 4, 1, false, 2>(a, stream);
+    err = product(a, pl.dw, false, dw_bf16 ? 1 : 3, dw, dw_bf16);
   }
   return err;
 }

@@ -89,13 +89,14 @@ def test_workspace_sizes():
         assert f(s["M"], s["N"], s["K"]) == 0, kw
     assert f(4, 32, 64, None, None) == 0 and f(4, 32, 64, 3, None) == 0
     assert f((1 << 32) + 4, 32, 64) == 0
-    # d in bf16 where every wanted gradient is bf16, in three parts where one is f32
-    assert f(256, 512, 128, None, moe.BF16) == 256 * 512 * 2
-    assert f(256, 512, 128, None, moe.F32) == 3 * 256 * 512 * 2
+    # d in bf16 where every wanted gradient is bf16, in three parts where one is
+    # f32; behind it the shares of a sum, where few tiles have a long one
+    assert f(256, 512, 128, None, moe.BF16) >= 256 * 512 * 2
+    assert f(256, 512, 128, None, moe.F32) >= 3 * 256 * 512 * 2
     assert f(256, 512, 128, moe.BF16, moe.F32) >= 3 * 256 * 512 * 2
-    # shares of dx's sums only where few tiles have a long sum
     assert f(4096, 4096, 4096, moe.BF16, moe.BF16) == 4096 * 4096 * 2
-    assert f(16, 4096, 4096, moe.BF16, None) > 16 * 4096 * 2
+    assert f(4096, 4096, 4096, moe.F32, None) == 3 * 4096 * 4096 * 2
+    assert f(16, 4096, 4096, moe.BF16, None) >= 16 * 4096 * 2 + 2 * 16 * 4096 * 4
 
 
 def test_binding_rejects_host_tensors_and_wrong_types():
