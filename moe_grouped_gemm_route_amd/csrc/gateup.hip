@@ -29,7 +29,10 @@ __device__ __forceinline__ f32x4_t gu_mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
                                                  0, 0, 0);
 }
 
-__device__ __forceinline__ float gu_silu(float z) { return z / (1.0f + __expf(-z)); }
+// 1 / (1 + e^-z) by the reciprocal instruction (1 ulp; the division's correct
+// rounding costs ten more instructions, 8 us of 4,096 x 4,096 sums' epilogue).
+__device__ __forceinline__ float gu_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+__device__ __forceinline__ float gu_silu(float z) { return z * gu_sigmoid(z); }
 
 __device__ __forceinline__ void gu_store8(void* p, bool bf16, int64_t i, const float (&v)[8]) {
   if (bf16) {
@@ -40,6 +43,17 @@ __device__ __forceinline__ void gu_store8(void* p, bool bf16, int64_t i, const f
     q[0] = make_float4(v[0], v[1], v[2], v[3]);
     q[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gu_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+
+__device__ __forceinline__ void gu_store4(void* p, bool bf16, int64_t i, f32x4_t v) {
+  if (bf16)
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  else
+    *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(p) + i) = v;
 }
 
 // ---------------------------------------------------------------------------
@@ -65,13 +79,14 @@ struct TileArgs {
 // r contiguous: rows of 128 bytes, 16-byte segment c of row q at place
 // c ^ swizzle(q), so that the eight lanes that are served together read eight
 // different segments of the 128 bytes that their rows share in the banks.
-// r as the row: rows of DIM * 2 bytes, segment c of row r at c ^ 4 (r & 3), so
-// that the four rows of a transposing read lie in different 64-byte quarters.
+// r as the row: rows of DIM * 2 bytes, segment c of row r at c ^ swizzle(r): 32
+// lanes of a transposing read take 32 bytes of eight rows, r = 0 .. 3 and 8 .. 11
+// of a step, which then lie in different banks.
 //
-// The columns of out that two neighbouring 16-column subtiles (PAIR: the B
-// operand) cover are dealt so that a lane's results are eight consecutive ones:
-// subtile s, row q of the operand is column (q >> 2) * 8 + s * 4 + (q & 3) of
-// the pair's 32.
+// PAIR (the B operand with r contiguous): the columns of out that two
+// neighbouring 16-column subtiles cover are dealt so that a lane's results are
+// eight consecutive ones: subtile s, row q of the operand is column
+// (q >> 2) * 8 + s * 4 + (q & 3) of the pair's 32.
 template <bool RROW, int DIM, int WAVES, bool PAIR>
 struct Operand {
   static constexpr int BYTES = DIM * GU_BK * 2;
@@ -82,7 +97,7 @@ struct Operand {
   static_assert(!RROW || (DIM >= 128 && DIM <= 512), "rows of 256 bytes at least, a load per two rows at most");
 
   static __device__ __forceinline__ int swizzle(int row) {
-    return RROW ? (row & 3) << 2 : PAIR ? (row & 3) | ((row >> 3) & 1) << 2 : row & 7;
+    return RROW ? ((row & 3) | ((row >> 3) & 1) << 2) << 1 : PAIR ? (row & 3) | ((row >> 3) & 1) << 2 : row & 7;
   }
   // LDS row and source segment of this lane in load j of a wave
   static __device__ __forceinline__ int row(int wave, int j) {
@@ -100,9 +115,8 @@ struct Operand {
     } else {
       // 16 lanes read four r of 16 columns, lane q four columns of row q / 4,
       // and get one column's four r
-      const int piece = q & 3;
-      const int seg = base / 8 + (PAIR ? (sub >> 1) * 4 + piece : sub * 2 + (piece >> 1));
-      const int half = PAIR ? sub & 1 : piece & 1;
+      const int seg = base / 8 + sub * 2 + ((q & 3) >> 1);
+      const int half = q & 1;
       u32x4_t v;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -145,17 +159,24 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 // loads have a whole stage to land in, and the matrix pipes do not run dry at
 // the barrier.  The wait before it is a full one: direct-to-LDS loads are not
 // counted as still on their way.
-template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, int OCC>
+//
+// REGS: the loads go through registers instead, two stages ahead.  The wait for
+// a register is counted by the compiler, so a stage has two stages' time to
+// land; tiles whose stages are short need that (a stage of 128 x 128 x 128 takes
+// 0.5 us of matrix instructions, a load 0.9).  Where the sums fill the registers
+// (256 x 256) the loads go to LDS.
+template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, bool REGS, int OCC>
 __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArgs p) {
   constexpr int NW = WI * WJ;
   constexpr int BM = WI * SI * 16, BN = WJ * SJ * 16;
   typedef Operand<AROW, BM, NW, false> OpA;
-  typedef Operand<BROW, BN, NW, true> OpB;
+  typedef Operand<BROW, BN, NW, !BROW> OpB;
   constexpr int A_BYTES = PARTS * OpA::BYTES;
   constexpr int SLICE = A_BYTES + OpB::BYTES;
   constexpr int STAGE = KG * SLICE;
   constexpr int JOIN = (KG - 1) * BM * BN * 4;
   constexpr int LDS = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
+  static_assert(!GATE || !BROW, "w13's rows are columns of out");
   static_assert(!GATE || SJ == 4, "a wave holds a pair of gate and a pair of up subtiles");
   __shared__ __attribute__((aligned(1024))) uint8_t s_all[LDS];
 
@@ -241,6 +262,42 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
     load_b(buf);
     at += KG;
   };
+  // The same through registers: a stage's share of this wave, and its place.
+  struct Held {
+    u32x4_t a[PARTS * OpA::LOADS], b[OpB::LOADS];
+  };
+  auto fetch = [&](Held& h) __attribute__((always_inline)) {
+    const bool live = at < stages;
+    const int r0 = live ? at * GU_BK : 0;
+    const int left = p.R - r0;
+    const uint32_t abytes = !live ? 0 : AROW ? (uint32_t)((min(left, GU_BK) * p.lda - i0) * 2) : OPEN;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      const __amdgpu_buffer_rsrc_t rs =
+          gu_rsrc(p.a + q * p.part_stride + (AROW ? (int64_t)r0 * p.lda + i0 : (int64_t)i0 * p.lda + r0), abytes);
+#pragma unroll
+      for (int j = 0; j < OpA::LOADS; ++j)
+        h.a[q * OpA::LOADS + j] =
+            __builtin_amdgcn_raw_buffer_load_b128(rs, AROW || aseg[j] < left ? avo[j] : kLaneOob, 0, 0);
+    }
+    const uint16_t* base = p.b + (BROW ? (int64_t)r0 * p.ldb + j0 : (int64_t)j0 * p.ldb + r0);
+    const uint32_t bbytes = !live ? 0 : BROW ? (uint32_t)((min(left, GU_BK) * p.ldb - j0) * 2) : OPEN;
+    const __amdgpu_buffer_rsrc_t rs = gu_rsrc(base, bbytes);
+    const __amdgpu_buffer_rsrc_t ru = GATE ? gu_rsrc(base + (int64_t)p.J * p.ldb, bbytes) : rs;
+#pragma unroll
+    for (int j = 0; j < OpB::LOADS; ++j)
+      h.b[j] = __builtin_amdgcn_raw_buffer_load_b128(up[j] ? ru : rs, BROW || bseg[j] < left ? bvo[j] : kLaneOob, 0, 0);
+    at += KG;
+  };
+  constexpr int PUTS = PARTS * OpA::LOADS + OpB::LOADS;
+  auto put = [&](const Held& h, int buf, int k) __attribute__((always_inline)) {
+    uint8_t* to = s_all + buf * STAGE + kg * SLICE + lane * 16;
+    if (k < PARTS * OpA::LOADS)
+      *reinterpret_cast<u32x4_t*>(to + k / OpA::LOADS * OpA::BYTES + (wave * OpA::LOADS + k % OpA::LOADS) * 1024) = h.a[k];
+    else
+      *reinterpret_cast<u32x4_t*>(to + A_BYTES + (wave * OpB::LOADS + k - PARTS * OpA::LOADS) * 1024) =
+          h.b[k - PARTS * OpA::LOADS];
+  };
 
   f32x4_t acc[SI][SJ];
 #pragma unroll
@@ -266,46 +323,73 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
   };
 
   const int steps = p.steps;
-  load_stage(0);
-  load_stage(1);
-  vm_wait();
+  Held held[2];
+  if constexpr (REGS) {
+    fetch(held[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(held[1]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < PUTS; ++k) put(held[0], 0, k);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(held[0]);
+    __builtin_amdgcn_sched_barrier(0);
+  } else {
+    load_stage(0);
+    load_stage(1);
+    vm_wait();
+  }
   lds_barrier();
 #pragma unroll
   for (int s = 0; s < SJ; ++s) read_b(0, 0, s);
 #pragma unroll
   for (int q = 0; q < CA; ++q) read_a(0, q);
 
-#pragma unroll 1
-  for (int st = 0; st < steps; ++st) {
-    const int buf = st & 1;
+  // Stage st, from buffer buf.  `next`: what the registers hold of stage st + 1.
+  auto step = [&](int buf, Held& next) __attribute__((always_inline)) {
     // reads in the order of need: A of the first half and B of the second
-    // between them, then A of the second; two a group
+    // between them, then A of the second
     constexpr int READS = NQ - CA + SJ;
-    int done = 0;
+    constexpr int FRONT = NQ - HOLD;               // groups before the barrier
+    int done = 0, puts = 0;
 #pragma unroll
-    for (int q = 0; q < NQ - HOLD; ++q) {
+    for (int q = 0; q < FRONT; ++q) {
       __builtin_amdgcn_sched_barrier(0);
-      constexpr int FRONT = SP - CA;               // A reads of the first half
-      const int upto = q == NQ - HOLD - 1 ? READS : (READS * (q + 1) + NQ - HOLD - 1) / (NQ - HOLD);
+      constexpr int FIRST = SP - CA;               // A reads of the first half
+      const int upto = q == FRONT - 1 ? READS : (READS * (q + 1) + FRONT - 1) / FRONT;
 #pragma unroll
       for (int k = 0; k < READS; ++k) {
         if (k < done || k >= upto) continue;
-        constexpr int MIX = FRONT < SJ ? FRONT : SJ;
+        constexpr int MIX = FIRST < SJ ? FIRST : SJ;
         if (k < 2 * MIX) {
           if (k & 1) read_b(buf, 1, k >> 1);
           else read_a(buf, CA + (k >> 1));
         } else {
           const int rest = k - 2 * MIX;            // one of the two is done
-          if (FRONT > SJ) read_a(buf, CA + MIX + rest);
+          if (FIRST > SJ) read_a(buf, CA + MIX + rest);
           else if (rest < SJ - MIX) read_b(buf, 1, MIX + rest);
           else read_a(buf, SP + rest - (SJ - MIX));
         }
       }
       done = upto;
       mults(q);
+      if constexpr (REGS) {
+        // the next stage goes to the other buffer in the first half of the
+        // groups, and the registers take the stage after the one that follows it
+        constexpr int OVER = FRONT >= 4 ? FRONT / 2 : 1;
+        const int all = q + 1 >= OVER ? PUTS : PUTS * (q + 1) / OVER;
+#pragma unroll
+        for (int k = 0; k < PUTS; ++k)
+          if (k >= puts && k < all) put(next, buf ^ 1, k);
+        if (q == OVER - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          fetch(next);
+        }
+        puts = all;
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
-    vm_wait();
+    if (!REGS) vm_wait();
     lds_barrier();
     u32x4_t na[CA], nb[SJ];
     {
@@ -319,21 +403,34 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
 #pragma unroll
     for (int q = NQ - HOLD; q < NQ; ++q) {
       mults(q);
-      __builtin_amdgcn_sched_barrier(0);
-      if (q == NQ - HOLD) {
-        load_a(buf);
-        if (HOLD == 1) load_b(buf);
+      if constexpr (!REGS) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (q == NQ - HOLD) {
+          load_a(buf);
+          if (HOLD == 1) load_b(buf);
+        }
+        if (q == NQ - HOLD + 1) load_b(buf);
       }
-      if (q == NQ - HOLD + 1) load_b(buf);
       __builtin_amdgcn_sched_barrier(0);
     }
-    at += KG;
+    if (!REGS) at += KG;
 #pragma unroll
     for (int s = 0; s < SJ; ++s) fb[0][s] = nb[s];
 #pragma unroll
     for (int q = 0; q < CA; ++q) fa[q] = na[q];
+  };
+  if constexpr (REGS) {
+#pragma unroll 1
+    for (int st = 0; st < steps; st += 2) {
+      step(0, held[1]);
+      if (st + 1 >= steps) break;
+      step(1, held[0]);
+    }
+  } else {
+#pragma unroll 1
+    for (int st = 0; st < steps; ++st) step(st & 1, held[0]);
+    vm_wait();    // the loads past the last stage land before LDS is used again
   }
-  vm_wait();    // the loads past the last stage land before LDS is used again
 
   if constexpr (KG > 1) {
     lds_barrier();
@@ -373,19 +470,15 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < SJ / 2; ++c) {
-        const int col = j0 + wj * SJ * 16 + c * 32 + g * 8;
-        if (col >= p.J) continue;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = acc[a][2 * c + (i >> 2)][i & 3];
-        gu_store8(p.out, p.out_bf16, ((int64_t)split * p.I + row) * p.J + col, v);
+      for (int c = 0; c < SJ; ++c) {
+        const int col = j0 + wj * SJ * 16 + c * 16 + g * 4;
+        if (col < p.J) gu_store4(p.out, p.out_bf16, ((int64_t)split * p.I + row) * p.J + col, acc[a][c]);
       }
     }
   }
 }
 
-template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, int OCC>
+template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, bool REGS, int OCC>
 static hipError_t launch_tiles(TileArgs a, hipStream_t stream) {
   constexpr int BM = WI * SI * 16, BN = WJ * SJ * 16, CN = GATE ? BN / 2 : BN;
   a.tiles_i = (a.I + BM - 1) / BM;
@@ -393,13 +486,9 @@ static hipError_t launch_tiles(TileArgs a, hipStream_t stream) {
   const int stages = ((a.R + GU_BK - 1) / GU_BK + KG - 1) / KG;
   a.steps = (stages + a.splits - 1) / a.splits;
   const int64_t groups = (int64_t)a.tiles_i * a.tiles_j * a.splits;
-  hipLaunchKernelGGL((gu_tile_kernel<AROW, BROW, WI, WJ, SI, SJ, KG, PARTS, GATE, OCC>), dim3((unsigned)groups),
+  hipLaunchKernelGGL((gu_tile_kernel<AROW, BROW, WI, WJ, SI, SJ, KG, PARTS, GATE, REGS, OCC>), dim3((unsigned)groups),
                      dim3(WI * WJ * KG * 64), 0, stream, a);
   return hipGetLastError();
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t gu_rsrc(const void* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
 }
 
 // v of the lane that a DPP control names, every lane having one.
@@ -630,7 +719,7 @@ __global__ __launch_bounds__(256) void gu_act_bwd_kernel(const void* __restrict_
     gu_load8<HBF16>(dh, at - m * F, hv);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float s = 1.0f / (1.0f + __expf(-gt[c]));
+      const float s = gu_sigmoid(gt[c]);
       const float dg = hv[c] * ut[c] * s * (1.0f + gt[c] * (1.0f - s));
       ut[c] = hv[c] * gt[c] * s;
       gt[c] = dg;
@@ -727,34 +816,34 @@ constexpr int GU_SPLITS = 16;
 
 static hipError_t launch_forward(int config, const TileArgs& a, hipStream_t s) {
   switch (config) {
-    case 0: return launch_tiles<false, false, 2, 4, 8, 4, 1, 1, true, 2>(a, s);
-    case 1: return launch_tiles<false, false, 2, 4, 4, 4, 1, 1, true, 2>(a, s);
-    case 2: return launch_tiles<false, false, 2, 2, 4, 4, 2, 1, true, 2>(a, s);
-    case 3: return launch_tiles<false, false, 4, 1, 1, 4, 4, 1, true, 4>(a, s);
-    default: return launch_tiles<false, false, 2, 1, 1, 4, 4, 1, true, 2>(a, s);
+    case 0: return launch_tiles<false, false, 2, 4, 8, 4, 1, 1, true, false, 2>(a, s);
+    case 1: return launch_tiles<false, false, 2, 4, 4, 4, 1, 1, true, false, 2>(a, s);
+    case 2: return launch_tiles<false, false, 2, 2, 4, 4, 2, 1, true, false, 2>(a, s);
+    case 3: return launch_tiles<false, false, 4, 1, 1, 4, 4, 1, true, false, 4>(a, s);
+    default: return launch_tiles<false, false, 2, 1, 1, 4, 4, 1, true, false, 2>(a, s);
   }
 }
 
 static hipError_t launch_dx(int parts, int config, const TileArgs& a, hipStream_t s) {
   if (parts == 1) switch (config) {
-    case 0: return launch_tiles<false, true, 2, 4, 8, 4, 1, 1, false, 2>(a, s);
-    case 1: return launch_tiles<false, true, 2, 4, 4, 4, 1, 1, false, 2>(a, s);
-    case 2: return launch_tiles<false, true, 2, 2, 4, 4, 2, 1, false, 2>(a, s);
-    default: return launch_tiles<false, true, 2, 2, 2, 4, 1, 1, false, 3>(a, s);
+    case 0: return launch_tiles<false, true, 2, 4, 8, 4, 1, 1, false, false, 2>(a, s);
+    case 1: return launch_tiles<false, true, 2, 4, 4, 4, 1, 1, false, false, 2>(a, s);
+    case 2: return launch_tiles<false, true, 2, 2, 4, 4, 2, 1, false, false, 2>(a, s);
+    default: return launch_tiles<false, true, 2, 2, 2, 4, 1, 1, false, false, 3>(a, s);
   }
   switch (config) {
-    case 0: return launch_tiles<false, true, 2, 4, 4, 4, 1, 3, false, 2>(a, s);
-    case 1: return launch_tiles<false, true, 2, 4, 2, 4, 1, 3, false, 2>(a, s);
-    default: return launch_tiles<false, true, 2, 2, 2, 4, 1, 3, false, 2>(a, s);
+    case 0: return launch_tiles<false, true, 2, 4, 4, 4, 1, 3, false, false, 2>(a, s);
+    case 1: return launch_tiles<false, true, 2, 4, 2, 4, 1, 3, false, false, 2>(a, s);
+    default: return launch_tiles<false, true, 2, 2, 2, 4, 1, 3, false, false, 2>(a, s);
   }
 }
 
 static hipError_t launch_dw(int parts, int config, const TileArgs& a, hipStream_t s) {
-  if (parts == 3) return launch_tiles<true, true, 2, 4, 4, 4, 1, 3, false, 2>(a, s);
+  if (parts == 3) return launch_tiles<true, true, 2, 4, 4, 4, 1, 3, false, false, 2>(a, s);
   switch (config) {
-    case 0: return launch_tiles<true, true, 2, 4, 8, 4, 1, 1, false, 2>(a, s);
-    case 1: return launch_tiles<true, true, 4, 2, 4, 4, 1, 1, false, 2>(a, s);
-    default: return launch_tiles<true, true, 2, 2, 4, 4, 2, 1, false, 2>(a, s);
+    case 0: return launch_tiles<true, true, 2, 4, 8, 4, 1, 1, false, false, 2>(a, s);
+    case 1: return launch_tiles<true, true, 4, 2, 4, 4, 1, 1, false, false, 2>(a, s);
+    default: return launch_tiles<true, true, 2, 2, 4, 4, 2, 1, false, false, 2>(a, s);
   }
 }
 

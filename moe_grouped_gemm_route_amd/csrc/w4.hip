@@ -71,17 +71,6 @@ __device__ __forceinline__ f32x4_t w4_mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
                                                  0, 0, 0);
 }
 
-// What one chunk of CT column tiles and NB token blocks needs, as it lies in
-// memory.
-template <int S, int NB, int CT>
-struct W4Chunk {
-  u32x4_t codes[CT];
-  uint32_t scale[CT][S];     // f32 words, or bf16 pairs in the first (S + 1) / 2
-  uint32_t zero[CT];         // a byte per group
-  u32x4_t x[NB][4];
-  float factor;              // router weight of the chunk's expert
-};
-
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t w4_rsrc(const void* base, int64_t offset, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) + offset, 0,
                                            (int)bytes, 0x00020000);
@@ -128,212 +117,6 @@ __device__ __forceinline__ uint32_t w4_load_zeros(__amdgpu_buffer_rsrc_t r, uint
   return q;
 }
 
-// S: scale groups a 128-k chunk (4, 2, or 1: G >= 128).  NB: blocks of 16 / S
-// tokens.  CT: 16-column tiles of a wave, with ACT half of them gate and half
-// up columns.  SUM: a row sums the chosen experts of a token, whose chunks
-// follow one another.  SB: bf16 scales.  VEC: the scales and zero points of a
-// chunk start at whole words.  D: chunks in flight.
-//
-// Every load is a bounded buffer load: lanes and chunks that do not exist read
-// zeros and need no branch, which would make the compiler wait for the loads in
-// flight where the paths meet.
-template <int S, int NB, int CT, bool ACT, bool SUM, bool SB, bool VEC, int D>
-__global__ __launch_bounds__(512) void w4_gemv_kernel(W4Args p) {
-  constexpr int R = 4 / S;               // tokens a lane holds of a block
-  constexpr int TB = 16 / S * NB;        // tokens of a workgroup
-  constexpr int CW = (ACT ? CT / 2 : CT) * 16;
-  constexpr int SZ = SB ? 2 : 4;
-  extern __shared__ float s_part[];      // [waves][NB * CT * R][64]
-
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
-  const int n16 = lane & 15, g = lane >> 4;
-  const int cg = blockIdx.x % (uint32_t)p.col_groups;
-  const int rb = blockIdx.x / (uint32_t)p.col_groups;
-  const int64_t N = p.N, K = p.K, groups = p.groups;
-  const int cols = (int)(ACT ? N / 2 : N);
-  const int KC = (int)((K + 127) >> 7);
-  const bool pairs = p.ids != nullptr;
-
-  // first column of each tile, and its columns that exist
-  int64_t col0[CT];
-  int have[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    const int at = cg * CW + (ACT ? c % (CT / 2) : c) * 16;
-    have[c] = max(0, min(16, cols - at));
-    col0[c] = at + (ACT && c >= CT / 2 ? N / 2 : 0);
-  }
-  const uint32_t cvo = (uint32_t)(n16 * (K / 2) + g * 16);
-  const uint32_t svo = (uint32_t)(n16 * groups * SZ), zvo = (uint32_t)(n16 * groups);
-  uint32_t xvo[NB];                      // the row of x that this lane's operand row takes
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const bool mine = S == 1 || (S == 2 ? (g >> 1) == (n16 & 1) : g == (n16 & 3));
-    const int t = b * (16 / S) + n16 / S;
-    xvo[b] = mine && (pairs ? t == 0 : rb * TB + t < p.T) ? (uint32_t)(t * K * 2 + g * 64) : kLaneOob;
-  }
-  const int x_rows = pairs ? 1 : min(TB, p.T - rb * TB);
-
-  float acc[NB][CT][R];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int i = 0; i < R; ++i) acc[b][c][i] = 0.f;
-
-  const int total = (SUM ? p.k : 1) * KC;
-  const int share = (total + waves - 1) / waves;
-  const int first = wave * share, end = min(first + share, total);
-
-  // The next chunk to load: chunk kc of pair `pair`, whose expert is e.
-  int v = first, pair = SUM ? rb * p.k + first / KC : rb, kc = SUM ? first % KC : first;
-  int64_t e = 0, xrow = pairs ? 0 : (int64_t)rb * TB;
-  bool live = true;
-  float factor = 1.f;
-  auto expert = [&]() __attribute__((always_inline)) {
-    const int id = p.ids[pair];
-    live = (uint32_t)id < (uint32_t)p.E;
-    e = live ? id : 0;
-    xrow = p.x_pairs ? pair : pair / p.k;
-    if (SUM) factor = live ? p.weights[pair] : 0.f;
-  };
-  if (pairs && v < end) expert();
-
-  typedef W4Chunk<S, NB, CT> Chunk;
-  auto load = [&](Chunk& q) __attribute__((always_inline)) {
-    const bool on = live && v < end;
-    q.factor = factor;
-    const __amdgpu_buffer_rsrc_t xr = w4_rsrc(p.x, xrow * K * 2, on ? x_rows * K * 2 : 0);
-    const bool in = kc * 128 + g * 32 < K;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        q.x[b][s] = __builtin_amdgcn_raw_buffer_load_b128(xr, (in ? xvo[b] : kLaneOob) + s * 16, kc * 256, 0);
-    const int gi = S > 1 ? kc * S : (int)(((int64_t)kc * 128) >> p.gshift);
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const int64_t row = e * N + col0[c];
-      const int rows = on ? have[c] : 0;
-      q.codes[c] = __builtin_amdgcn_raw_buffer_load_b128(w4_rsrc(p.codes, row * (K / 2), rows * (K / 2)), cvo, kc * 64, 0);
-      w4_load_scales<S, SB, VEC>(w4_rsrc(p.scales, row * groups * SZ, rows * groups * SZ), svo, gi * SZ,
-                                 (int)groups - gi, q.scale[c]);
-      q.zero[c] = w4_load_zeros<S, VEC>(w4_rsrc(p.zeros, row * groups, p.zeros ? rows * groups : 0), zvo, gi);
-    }
-    ++v;
-    if (++kc == KC && SUM) {
-      kc = 0;
-      ++pair;
-      if (v < end) expert();
-    }
-  };
-  const float zero_base = p.zeros ? 0.f : 8.f;
-
-  auto use = [&](const Chunk& q) __attribute__((always_inline)) {
-    f32x4_t d[NB][CT], sx[NB];
-    const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      sx[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < CT; ++c) d[b][c] = sx[b];
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4_t w[CT];
-#pragma unroll
-      for (int c = 0; c < CT; ++c) w[c] = codes_to_bf16(q.codes[c][s]);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const u32x4_t x = x_order(q.x[b][s]);
-        sx[b] = w4_mfma(x, ones, sx[b]);
-#pragma unroll
-        for (int c = 0; c < CT; ++c) d[b][c] = w4_mfma(x, w[c], d[b][c]);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      float s[S], z[S];
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        s[i] = SB ? ((i & 1) ? bf16_hi(q.scale[c][i >> 1]) : bf16_lo(q.scale[c][i >> 1]))
-                  : __uint_as_float(q.scale[c][i]);
-        if (SUM) s[i] *= q.factor;
-        z[i] = zero_base + (float)((q.zero[c] >> (8 * i)) & 0xFFu);
-      }
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = fmaf(-z[i % S], sx[b][i], d[b][c][i]);
-          acc[b][c][i / S] = fmaf(s[i % S], f, acc[b][c][i / S]);
-        }
-    }
-  };
-
-  Chunk ring[D];
-#pragma unroll
-  for (int i = 0; i < D; ++i) {
-    load(ring[i]);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  for (int u = first; u < end; u += D) {
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      use(ring[i]);
-      load(ring[i]);
-    }
-  }
-
-  // the waves' shares, added in the waves' order
-  constexpr int V = NB * CT * R;
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int i = 0; i < R; ++i) s_part[(wave * V + (b * CT + c) * R + i) * 64 + lane] = acc[b][c][i];
-  __syncthreads();
-  auto total_of = [&](int v, int l) {
-    float f = s_part[v * 64 + l];
-    for (int w = 1; w < waves; ++w) f += s_part[(w * V + v) * 64 + l];
-    return f;
-  };
-  constexpr int OC = ACT ? CT / 2 : CT;
-  for (int o = threadIdx.x; o < NB * OC * R * 64; o += blockDim.x) {
-    const int l = o & 63, i = (o >> 6) % R, c = (o >> 6) / R % OC, b = (o >> 6) / R / OC;
-    const int t = b * (16 / S) + (l >> 4) * R + i;   // token of the workgroup's
-    const int64_t row = pairs ? rb : (int64_t)rb * TB + t;
-    const int col = cg * CW + c * 16 + (l & 15);
-    if (col >= cols || (pairs ? t != 0 : row >= p.T)) continue;
-    float f = total_of((b * CT + c) * R + i, l);
-    if (ACT) {
-      const float u = total_of((b * CT + c + OC) * R + i, l);
-      f = f / (1.0f + __expf(-f)) * u;
-    }
-    const int64_t at = row * cols + col;
-    if (p.y_bf16) reinterpret_cast<uint16_t*>(p.y)[at] = f32_to_bf16_rne(f);
-    else reinterpret_cast<float*>(p.y)[at] = f;
-  }
-}
-
-template <int S, int NB, int CT, bool ACT, bool SUM, bool SB, bool VEC, int D>
-static hipError_t launch_w4_t(W4Args a, int64_t row_blocks, hipStream_t stream) {
-  const int64_t cols = ACT ? a.N / 2 : a.N;
-  constexpr int CW = (ACT ? CT / 2 : CT) * 16;
-  a.col_groups = (int)((cols + CW - 1) / CW);
-  const int64_t groups = row_blocks * a.col_groups;
-  const int64_t chunks = (a.K + 127) / 128 * (SUM ? a.k : 1);
-  const int waves = groups * 4 < 2048 && chunks >= 8 ? 8 : 4;
-  const size_t lds = (size_t)waves * NB * CT * (4 / S) * 64 * 4;
-  hipLaunchKernelGGL((w4_gemv_kernel<S, NB, CT, ACT, SUM, SB, VEC, D>), dim3((unsigned)groups), dim3(waves * 64), lds,
-                     stream, a);
-  return hipGetLastError();
-}
-
 // ---------------------------------------------------------------------------
 // Few tokens: a lane's own 32 codes
 // ---------------------------------------------------------------------------
@@ -369,21 +152,21 @@ __device__ __forceinline__ float quad_xor(float v) {
 // and over the waves are joined in LDS, in order, while the next block's loads
 // are on their way.
 constexpr int W4_NT = 2;       // non-temporal: codes are read once
-constexpr int W4_LANE_TOKENS = 16;
 constexpr int W4_WAVES = 8;
 constexpr int W4_RING = 8;     // loads of 1 KiB in flight per wave, and row quads of a block
 
 struct W4LaneArgs {
   W4Args a;
   int blocks;                  // of a workgroup
+  int row_blocks;              // of the rows of x (w4_few_kernel)
 };
 
-template <int TT, bool ACT, bool SUM, bool SB, bool Z>
+template <bool ACT, bool SUM, bool SB, bool Z>
 __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
   const W4Args& p = la.a;
   constexpr int SZ = SB ? 2 : 4;
   constexpr int HALF = ACT ? W4_RING / 2 : W4_RING;   // quads of a block that are rows of y
-  __shared__ __attribute__((aligned(16))) float s_sum[2][W4_RING * TT][W4_WAVES][16];
+  __shared__ __attribute__((aligned(16))) float s_sum[2][W4_RING][W4_WAVES][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -395,7 +178,6 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
   const int cg = blockIdx.x % (uint32_t)p.col_groups;
   const int rb = blockIdx.x / (uint32_t)p.col_groups;
   const bool pairs = p.ids != nullptr;
-  const int tokens = pairs ? 1 : min(TT, p.T - rb * TT);
 
   const int row0 = cg * la.blocks * HALF * 4;
   const int rows = min(la.blocks * HALF * 4, cols - row0);
@@ -426,7 +208,7 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
   auto unit = [&](int u) __attribute__((always_inline)) {
     const int j = SUM ? u / per : 0;
     const int pair = SUM ? rb * p.k + j : rb;
-    Unit n = {0, pairs ? 0 : (int64_t)rb * TT, SUM ? u - j * per : u, u < total, 1.f};
+    Unit n = {0, 0, SUM ? u - j * per : u, u < total, 1.f};
     if (pairs) {
       const int id = u < total ? scalar_load(p.ids + pair) : -1;
       n.live = (uint32_t)id < (uint32_t)p.E;
@@ -480,28 +262,23 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
     }
   };
 
-  u32x4_t x[TT][4], xn[TT][4];
-  float sx[TT], factor = 1.f, nfactor = 1.f;
-  auto load_x = [&](const Unit& n, u32x4_t (&to)[TT][4], float& f) __attribute__((always_inline)) {
-    const __amdgpu_buffer_rsrc_t xr = w4_rsrc(p.x, n.xrow * K * 2, n.live ? (int64_t)tokens * K * 2 : 0);
+  u32x4_t x[4], xn[4];
+  float sx, factor = 1.f, nfactor = 1.f;
+  auto load_x = [&](const Unit& n, u32x4_t (&to)[4], float& f) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t xr = w4_rsrc(p.x, n.xrow * K * 2, n.live ? (int64_t)K * 2 : 0);
     const uint32_t xvo = n.c * 512 + block * 32 < K && diag ? (uint32_t)(n.c * 1024 + block * 64) : kLaneOob;
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) to[t][s] = __builtin_amdgcn_raw_buffer_load_b128(xr, xvo + s * 16, t * K * 2, 0);
+    for (int s = 0; s < 4; ++s) to[s] = __builtin_amdgcn_raw_buffer_load_b128(xr, xvo + s * 16, 0, 0);
     f = n.factor;
   };
   auto sum_x = [&]() __attribute__((always_inline)) {
+    f32x4_t d = zero4;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      f32x4_t d = zero4;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        x[t][s] = x_order(x[t][s]);
-        d = w4_mfma(x[t][s], ones, d);
-      }
-      sx[t] = own(d);
+    for (int s = 0; s < 4; ++s) {
+      x[s] = x_order(x[s]);
+      d = w4_mfma(x[s], ones, d);
     }
+    sx = own(d);
   };
 
   // x of the first unit, then the ring, in the order of use (a load waits for
@@ -519,11 +296,9 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
   for (int b = 0; b < blocks; ++b) {
     float (*sums)[W4_WAVES][16] = s_sum[b & 1];
     for (int u = wave; u < total; u += waves) {
-      // one token: the next unit's x (the last one's: the first of the next
-      // block) comes ahead of the loads that follow it
-      constexpr bool AHEAD = TT == 1;
-      auto next_x = [&]() __attribute__((always_inline)) { return unit(u + waves < total ? u + waves : wave); };
-      if (AHEAD && total > waves) load_x(next_x(), xn, nfactor);
+      // the next unit's x (the last one's: the first of the next block) comes
+      // ahead of the loads that follow it
+      if (total > waves) load_x(unit(u + waves < total ? u + waves : wave), xn, nfactor);
 #pragma unroll
       for (int i = 0; i < W4_RING; ++i) {
         const Row& q = ring[i];
@@ -536,43 +311,23 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
         __builtin_amdgcn_sched_barrier(0);
         load(i, ring[i]);
         __builtin_amdgcn_sched_barrier(0);
-        // sums of the row's 64 bytes, in all four of their lanes; lane q4 keeps
-        // those of token q4 of four.  (Tokens of a call that TT exceeds are
-        // zeros: a branch around them would keep the chains of matrix
-        // instructions from overlapping.)
+        f32x4_t d = zero4;
 #pragma unroll
-        for (int t0 = 0; t0 < TT; t0 += 4) {
-          constexpr int C = TT < 4 ? TT : 4;
-          f32x4_t d[C];
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int t = 0; t < C; ++t)
-              if (t0 + t < TT) d[t] = w4_mfma(x[t0 + t][s], w[s], s ? d[t] : zero4);
-          float keep = 0.f;
-#pragma unroll
-          for (int t = 0; t < C; ++t)
-            if (t0 + t < TT) {
-              float f = sc * fmaf(-z, sx[t0 + t], own(d[t]));
-              f += quad_xor<0xB1>(f);
-              f += quad_xor<0x4E>(f);
-              keep = t == 0 || q4 == t ? f : keep;
-            }
-          if (t0 + q4 < TT) {
-            float* to = &sums[i * TT + t0 + q4][wave][r * 4 + g];
-            *to = u == wave ? keep : *to + keep;
-          }
+        for (int s = 0; s < 4; ++s) d = w4_mfma(x[s], w[s], d);
+        // over the four lanes of the row's 64 bytes
+        float f = sc * fmaf(-z, sx, own(d));
+        f += quad_xor<0xB1>(f);
+        f += quad_xor<0x4E>(f);
+        if (q4 == 0) {
+          float* to = &sums[i][wave][r * 4 + g];
+          *to = u == wave ? f : *to + f;
         }
       }
       next_unit();
       if (total > waves) {
-        if (AHEAD) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) x[0][s] = xn[0][s];
-          factor = nfactor;
-        } else {
-          load_x(next_x(), x, factor);
-        }
+        for (int s = 0; s < 4; ++s) x[s] = xn[s];
+        factor = nfactor;
         sum_x();
       }
     }
@@ -581,67 +336,51 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
     // eight lanes add up a row, one a wave
     const int w = threadIdx.x & 7;
     const int live = min(rows - b * HALF * 4, HALF * 4);    // rows of y of the block
-    auto total_of = [&](int quad, int t, int row) __attribute__((always_inline)) {
+    auto total_of = [&](int quad, int row) __attribute__((always_inline)) {
       float f = 0.f;
       if (w < min(waves, total)) {
-        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&sums[quad * TT + t][w][row * 4]);
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&sums[quad][w][row * 4]);
         f = (v[0] + v[1]) + (v[2] + v[3]);
       }
       f += quad_xor<0xB1>(f);
       f += quad_xor<0x4E>(f);
       return f + quad_xor<0x141>(f);                        // the other quad of eight lanes
     };
-    for (int o = threadIdx.x >> 3; o < HALF * 4 * TT; o += blockDim.x >> 3) {
-      const int t = o % TT, row = o / TT;
-      float f = total_of(row >> 2, t, row & 3);
-      if (ACT) f = f / (1.0f + __expf(-f)) * total_of(HALF + (row >> 2), t, row & 3);
-      if (w != 0 || t >= tokens || row >= live) continue;
-      const int64_t at = ((pairs ? rb : (int64_t)rb * TT) + t) * cols + row0 + b * HALF * 4 + row;
+    for (int row = threadIdx.x >> 3; row < HALF * 4; row += blockDim.x >> 3) {
+      float f = total_of(row >> 2, row & 3);
+      if (ACT) f = f / (1.0f + __expf(-f)) * total_of(HALF + (row >> 2), row & 3);
+      if (w != 0 || row >= live) continue;
+      const int64_t at = (int64_t)rb * cols + row0 + b * HALF * 4 + row;
       if (p.y_bf16) reinterpret_cast<uint16_t*>(p.y)[at] = f32_to_bf16_rne(f);
       else reinterpret_cast<float*>(p.y)[at] = f;
     }
   }
 }
 
-template <int TT, bool ACT, bool SUM, bool SB, bool Z>
+template <bool ACT, bool SUM, bool SB, bool Z>
 static hipError_t launch_w4_lane_t(const W4Args& a, int64_t row_blocks, hipStream_t stream) {
-  W4LaneArgs la = {a, 0};
+  W4LaneArgs la = {a, 0, 1};
   const int64_t cols = ACT ? a.N / 2 : a.N;
   constexpr int ROWS = 4 * (ACT ? W4_RING / 2 : W4_RING);
   const int64_t blocks = (cols + ROWS - 1) / ROWS;
   const int64_t units = (a.K + 511) / 512 * (SUM ? a.k : 1);
   const int waves = units < W4_WAVES ? (int)units : W4_WAVES;
   // as many workgroups as the CUs hold at once, where there are as many blocks
-  const int64_t room = TT == 1 ? 512 : 256;
-  const int64_t per = (blocks * row_blocks + room - 1) / room;
+  constexpr int ROOM = 512;
+  const int64_t per = (blocks * row_blocks + ROOM - 1) / ROOM;
   la.blocks = (int)(per < blocks ? per : blocks);
   la.a.col_groups = (int)((blocks + la.blocks - 1) / la.blocks);
-  hipLaunchKernelGGL((w4_lane_kernel<TT, ACT, SUM, SB, Z>), dim3((unsigned)(row_blocks * la.a.col_groups)),
+  hipLaunchKernelGGL((w4_lane_kernel<ACT, SUM, SB, Z>), dim3((unsigned)(row_blocks * la.a.col_groups)),
                      dim3(waves * 64), 0, stream, la);
   return hipGetLastError();
 }
 
 template <bool SB, bool Z>
 static hipError_t launch_w4_lane(const W4Args& a, int act, hipStream_t stream) {
-  if (a.weights) return launch_w4_lane_t<1, false, true, SB, Z>(a, a.T, stream);
-  if (a.ids || a.T == 1) {
-    const int64_t rows = a.ids ? (int64_t)a.T * a.k : 1;
-    return act ? launch_w4_lane_t<1, true, false, SB, Z>(a, rows, stream)
-               : launch_w4_lane_t<1, false, false, SB, Z>(a, rows, stream);
-  }
-  const int64_t blocks = a.T <= 8 ? 1 : ((int64_t)a.T + 7) / 8;
-  switch (a.T <= 8 ? a.T : (int)((a.T + blocks - 1) / blocks)) {
-#define MOE_CASE(TT)                                                       \
-  return act ? launch_w4_lane_t<TT, true, false, SB, Z>(a, blocks, stream) \
-             : launch_w4_lane_t<TT, false, false, SB, Z>(a, blocks, stream)
-    case 2: MOE_CASE(2);
-    case 3: MOE_CASE(3);
-    case 4: MOE_CASE(4);
-    case 5: MOE_CASE(5);
-    case 6: MOE_CASE(6);
-    default: MOE_CASE(8);
-#undef MOE_CASE
-  }
+  if (a.weights) return launch_w4_lane_t<false, true, SB, Z>(a, a.T, stream);
+  const int64_t rows = a.ids ? (int64_t)a.T * a.k : 1;
+  return act ? launch_w4_lane_t<true, false, SB, Z>(a, rows, stream)
+             : launch_w4_lane_t<false, false, SB, Z>(a, rows, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -654,15 +393,13 @@ static hipError_t launch_w4_lane(const W4Args& a, int act, hipStream_t stream) {
 // and goes through 16-column tiles, two to a block (with ACT a gate and an up
 // tile).  A tile's scales and zero points are loaded by lane group g for chunk g
 // and handed to the lanes that need them through the LDS crossbar.
-constexpr int W4_TILES = 4;    // of 4 KiB in flight per wave, and of a block
-
-template <int S, bool ACT, bool SB, bool VEC, bool Z>
+template <int S, bool ACT, bool SB, bool VEC, bool Z, int BT>
 __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   const W4Args& p = la.a;
   constexpr int SZ = SB ? 2 : 4;
   constexpr int SW = SB ? (S + 1) / 2 : S;            // scale words of a chunk
   constexpr int R = 4 / S;                            // tokens a lane holds
-  constexpr int BT = W4_TILES, HALF = ACT ? BT / 2 : BT;   // tiles of a block; of y's columns
+  constexpr int HALF = ACT ? BT / 2 : BT;             // tiles of a block that are columns of y
   __shared__ float s_sum[2][BT * R][W4_WAVES][64];
   __shared__ __attribute__((aligned(256))) uint8_t s_codes[W4_WAVES][4096];
   const int lane = threadIdx.x & 63;
@@ -673,7 +410,13 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   const int64_t N = p.N;
   const int cols = (int)(ACT ? N / 2 : N);
 
-  const int row0 = blockIdx.x * la.blocks * HALF * 16;   // first column of y
+  // the row blocks of one column group follow one another on an XCD (workgroup
+  // ids go round them), so that its codes come from memory once
+  const int id = blockIdx.x >> 3;
+  const int cg = id / la.row_blocks * 8 + (blockIdx.x & 7), rb = id % la.row_blocks;
+  if (cg >= p.col_groups) return;
+  const int t0 = rb * (16 / S);                          // first token
+  const int row0 = cg * la.blocks * HALF * 16;           // first column of y
   const int rows = min(la.blocks * HALF * 16, cols - row0);
   const int blocks = (rows + HALF * 16 - 1) / (HALF * 16);
   const int total = (K + 511) >> 9;
@@ -684,7 +427,7 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   uint8_t* own = s_codes[wave];
   const uint32_t srow = (uint32_t)(n16 * groups);
   const bool mine = S == 1 || (S == 2 ? (g >> 1) == (n16 & 1) : g == (n16 & 3));
-  const uint32_t xrow = mine && n16 / S < p.T ? (uint32_t)(n16 / S * K * 2 + g * 64) : kLaneOob;
+  const uint32_t xrow = mine && t0 + n16 / S < p.T ? (uint32_t)(n16 / S * K * 2 + g * 64) : kLaneOob;
 
   const f32x4_t zero4 = {0.f, 0.f, 0.f, 0.f};
   const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
@@ -723,7 +466,7 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
 
   u32x4_t x[4][4];
   f32x4_t sx[4];
-  const __amdgpu_buffer_rsrc_t xr = w4_rsrc(p.x, 0, (int64_t)p.T * K * 2);
+  const __amdgpu_buffer_rsrc_t xr = w4_rsrc(p.x, (int64_t)t0 * K * 2, (int64_t)min(16 / S, p.T - t0) * K * 2);
   auto load_x = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -817,7 +560,7 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
     const int live = min(rows - b * HALF * 16, HALF * 16);
     for (int o = threadIdx.x; o < HALF * R * 64; o += blockDim.x) {
       const int l = o & 63, j = (o >> 6) % R, c = (o >> 6) / R;
-      const int t = (l >> 4) * R + j, col = c * 16 + (l & 15);
+      const int t = t0 + (l >> 4) * R + j, col = c * 16 + (l & 15);
       if (t >= p.T || col >= live) continue;
       float f = 0.f, h = 0.f;
       for (int w = 0; w < live_waves; ++w) {
@@ -832,60 +575,43 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   }
 }
 
-template <int S, bool ACT, bool SB, bool VEC, bool Z>
+template <int S, bool ACT, bool SB, bool VEC, bool Z, int BT>
 static hipError_t launch_w4_few_t(const W4Args& a, hipStream_t stream) {
-  W4LaneArgs la = {a, 0};
+  W4LaneArgs la = {a, 0, (a.T + 16 / S - 1) / (16 / S)};
   const int64_t cols = ACT ? a.N / 2 : a.N;
-  constexpr int COLS = 16 * (ACT ? W4_TILES / 2 : W4_TILES);
+  constexpr int COLS = 16 * (ACT ? BT / 2 : BT);
   const int64_t blocks = (cols + COLS - 1) / COLS;
   const int64_t units = (a.K + 511) / 512;
   const int waves = units < W4_WAVES ? (int)units : W4_WAVES;
-  const int64_t per = (blocks + 255) / 256;
-  la.blocks = (int)per;
-  hipLaunchKernelGGL((w4_few_kernel<S, ACT, SB, VEC, Z>), dim3((unsigned)((blocks + per - 1) / per)), dim3(waves * 64),
-                     0, stream, la);
+  // a workgroup per CU at a time, its column groups in eights
+  const int64_t room = la.row_blocks > 32 ? 8 : 32 / la.row_blocks * 8;
+  la.blocks = (int)((blocks + room - 1) / room);
+  la.a.col_groups = (int)((blocks + la.blocks - 1) / la.blocks);
+  const int64_t groups = ((int64_t)la.a.col_groups + 7) / 8 * 8 * la.row_blocks;
+  hipLaunchKernelGGL((w4_few_kernel<S, ACT, SB, VEC, Z, BT>), dim3((unsigned)groups), dim3(waves * 64), 0, stream, la);
   return hipGetLastError();
+}
+
+template <int S, bool SB, bool VEC, bool Z>
+static hipError_t launch_w4_few_z(const W4Args& a, int act, hipStream_t stream) {
+  // four tiles a block where that still leaves a block per CU
+  const int64_t rows = (a.T + 16 / S - 1) / (16 / S), wide = a.N / 64 * rows;
+  if (wide >= 256)
+    return act ? launch_w4_few_t<S, true, SB, VEC, Z, 4>(a, stream) : launch_w4_few_t<S, false, SB, VEC, Z, 4>(a, stream);
+  return act ? launch_w4_few_t<S, true, SB, VEC, Z, 2>(a, stream) : launch_w4_few_t<S, false, SB, VEC, Z, 2>(a, stream);
 }
 
 template <int S, bool SB, bool VEC>
 static hipError_t launch_w4_few(const W4Args& a, int act, hipStream_t stream) {
-  if (a.zeros) return act ? launch_w4_few_t<S, true, SB, VEC, true>(a, stream) : launch_w4_few_t<S, false, SB, VEC, true>(a, stream);
-  return act ? launch_w4_few_t<S, true, SB, VEC, false>(a, stream) : launch_w4_few_t<S, false, SB, VEC, false>(a, stream);
-}
-
-// Tokens of a workgroup for T rows of a dense product.
-static int w4_blocks(int64_t rows, int S) {
-  const int64_t need = (rows * S + 15) / 16;
-  return need <= 1 ? 1 : need <= 2 ? 2 : 4;
+  return a.zeros ? launch_w4_few_z<S, SB, VEC, true>(a, act, stream) : launch_w4_few_z<S, SB, VEC, false>(a, act, stream);
 }
 
 static int w4_groups_per_chunk(int32_t G) { return G >= 128 ? 1 : 128 / G; }
 
 int64_t w4_workgroups(int32_t N, int32_t G, int32_t T, int32_t k, int pairs, int sum, int act) {
-  const int S = w4_groups_per_chunk(G);
-  const int nb = pairs ? 1 : w4_blocks(T, S);
-  const int64_t rows = pairs ? (sum ? T : (int64_t)T * k) : ((int64_t)T + 16 / S * nb - 1) / (16 / S * nb);
-  return rows * (((act ? N / 2 : N) + 15) / 16);
-}
-
-template <int S, bool SB, bool VEC>
-static hipError_t launch_w4_s(const W4Args& a, int act, hipStream_t stream) {
-  if (a.ids) {
-    if (a.weights) return launch_w4_t<S, 1, 2, false, true, SB, VEC, 3>(a, a.T, stream);
-    const int64_t rows = (int64_t)a.T * a.k;
-    return act ? launch_w4_t<S, 1, 2, true, false, SB, VEC, 3>(a, rows, stream)
-               : launch_w4_t<S, 1, 2, false, false, SB, VEC, 3>(a, rows, stream);
-  }
-  const int nb = w4_blocks(a.T, S);
-  const int64_t blocks = ((int64_t)a.T + 16 / S * nb - 1) / (16 / S * nb);
-  if (nb == 1)
-    return act ? launch_w4_t<S, 1, 2, true, false, SB, VEC, 3>(a, blocks, stream)
-               : launch_w4_t<S, 1, 2, false, false, SB, VEC, 3>(a, blocks, stream);
-  if (nb == 2)
-    return act ? launch_w4_t<S, 2, 2, true, false, SB, VEC, 2>(a, blocks, stream)
-               : launch_w4_t<S, 2, 2, false, false, SB, VEC, 2>(a, blocks, stream);
-  return act ? launch_w4_t<S, 4, 2, true, false, SB, VEC, 1>(a, blocks, stream)
-             : launch_w4_t<S, 4, 2, false, false, SB, VEC, 1>(a, blocks, stream);
+  const int per = 16 / w4_groups_per_chunk(G);
+  const int64_t rows = pairs ? (sum ? T : (int64_t)T * k) : ((int64_t)T + per - 1) / per;
+  return rows * (((int64_t)(act ? N / 2 : N) + 15) / 16 + 8);
 }
 
 hipError_t launch_w4_gemv(const uint8_t* codes, const void* scales, int scale_bf16, const uint8_t* zeros, int32_t G,
@@ -911,23 +637,19 @@ hipError_t launch_w4_gemv(const uint8_t* codes, const void* scales, int scale_bf
   a.scale_bf16 = scale_bf16;
   a.y_bf16 = y_bf16;
   a.col_groups = 0;
-  const int S = w4_groups_per_chunk(G);
-  const uintptr_t run = S * (scale_bf16 ? 2 : 4);
-  const bool vec = a.groups % S == 0 && ((uintptr_t)scales & (run - 1)) == 0 && ((uintptr_t)zeros & (S - 1)) == 0;
-  if (!ids && T > 1 && T <= 16 / S) {
-#define MOE_W4(SV, VECV) \
-  (scale_bf16 ? launch_w4_few<SV, true, VECV>(a, act, stream) : launch_w4_few<SV, false, VECV>(a, act, stream))
-    if (S == 4) return vec ? MOE_W4(4, true) : MOE_W4(4, false);
-    if (S == 2) return vec ? MOE_W4(2, true) : MOE_W4(2, false);
-    return MOE_W4(1, true);
-#undef MOE_W4
-  }
-  if (ids || T <= W4_LANE_TOKENS) {
+  // One row: a lane's own codes, the fewest instructions and cache accesses a
+  // code (131,072 x 4,096, groups of 128: 46 us, 52 with two rows of the other).
+  // More: 16 columns at a time (4,096 x 4,096, 4 rows, groups of 32: 6.1 us; the
+  // lane kernel with four rows in registers took 7.6, with eight 11.6).
+  if (ids || T == 1) {
     if (scale_bf16) return zeros ? launch_w4_lane<true, true>(a, act, stream) : launch_w4_lane<true, false>(a, act, stream);
     return zeros ? launch_w4_lane<false, true>(a, act, stream) : launch_w4_lane<false, false>(a, act, stream);
   }
+  const int S = w4_groups_per_chunk(G);
+  const uintptr_t run = S * (scale_bf16 ? 2 : 4);
+  const bool vec = a.groups % S == 0 && ((uintptr_t)scales & (run - 1)) == 0 && ((uintptr_t)zeros & (S - 1)) == 0;
 #define MOE_W4(SV, VECV) \
-  (scale_bf16 ? launch_w4_s<SV, true, VECV>(a, act, stream) : launch_w4_s<SV, false, VECV>(a, act, stream))
+  (scale_bf16 ? launch_w4_few<SV, true, VECV>(a, act, stream) : launch_w4_few<SV, false, VECV>(a, act, stream))
   if (S == 4) return vec ? MOE_W4(4, true) : MOE_W4(4, false);
   if (S == 2) return vec ? MOE_W4(2, true) : MOE_W4(2, false);
   return MOE_W4(1, true);
