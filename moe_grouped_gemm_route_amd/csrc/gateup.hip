@@ -518,17 +518,16 @@ struct StreamArgs {
 // 8 KiB, loaded by one wave in runs of 512 bytes and turned into the matrix
 // unit's order through LDS of the wave's own (the operand's lanes lie across the
 // rows, 16 bytes each: loaded that way, every lane is a cache access of its own,
-// and the L1 takes one a cycle).  A workgroup's waves share K, in units of 256;
-// blocks of 8 columns of h follow one another.  NB blocks of 16 rows of x, which
-// come along with the tiles; two tiles in flight per wave, or one where 32 rows
-// of x fill the registers.
+// and the L1 takes one a cycle).  The 16 rows of x come along with the tiles in
+// the same way.  A workgroup's waves share K, in units of 256; blocks of 8
+// columns of h follow one another; two tiles in flight per wave.
 constexpr int GS_WAVES = 8;
+constexpr int GS_ROWS = 16;
 
-template <int NB>
 __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) {
   constexpr int D = 2;
-  __shared__ __attribute__((aligned(512))) uint8_t s_tile[GS_WAVES][8192];
-  __shared__ float s_part[2][GS_WAVES][NB * 4][64];
+  __shared__ __attribute__((aligned(512))) uint8_t s_tile[GS_WAVES][2][8192];
+  __shared__ float s_part[2][GS_WAVES][4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -542,15 +541,12 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
   // load i of a tile: rows 2 i and 2 i + 1, a half of the wave each; segment c of
   // row r at place c ^ r of its 32
   const int half = lane >> 5, seg = lane & 31;
-  const uint32_t wvo = (uint32_t)half * (uint32_t)(K * 2) + seg * 16;
-  uint8_t* tile = s_tile[wave];
-  uint32_t xvo[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) xvo[b] = b * 16 + n16 < p.M ? (uint32_t)((b * 16 + n16) * K * 2 + g * 16) : kLaneOob;
+  const uint32_t rvo = (uint32_t)half * (uint32_t)(K * 2) + seg * 16;
+  uint8_t* tile = s_tile[wave][0];
   const __amdgpu_buffer_rsrc_t xr = gu_rsrc(p.x, (int64_t)p.M * K * 2);
 
   struct Slot {
-    u32x4_t w[8], x[NB][8];
+    u32x4_t w[8], x[8];
   };
   Slot ring[D];
   int lu = wave, lb = 0;                                    // unit and block of the next load
@@ -559,17 +555,12 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
     const uint16_t* base = p.w + (int64_t)(j0 + lb * 8) * K;
     const uint32_t bytes = (uint32_t)max(0, min(left, 8)) * (uint32_t)(K * 2);
     const __amdgpu_buffer_rsrc_t gr = gu_rsrc(base, bytes), ur = gu_rsrc(base + (int64_t)p.F * K, bytes);
-    const uint32_t wo = lu * 256 + seg * 8 < K ? wvo : kLaneOob;
+    const uint32_t vo = lu * 256 + seg * 8 < K ? rvo : kLaneOob;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      q.w[i] = __builtin_amdgcn_raw_buffer_load_b128(i < 4 ? gr : ur, wo, (i & 3) * K * 4 + lu * 512, GS_NT);
+      q.w[i] = __builtin_amdgcn_raw_buffer_load_b128(i < 4 ? gr : ur, vo, (i & 3) * K * 4 + lu * 512, GS_NT);
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const uint32_t xo = lu * 256 + s * 32 + g * 8 < K ? xvo[b] : kLaneOob;
-        q.x[b][s] = __builtin_amdgcn_raw_buffer_load_b128(xr, xo, lu * 512 + s * 64, 0);
-      }
+    for (int i = 0; i < 8; ++i) q.x[i] = __builtin_amdgcn_raw_buffer_load_b128(xr, vo, i * K * 4 + lu * 512, 0);
     lu += waves;
     if (lu >= total) {
       lu = wave;
@@ -582,27 +573,20 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  f32x4_t acc[NB];
-  auto clear = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int b = 0; b < NB; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  };
-  clear();
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   auto join = [&](int blk) __attribute__((always_inline)) {
-    float (*part)[NB * 4][64] = s_part[blk & 1];
+    float (*part)[4][64] = s_part[blk & 1];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[wave][b * 4 + i][lane] = acc[b][i];
-    clear();
+    for (int i = 0; i < 4; ++i) part[wave][i][lane] = acc[i];
+    acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
     lds_barrier();
     const int live = min(cols - blk * 8, 8);
     // eight lanes to a column's row: one a wave
-    for (int o = threadIdx.x >> 3; o < NB * 128; o += blockDim.x >> 3) {
+    for (int o = threadIdx.x >> 3; o < GS_ROWS * 8; o += blockDim.x >> 3) {
       const int w = threadIdx.x & 7, c = o & 7, row = o >> 3;
       float gt = 0.f, ut = 0.f;
       if (w < min(waves, total)) {
-        const float* from = &part[w][(row >> 4) * 4 + (row & 3)][((row >> 2) & 3) * 16 + c];
+        const float* from = &part[w][row & 3][(row >> 2) * 16 + c];
         gt = from[0];
         ut = from[8];
       }
@@ -643,15 +627,15 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const int row = 2 * c + half;
-        *reinterpret_cast<u32x4_t*>(tile + row * 512 + ((seg ^ row) << 4)) = q.w[c];
+        const int row = 2 * c + half, place = row * 512 + ((seg ^ row) << 4);
+        *reinterpret_cast<u32x4_t*>(tile + place) = q.w[c];
+        *reinterpret_cast<u32x4_t*>(tile + 8192 + place) = q.x[c];
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(tile + n16 * 512 + (((s * 4 + g) ^ n16) << 4));
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[b] = gu_mfma(q.x[b][s], w, acc[b]);
+        const uint8_t* from = tile + n16 * 512 + (((s * 4 + g) ^ n16) << 4);
+        acc = gu_mfma(*reinterpret_cast<const u32x4_t*>(from + 8192), *reinterpret_cast<const u32x4_t*>(from), acc);
       }
       __builtin_amdgcn_sched_barrier(0);
       load(q);
@@ -776,7 +760,7 @@ int64_t gate_up_workgroups(int32_t M, int32_t N, int32_t K) {
 //   dw13 of 2,832 x 2,560 over 1,237 rows: 256 x 128 28.5, 256 x 256 39.7
 struct TileConfig {
   int bm, bn, kg, fit;    // rows, columns (gate and up: of w13), groups, workgroups that run at once
-  float stage;
+  float stage, alone;     // a stage with `fit` workgroups, and with one per CU at most
 };
 
 struct TilePlan {
@@ -794,7 +778,8 @@ static TilePlan tile_plan(const TileConfig (&configs)[COUNT], int gate, int64_t 
     const int64_t stages = ceil_div(ceil_div(R, GU_BK), t.kg);
     for (int splits = 1; splits <= most_splits && splits <= stages; splits *= 2) {
       if (splits > 1 && tiles * splits > 2 * t.fit) break;
-      float us = (float)ceil_div(tiles * splits, t.fit) * (3.f + (float)(ceil_div(stages, splits) * t.kg) * t.stage);
+      const float stage = tiles * splits <= GU_CUS ? t.alone : t.stage;
+      float us = (float)ceil_div(tiles * splits, t.fit) * (3.f + (float)(ceil_div(stages, splits) * t.kg) * stage);
       if (splits > 1) us += 4.f + (float)splits * (float)I * (float)J * (8.f / 4.5e6f);
       if (least == 0.f || us < least) {
         least = us;
@@ -805,13 +790,17 @@ static TilePlan tile_plan(const TileConfig (&configs)[COUNT], int gate, int64_t 
   return best;
 }
 
-static const TileConfig kForward[] = {{256, 256, 1, 256, 1.65f}, {128, 256, 1, 256, 1.f}, {128, 128, 2, 256, .6f},
-                                      {64, 64, 4, 256, .3f}, {32, 64, 4, 256, .25f}};
-static const TileConfig kDx[] = {{256, 256, 1, 256, 1.7f}, {128, 256, 1, 256, .97f}, {128, 128, 2, 256, .6f},
-                                 {64, 128, 1, 768, .7f}};
-static const TileConfig kDx3[] = {{128, 256, 1, 256, 2.2f}, {64, 256, 1, 256, 1.25f}, {64, 128, 1, 512, 1.3f}};
-static const TileConfig kDw[] = {{256, 256, 1, 256, 1.7f}, {256, 128, 1, 256, 1.02f}, {128, 128, 2, 256, .6f}};
-static const TileConfig kDw3[] = {{128, 256, 1, 256, 2.3f}};
+static const TileConfig kForward[] = {{256, 256, 1, 256, 1.7f, 1.7f}, {128, 256, 1, 256, .94f, .94f},
+                                      {128, 128, 2, 256, .55f, .55f}, {64, 64, 4, 256, .23f, .23f},
+                                      {32, 64, 4, 256, .17f, .17f}};
+static const TileConfig kDx[] = {{256, 256, 1, 256, 1.65f, 1.65f}, {128, 256, 1, 256, .95f, .95f},
+                                 {128, 128, 2, 256, .58f, .58f}, {64, 128, 1, 768, .7f, .7f},
+                                 {64, 128, 2, 256, .4f, .4f}};
+static const TileConfig kDx3[] = {{128, 256, 1, 256, 2.1f, 2.1f}, {64, 256, 1, 256, 1.25f, 1.4f},
+                                  {64, 128, 1, 512, 1.3f, 1.05f}};
+static const TileConfig kDw[] = {{256, 256, 1, 256, 1.7f, 1.7f}, {256, 128, 1, 256, 1.f, 1.f},
+                                 {128, 128, 2, 256, .58f, .58f}};
+static const TileConfig kDw3[] = {{128, 256, 1, 256, 2.2f, 2.2f}};
 constexpr int GU_SPLITS = 16;
 
 static hipError_t launch_forward(int config, const TileArgs& a, hipStream_t s) {
@@ -819,8 +808,8 @@ static hipError_t launch_forward(int config, const TileArgs& a, hipStream_t s) {
     case 0: return launch_tiles<false, false, 2, 4, 8, 4, 1, 1, true, false, 2>(a, s);
     case 1: return launch_tiles<false, false, 2, 4, 4, 4, 1, 1, true, false, 2>(a, s);
     case 2: return launch_tiles<false, false, 2, 2, 4, 4, 2, 1, true, false, 2>(a, s);
-    case 3: return launch_tiles<false, false, 4, 1, 1, 4, 4, 1, true, false, 4>(a, s);
-    default: return launch_tiles<false, false, 2, 1, 1, 4, 4, 1, true, false, 2>(a, s);
+    case 3: return launch_tiles<false, false, 4, 1, 1, 4, 4, 1, true, true, 4>(a, s);
+    default: return launch_tiles<false, false, 2, 1, 1, 4, 4, 1, true, true, 2>(a, s);
   }
 }
 
@@ -829,7 +818,8 @@ static hipError_t launch_dx(int parts, int config, const TileArgs& a, hipStream_
     case 0: return launch_tiles<false, true, 2, 4, 8, 4, 1, 1, false, false, 2>(a, s);
     case 1: return launch_tiles<false, true, 2, 4, 4, 4, 1, 1, false, false, 2>(a, s);
     case 2: return launch_tiles<false, true, 2, 2, 4, 4, 2, 1, false, false, 2>(a, s);
-    default: return launch_tiles<false, true, 2, 2, 2, 4, 1, 1, false, false, 3>(a, s);
+    case 3: return launch_tiles<false, true, 2, 2, 2, 4, 1, 1, false, false, 3>(a, s);
+    default: return launch_tiles<false, true, 2, 2, 2, 4, 2, 1, false, true, 2>(a, s);
   }
   switch (config) {
     case 0: return launch_tiles<false, true, 2, 4, 4, 4, 1, 3, false, false, 2>(a, s);
@@ -850,13 +840,11 @@ static hipError_t launch_dw(int parts, int config, const TileArgs& a, hipStream_
 hipError_t launch_gate_up(const uint16_t* x, const uint16_t* w, int32_t M, int32_t N, int32_t K, void* h, int h_bf16,
                           void* pre, int pre_bf16, hipStream_t stream) {
   const int F = N / 2;
-  if (M <= 32) {
+  if (M <= GS_ROWS) {
     const int all = (F + 7) / 8, per = (all + GU_CUS - 1) / GU_CUS;
     StreamArgs a = {x, w, K, M, F, per, h, h_bf16, pre, pre_bf16};
     const int units = (K + 255) / 256, waves = units < GS_WAVES ? units : GS_WAVES;
-    const dim3 grid((all + per - 1) / per), block(waves * 64);
-    if (M <= 16) hipLaunchKernelGGL(gu_stream_kernel<1>, grid, block, 0, stream, a);
-    else hipLaunchKernelGGL(gu_stream_kernel<2>, grid, block, 0, stream, a);
+    hipLaunchKernelGGL(gu_stream_kernel, dim3((all + per - 1) / per), dim3(waves * 64), 0, stream, a);
     return hipGetLastError();
   }
   TileArgs a = {};
