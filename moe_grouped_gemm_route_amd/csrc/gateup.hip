@@ -582,7 +582,7 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
     lds_barrier();
     const int live = min(cols - blk * 8, 8);
     // eight lanes to a column's row: one a wave
-    for (int o = threadIdx.x >> 3; o < GS_ROWS * 8; o += blockDim.x >> 3) {
+    for (int o = threadIdx.x >> 3; o < p.M * 8; o += blockDim.x >> 3) {
       const int w = threadIdx.x & 7, c = o & 7, row = o >> 3;
       float gt = 0.f, ut = 0.f;
       if (w < min(waves, total)) {
@@ -593,7 +593,7 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
       gt += dpp_add<0xB1>(gt), ut += dpp_add<0xB1>(ut);
       gt += dpp_add<0x4E>(gt), ut += dpp_add<0x4E>(ut);
       gt += dpp_add<0x141>(gt), ut += dpp_add<0x141>(ut);
-      if (w != 0 || row >= p.M || c >= live) continue;
+      if (w != 0 || c >= live) continue;
       const float h = gu_silu(gt) * ut;
       const int col = j0 + blk * 8 + c;
       const int64_t at = (int64_t)row * p.F + col;
@@ -623,6 +623,7 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
   while (blk < blocks) {
 #pragma unroll
     for (int i = 0; i < D; ++i) {
+      if (i > 0 && blk >= blocks) break;
       Slot& q = ring[i];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
@@ -642,8 +643,7 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
       __builtin_amdgcn_sched_barrier(0);
       if (++u == per) {
         u = 0;
-        if (blk < blocks) join(blk);
-        ++blk;
+        join(blk++);
       }
     }
   }
