@@ -357,6 +357,13 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
   }
 }
 
+// Blocks of `rows` columns of a workgroup, at most as many as keep its codes
+// within 2^30 bytes, which its loads address with 32-bit offsets.
+static int64_t w4_hold(int64_t blocks, int rows, int64_t K) {
+  const int64_t most = (int64_t(1) << 30) / (K / 2) / rows;   // K <= 2^23: 4 at least
+  return blocks < most ? blocks : most;
+}
+
 template <bool ACT, bool SUM, bool SB, bool Z>
 static hipError_t launch_w4_lane_t(const W4Args& a, int64_t row_blocks, hipStream_t stream) {
   W4LaneArgs la = {a, 0, 1};
@@ -368,7 +375,7 @@ static hipError_t launch_w4_lane_t(const W4Args& a, int64_t row_blocks, hipStrea
   // as many workgroups as the CUs hold at once, where there are as many blocks
   constexpr int ROOM = 512;
   const int64_t per = (blocks * row_blocks + ROOM - 1) / ROOM;
-  la.blocks = (int)(per < blocks ? per : blocks);
+  la.blocks = (int)w4_hold(per < blocks ? per : blocks, ROWS, a.K);
   la.a.col_groups = (int)((blocks + la.blocks - 1) / la.blocks);
   hipLaunchKernelGGL((w4_lane_kernel<ACT, SUM, SB, Z>), dim3((unsigned)(row_blocks * la.a.col_groups)),
                      dim3(waves * 64), 0, stream, la);
@@ -585,7 +592,7 @@ static hipError_t launch_w4_few_t(const W4Args& a, hipStream_t stream) {
   const int waves = units < W4_WAVES ? (int)units : W4_WAVES;
   // a workgroup per CU at a time, its column groups in eights
   const int64_t room = la.row_blocks > 32 ? 8 : 32 / la.row_blocks * 8;
-  la.blocks = (int)((blocks + room - 1) / room);
+  la.blocks = (int)w4_hold((blocks + room - 1) / room, COLS, a.K);
   la.a.col_groups = (int)((blocks + la.blocks - 1) / la.blocks);
   const int64_t groups = ((int64_t)la.a.col_groups + 7) / 8 * 8 * la.row_blocks;
   hipLaunchKernelGGL((w4_few_kernel<S, ACT, SB, VEC, Z, BT>), dim3((unsigned)groups), dim3(waves * 64), 0, stream, la);

@@ -170,3 +170,39 @@ def test_refusals():
         with pytest.raises(moe.MoeGmmError):
             f()
             pytest.fail("call %d was taken" % i)
+
+
+def ones_but(N, K, lead=()):
+    """Codes whose weights are 1 (c - 8), the last k of column N - 2 counting
+    twice, and scales of 1, of 2 in the last column."""
+    codes = torch.empty(lead + (N, K // 2), dtype=torch.uint8, device=DEV).fill_(0x99)
+    codes[..., N - 2, K // 2 - 1] = 0xA9
+    scales = torch.ones(lead + (N, K // 256), dtype=torch.bfloat16, device=DEV)
+    scales[..., N - 1, :] = 2.0
+    return codes, scales
+
+
+def edges(T, K):
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device=DEV)
+    t = torch.arange(T, device=DEV) % 5 + 1
+    x[:, 0], x[:, K - 1] = 1.0, t.bfloat16()
+    return x, t.float()
+
+
+def test_many_pairs_of_a_matrix_past_32_bit_offsets():
+    """So many rows that a workgroup would take 4 GiB of codes."""
+    N, K, T = 131072, 65536, 600
+    codes, scales = ones_but(N, K, (1,))
+    x, t = edges(T, K)
+    y = moe.w4_gemv(codes, scales, x, topk_ids=torch.zeros((T, 1), dtype=torch.int32, device=DEV))
+    assert bool((y[:, : N - 2] == (1 + t)[:, None]).all())
+    assert torch.equal(y[:, N - 2], 1 + 2 * t) and torch.equal(y[:, N - 1], 2 + 2 * t)
+
+
+def test_many_rows_of_a_matrix_past_32_bit_offsets():
+    N, K, T = 1 << 20, 32768, 520
+    codes, scales = ones_but(N, K)
+    x, t = edges(T, K)
+    y = moe.w4_gemv(codes, scales, x, out_dtype=moe.BF16).float()
+    assert bool((y[:, : N - 2] == (1 + t)[:, None]).all())
+    assert torch.equal(y[:, N - 2], 1 + 2 * t) and torch.equal(y[:, N - 1], 2 + 2 * t)
