@@ -162,9 +162,22 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 //
 // REGS: the loads go through registers instead, two stages ahead.  The wait for
 // a register is counted by the compiler, so a stage has two stages' time to
-// land; tiles whose stages are short need that (a stage of 128 x 128 x 128 takes
-// 0.5 us of matrix instructions, a load 0.9).  Where the sums fill the registers
-// (256 x 256) the loads go to LDS.
+// land, which short stages need (K 4,096, 2,048 columns of h, us through LDS and
+// through registers: 64 rows in 32 x 64 tiles 18.9, 16.0; 256 rows in 64 x 64
+// 24.2, 21.8; 512 rows in 64 x 128 33.5, 30.0; dx of 64 rows in 64 x 128 14.4,
+// 12.8).  Larger tiles load to LDS: their stages hide the loads (128 x 256 65.9,
+// 69.2), and with the sums their registers spill (128 x 128 in two groups 40.7,
+// 86.2).
+//
+// What bounds it.  256 x 256 tiles: the matrix pipes, 1.34 PFLOP/s forward and
+// 1.18 to 1.26 backward at 4,096 rows, where a library product reaches 1.22 to
+// 1.26; 53 % of the pipes' cycles at the clock that the chip holds.  Of 116 us of
+// such a product 88 are left without the loads, 91 without the LDS reads and 71
+// without the matrix instructions.  Smaller tiles: the loads on their way from
+// L2 (about 15 TB/s over the chip; 340 to 470 cycles each), since with fewer rows
+// each weight meets less work.  Tried and not faster: 4 waves of 128 x 128
+// (116 to 124 for 110), half or three eighths of the groups behind the barrier,
+// loads between single matrix instructions.
 template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, bool REGS, int OCC>
 __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArgs p) {
   constexpr int NW = WI * WJ;
@@ -521,6 +534,11 @@ struct StreamArgs {
 // and the L1 takes one a cycle).  The 16 rows of x come along with the tiles in
 // the same way.  A workgroup's waves share K, in units of 256; blocks of 8
 // columns of h follow one another; two tiles in flight per wave.
+//
+// Bound by memory where the weights come from there, and by the start of the
+// stream where they do not (33.6 MB of w13, one row: 10.7 us a call, 8.0 at best,
+// for 6.6 at a copy's rate).  Tiles with 17 rows and more: at 16 rows the stream
+// takes 11.6 us, the smallest tiles 14.9; a row more would take a second x.
 constexpr int GS_WAVES = 8;
 constexpr int GS_ROWS = 16;
 
@@ -750,14 +768,19 @@ int64_t gate_up_workgroups(int32_t M, int32_t N, int32_t K) {
 // workgroups that fit the CUs run (us, from 4,096 x 4,096 products; a stage of KG
 // groups counts KG).  A product takes the instance, and the shares of its sum,
 // of the least estimate: whole rounds of workgroups, and for shares the sums
-// written, read and added at 4.5 TB/s in one more launch.  The sides measured, us:
-//   gate/up, K 4,096, 2,048 columns of h: 64 rows 32 x 64 tiles 19.8, 64 x 64 22.7,
-//     128 x 128 38.5; 256 rows 64 x 64 23.7, 128 x 128 39.7; 1,024 rows 128 x 128
-//     43.8, 128 x 256 64, 64 x 64 over 64; 2,048 rows 128 x 256 67.8, 256 x 256
-//     89.9; 4,096 rows 256 x 256 109.8, 128 x 256 131.2
-//   dx of 1,237 rows (2,560 columns, sum over 2,832): 128 x 128 36.8, 256 x 256
-//     in four shares 37.5 and their sum
-//   dw13 of 2,832 x 2,560 over 1,237 rows: 256 x 128 28.5, 256 x 256 39.7
+// written, read and added at 4.5 TB/s in one more launch.  The sides measured, us
+// (the instance taken first; sN: in N shares, without the launch that adds them):
+//   gate/up, K 4,096, 2,048 columns of h: 64 rows 32 x 64 tiles 16.0, 64 x 64
+//     19.4, 64 x 128 27; 256 rows 64 x 64 21.8, 64 x 128 28.5, 32 x 64 28.7; 512
+//     rows 64 x 128 30.0, 64 x 64 37.9, 128 x 128 38.2; 1,024 rows 128 x 128
+//     40.7, 64 x 128 53.2, 128 x 256 58; 2,048 rows 128 x 256 65.9, 128 x 128
+//     75.9, 256 x 256 88.6; 4,096 rows 256 x 256 102.7, 128 x 256 124.5
+//   dx of 1,237 rows (2,560 columns, sum over 2,832): 128 x 128 36.2, 128 x 256
+//     in s2 33.2, 256 x 256 in s4 36.8, 64 x 128 40.5
+//   dx of 64 rows (4,096 columns and sums): 64 x 128 in s8 12.8, s4 14.1, 128 x
+//     128 in s8 15.5
+//   dw13 of 2,832 x 2,560 over 1,237 rows: 256 x 128 30.3, 128 x 256 31.9, 256 x
+//     256 in s2 33.4, alone 44.7; 128 x 128 37.5
 struct TileConfig {
   int bm, bn, kg, fit;    // rows, columns (gate and up: of w13), groups, workgroups that run at once
   float stage, alone;     // a stage with `fit` workgroups, and with one per CU at most
@@ -790,9 +813,9 @@ static TilePlan tile_plan(const TileConfig (&configs)[COUNT], int gate, int64_t 
   return best;
 }
 
-static const TileConfig kForward[] = {{256, 256, 1, 256, 1.7f, 1.7f}, {128, 256, 1, 256, .94f, .94f},
-                                      {128, 128, 2, 256, .55f, .55f}, {64, 64, 4, 256, .23f, .23f},
-                                      {32, 64, 4, 256, .17f, .17f}};
+static const TileConfig kForward[] = {{256, 256, 1, 256, 1.57f, 1.57f}, {128, 256, 1, 256, .98f, .98f},
+                                      {128, 128, 2, 256, .58f, .58f},   {64, 128, 2, 256, .42f, .42f},
+                                      {64, 64, 4, 256, .29f, .29f},     {32, 64, 4, 256, .2f, .2f}};
 static const TileConfig kDx[] = {{256, 256, 1, 256, 1.65f, 1.65f}, {128, 256, 1, 256, .95f, .95f},
                                  {128, 128, 2, 256, .58f, .58f}, {64, 128, 1, 768, .7f, .7f},
                                  {64, 128, 2, 256, .4f, .4f}};
@@ -808,7 +831,8 @@ static hipError_t launch_forward(int config, const TileArgs& a, hipStream_t s) {
     case 0: return launch_tiles<false, false, 2, 4, 8, 4, 1, 1, true, false, 2>(a, s);
     case 1: return launch_tiles<false, false, 2, 4, 4, 4, 1, 1, true, false, 2>(a, s);
     case 2: return launch_tiles<false, false, 2, 2, 4, 4, 2, 1, true, false, 2>(a, s);
-    case 3: return launch_tiles<false, false, 4, 1, 1, 4, 4, 1, true, true, 4>(a, s);
+    case 3: return launch_tiles<false, false, 2, 2, 2, 4, 2, 1, true, true, 2>(a, s);
+    case 4: return launch_tiles<false, false, 4, 1, 1, 4, 4, 1, true, true, 4>(a, s);
     default: return launch_tiles<false, false, 2, 1, 1, 4, 4, 1, true, true, 2>(a, s);
   }
 }

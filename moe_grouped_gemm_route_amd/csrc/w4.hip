@@ -14,14 +14,16 @@
 // the matrix unit (the second against a constant operand of ones).  A group's
 // sums are then multiplied by its scale and added in f32: no weight is rounded.
 //
-// MFMA mapping (v_mfma_f32_16x16x32_bf16).  A wave takes chunks of 128 k of
-// 16 columns: lane l loads the 16 bytes of column n = l & 15 and 32-block
-// g = l >> 4, and one of four steps multiplies 8 k of all four blocks.  Summing
-// over the lane groups would mix scales, so x is laid out block-diagonally:
-// row r of the first operand is token r / S with the lanes of group r % S alone
-// (S = 128 / G groups a chunk, at least 1), the rest zero.  The 16 rows hold
-// 16 / S tokens, and every lane of the result holds whole group sums of one
-// column.
+// Both kernels multiply with v_mfma_f32_16x16x32_bf16, which adds over the lane
+// groups of a column of codes, while groups with different scales must stay
+// apart.  So x is laid out block-diagonally: a row of the first operand holds x
+// of one 32-block (one row of x: w4_lane_kernel) or of one token's blocks with
+// one scale (several: w4_few_kernel) and zeros elsewhere, and every result is a
+// whole sum under one scale.
+//
+// Bound by memory: 4 bits a weight and the scales.  Matrices in the caches' reach
+// and small ones are bound by the start and end of a stream: the first loads, the
+// join over the waves, one launch.
 #include "common.h"
 #include "launch.h"
 #include "lds_load.h"
@@ -134,16 +136,17 @@ __device__ __forceinline__ float quad_xor(float v) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
 
-// Lane sums: for up to TT tokens a wave multiplies 4 rows x 512 k of codes at a
-// time, 1 KiB in one load of whole 256-byte runs.  Lane l holds 32 codes of one
+// A wave multiplies 4 rows x 512 k of codes at a time, 1 KiB in one load of whole
+// 256-byte runs (loads in the matrix unit's order would be 64 cache accesses a
+// KiB instead of 16, and the L1 takes one a cycle).  Lane l holds 32 codes of one
 // row, r = (l & 15) >> 2, and one 32-block, b = 4 (l >> 4) + (l & 3), and needs
-// the sum over just these.  The matrix unit adds over the four lanes groups of a
-// column and shares x between columns, so x is laid out with a row per block:
-// row 4 g + s of the first operand holds x of block 4 g + s in lane group g and
-// zeros elsewhere.  Result register i of lane l is then block 4 (l >> 4) + i
-// against the codes of column l & 15, of which the lane's own is i = l & 3.  The
-// lane's scale and zero point are those of the block, loaded as it loads the
-// codes; x and its block sums stay in registers for all rows.
+// the sum over just these.  The matrix unit adds over the four lanes of a column
+// and shares x between columns, so x is laid out with a row per block: row 4 g + s
+// of the first operand holds x of block 4 g + s in lane group g and zeros
+// elsewhere.  Result register i of lane l is then block 4 (l >> 4) + i against the
+// codes of column l & 15, of which the lane's own is i = l & 3.  The lane's scale
+// and zero point are those of the block, loaded as it loads the codes; x and its
+// block sums stay in registers for all rows.
 //
 // Waves of a workgroup take units of 512 k (of a token's experts one after the
 // other: SUM) of the same rows, blocks of 8 row quads after one another (with
@@ -151,6 +154,12 @@ __device__ __forceinline__ float quad_xor(float v) {
 // all of its blocks and units in a ring; a block's sums over the lanes of a row
 // and over the waves are joined in LDS, in order, while the next block's loads
 // are on their way.
+//
+// Measured, one row, groups of 128: 131,072 x 4,096 46 to 48 us (5.8 TB/s of codes
+// and scales, above a copy's 5.1: nothing is written), 8,192 x 8,192 10.5, 4,096
+// x 4,096 5.4 (1.7 at a copy's rate: the launch and the stream's two ends are the
+// rest).  Six experts of one token (57 MB) 13.9, 42 pairs summed per token (231 MB)
+// 39.5 to 44.
 constexpr int W4_NT = 2;       // non-temporal: codes are read once
 constexpr int W4_WAVES = 8;
 constexpr int W4_RING = 8;     // loads of 1 KiB in flight per wave, and row quads of a block
@@ -372,7 +381,8 @@ static hipError_t launch_w4_lane_t(const W4Args& a, int64_t row_blocks, hipStrea
   const int64_t blocks = (cols + ROWS - 1) / ROWS;
   const int64_t units = (a.K + 511) / 512 * (SUM ? a.k : 1);
   const int waves = units < W4_WAVES ? (int)units : W4_WAVES;
-  // as many workgroups as the CUs hold at once, where there are as many blocks
+  // two workgroups of 8 waves to a CU, where there are as many blocks (28,672 x
+  // 4,096: 14.3 us, one to a CU 13.8, four 15.0; 131,072: 48.3, 48.9, 48.1)
   constexpr int ROOM = 512;
   const int64_t per = (blocks * row_blocks + ROOM - 1) / ROOM;
   la.blocks = (int)w4_hold(per < blocks ? per : blocks, ROWS, a.K);
@@ -394,12 +404,26 @@ static hipError_t launch_w4_lane(const W4Args& a, int act, hipStream_t stream) {
 // A few more tokens: x in registers, 16 columns at a time
 // ---------------------------------------------------------------------------
 
-// Up to 16 / S tokens of a dense product.  The operands are laid out as in
-// w4_gemv_kernel (one block of tokens), and the walk is w4_lane_kernel's: a wave
-// keeps x of its 512 k (four chunks) in registers, with the sums of x per group,
-// and goes through 16-column tiles, two to a block (with ACT a gate and an up
-// tile).  A tile's scales and zero points are loaded by lane group g for chunk g
-// and handed to the lanes that need them through the LDS crossbar.
+// 16 / S tokens of a dense product, S = 128 / G scale groups of a chunk of 128 k
+// (at least 1); more tokens are more row blocks.  In a chunk lane l holds the 16
+// bytes of column n = l & 15 and 32-block g = l >> 4, and one of four matrix
+// instructions multiplies 8 k of all four blocks.  Row r of the first operand is
+// token r / S with the lane groups of scale group r % S alone, the rest zero; a
+// lane's four results are whole group sums of one column.
+//
+// The walk is w4_lane_kernel's: a wave keeps x of its 512 k (four chunks) in
+// registers, with the sums of x per group, and goes through 16-column tiles, BT to
+// a block (with ACT half of them gate and half up tiles).  Codes are loaded in
+// runs of 256 bytes and turned into the operand's order through LDS of the wave's
+// own; a tile's scales and zero points are loaded by lane group g for chunk g and
+// handed to the lanes that need them through the LDS crossbar.
+//
+// Measured (us; 131,072 x 4,096): groups of 128, 2 rows 53, 16 rows 60, 64 rows
+// 170; groups of 32, 2 to 4 rows 51 to 54, 5 to 8 (two row blocks) 77.  4,096 x
+// 4,096: groups of 32, 2 to 8 rows 6.2, 16 rows 9, 64 rows 21; groups of 128, 64
+// rows 11.8.  One row block is bound by memory (5.2 TB/s at 2 rows); with more the
+// codes come from L2 and each is converted and multiplied again for every row
+// block, which bounds it then: that product is for few rows.
 template <int S, bool ACT, bool SB, bool VEC, bool Z, int BT>
 __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   const W4Args& p = la.a;
@@ -601,7 +625,9 @@ static hipError_t launch_w4_few_t(const W4Args& a, hipStream_t stream) {
 
 template <int S, bool SB, bool VEC, bool Z>
 static hipError_t launch_w4_few_z(const W4Args& a, int act, hipStream_t stream) {
-  // four tiles a block where that still leaves a block per CU
+  // four tiles a block where that still leaves a block per CU: one join for twice
+  // the codes (131,072 x 4,096, 5 rows, groups of 128: 55.7 us, 60.4 with two);
+  // else two, so that more CUs have one (4,096 x 4,096: 6.7, 10.1 with four)
   const int64_t rows = (a.T + 16 / S - 1) / (16 / S), wide = a.N / 64 * rows;
   if (wide >= 256)
     return act ? launch_w4_few_t<S, true, SB, VEC, Z, 4>(a, stream) : launch_w4_few_t<S, false, SB, VEC, Z, 4>(a, stream);
@@ -645,7 +671,7 @@ hipError_t launch_w4_gemv(const uint8_t* codes, const void* scales, int scale_bf
   a.y_bf16 = y_bf16;
   a.col_groups = 0;
   // One row: a lane's own codes, the fewest instructions and cache accesses a
-  // code (131,072 x 4,096, groups of 128: 46 us, 52 with two rows of the other).
+  // code (131,072 x 4,096, groups of 128: 48 us, 53 for two rows of the other).
   // More: 16 columns at a time (4,096 x 4,096, 4 rows, groups of 32: 6.1 us; the
   // lane kernel with four rows in registers took 7.6, with eight 11.6).
   if (ids || T == 1) {

@@ -40,7 +40,8 @@ SHAPES = [(17, 2912, 2704), (1414, 4144, 144), (676, 16, 2824), (921, 32, 8), (2
           (2798, 2752, 272), (33, 784, 16), (18, 992, 8), (2078, 1712, 136), (2209, 1104, 24), (29, 928, 24),
           (18, 2432, 8), (2354, 16, 1688), (2707, 2640, 672), (2766, 1456, 272), (2339, 2320, 136), (65, 3680, 2104),
           (2482, 16, 3144), (199, 784, 3040), (27, 400, 16), (2476, 3120, 8), (193, 4480, 8), (199, 4192, 72),
-          (98, 4336, 8), (16, 4112, 2056), (9, 6000, 264), (1, 4400, 8200)]
+          (98, 4336, 8), (16, 4112, 2056), (9, 6000, 264), (1, 4400, 8200), (237, 2832, 200), (250, 4112, 1032),
+          (450, 2832, 72), (513, 4112, 520)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
