@@ -536,8 +536,9 @@ def _is_bits16(t, name):
 
 def _one_device(index, *tensors):
     for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise MoeGmmError("the tensors must be on one device, got cuda:%d and %s" % (index, t.device))
+        if t is not None and not (isinstance(t, _Tensor) and t.get_device() == index):
+            raise MoeGmmError("the tensors must be on one device, got cuda:%d and %s"
+                              % (index, getattr(t, "device", type(t))))
 
 
 def _enqueue(fn, index, args):

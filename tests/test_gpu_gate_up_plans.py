@@ -163,6 +163,12 @@ def test_refusals():
         moe.gate_up_bwd(dh, x, w, pre, ws=big[128:])
     with pytest.raises(E):
         moe.gate_up_bwd(dh, x, w, pre, ws=big.cpu())
+    for kw in (dict(out=[]), dict(preact=[]), dict(out=torch.empty((8, 16))), dict(preact=torch.empty((8, 32)))):
+        with pytest.raises(E):
+            moe.gate_up(x, w, **kw)                                 # no device tensors
+    for kw in (dict(dx=[]), dict(dw13=[]), dict(ws=1), dict(dx=torch.empty((8, 64))), dict(dw13=torch.empty((32, 64)))):
+        with pytest.raises(E):
+            moe.gate_up_bwd(dh, x, w, pre, **kw)
 
 
 def test_rows_past_32_bit_offsets():
