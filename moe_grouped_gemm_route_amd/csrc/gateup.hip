@@ -160,35 +160,39 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 // the barrier.  The wait before it is a full one: direct-to-LDS loads are not
 // counted as still on their way.
 //
-// REGS: the loads go through registers instead, two stages ahead.  The wait for
-// a register is counted by the compiler, so a stage has two stages' time to
-// land, which short stages need (K 4,096, 2,048 columns of h, us through LDS and
-// through registers: 64 rows in 32 x 64 tiles 18.9, 16.0; 256 rows in 64 x 64
-// 24.2, 21.8; 512 rows in 64 x 128 33.5, 30.0; dx of 64 rows in 64 x 128 14.4,
-// 12.8).  Larger tiles load to LDS: their stages hide the loads (128 x 256 65.9,
-// 69.2), and with the sums their registers spill (128 x 128 in two groups 40.7,
-// 86.2).
+// TURNS: half of the waves load the even stages and half the odd ones, each wave
+// twice as much, into three buffers.  A wave waits, fully, at every other barrier,
+// so that two stages are on their way at a time and a stage has two stages' time
+// to land.  Tiles of which three stages fit LDS do this (us with and without, K
+// 4,096, 2,048 columns of h: 64 rows in 32 x 64 tiles 14.7, 19.0; 256 rows in 64
+// x 64 19.6, 27.4; 512 rows in 64 x 128 26.8, 33.4; 2,048 rows in 128 x 256 59.5,
+// 63.6; dx of 1,237 rows of 2,560, a sum over 2,832, in 128 x 128 30.1, 36.1).
+// Loads alone, without products, take 0.67 us a stage of 128 x 128 tiles with one
+// stage on its way, 0.41 with two, 0.47 with four: one more half of the waves and
+// one more buffer are worth it, three more are not.
 //
 // What bounds it.  256 x 256 tiles: the matrix pipes, 1.34 PFLOP/s forward and
 // 1.18 to 1.26 backward at 4,096 rows, where a library product reaches 1.22 to
 // 1.26; 53 % of the pipes' cycles at the clock that the chip holds.  Of 116 us of
 // such a product 88 are left without the loads, 91 without the LDS reads and 71
-// without the matrix instructions.  Smaller tiles: the loads on their way from
-// L2 (about 15 TB/s over the chip; 340 to 470 cycles each), since with fewer rows
-// each weight meets less work.  Tried and not faster: 4 waves of 128 x 128
+// without the matrix instructions.  Smaller tiles: the loads from L2 (14 to 18 TB/s
+// over the chip with two stages on their way), since with fewer rows each weight
+// meets less work.  Tried and not faster: 4 waves of 128 x 128
 // (116 to 124 for 110), half or three eighths of the groups behind the barrier,
 // loads between single matrix instructions.
-template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, bool REGS, int OCC>
+template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, bool TURNS, int OCC>
 __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArgs p) {
   constexpr int NW = WI * WJ;
+  constexpr int LW = TURNS ? NW / 2 : NW;          // waves that load a slice
+  constexpr int BUFS = TURNS ? 3 : 2;
   constexpr int BM = WI * SI * 16, BN = WJ * SJ * 16;
-  typedef Operand<AROW, BM, NW, false> OpA;
-  typedef Operand<BROW, BN, NW, !BROW> OpB;
+  typedef Operand<AROW, BM, LW, false> OpA;
+  typedef Operand<BROW, BN, LW, !BROW> OpB;
   constexpr int A_BYTES = PARTS * OpA::BYTES;
   constexpr int SLICE = A_BYTES + OpB::BYTES;
   constexpr int STAGE = KG * SLICE;
   constexpr int JOIN = (KG - 1) * BM * BN * 4;
-  constexpr int LDS = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
+  constexpr int LDS = BUFS * STAGE > JOIN ? BUFS * STAGE : JOIN;
   static_assert(!GATE || !BROW, "w13's rows are columns of out");
   static_assert(!GATE || SJ == 4, "a wave holds a pair of gate and a pair of up subtiles");
   __shared__ __attribute__((aligned(1024))) uint8_t s_all[LDS];
@@ -196,8 +200,12 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kg = KG > 1 ? wid / NW : 0;
-  const int wave = wid % NW;
-  const int wi = wave / WJ, wj = wave % WJ;
+  const int wi = wid % NW / WJ, wj = wid % NW % WJ;
+  // what this wave loads: share `wave` of group lg's slice, with TURNS of the
+  // stages of parity `turn` (each SIMD holds waves of both)
+  const int turn = TURNS ? wid / (LW * KG) : 0;
+  const int lg = TURNS ? wid % (LW * KG) / LW : kg;
+  const int wave = wid % LW;
 
   const int tiles = p.tiles_i * p.tiles_j;
   const int split = blockIdx.x / (uint32_t)tiles;
@@ -237,8 +245,8 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
 
   // The next stage to load: this group's KG stages on from its last.
   const int stages = (p.R + GU_BK - 1) / GU_BK;
-  int at = split * p.steps * KG + kg;
-  const uint32_t l0 = lds_addr(s_all) + kg * SLICE;
+  int at = (split * p.steps + turn) * KG + lg;
+  const uint32_t l0 = lds_addr(s_all) + lg * SLICE;
   constexpr uint32_t OPEN = 0x7FFE0000u;   // lanes outside are marked: the range need not end anywhere
   auto load_a = [&](int buf) __attribute__((always_inline)) {
     const bool live = at < stages;
@@ -273,45 +281,8 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
   auto load_stage = [&](int buf) __attribute__((always_inline)) {
     load_a(buf);
     load_b(buf);
-    at += KG;
+    at += (TURNS ? 2 : 1) * KG;
   };
-  // The same through registers: a stage's share of this wave, and its place.
-  struct Held {
-    u32x4_t a[PARTS * OpA::LOADS], b[OpB::LOADS];
-  };
-  auto fetch = [&](Held& h) __attribute__((always_inline)) {
-    const bool live = at < stages;
-    const int r0 = live ? at * GU_BK : 0;
-    const int left = p.R - r0;
-    const uint32_t abytes = !live ? 0 : AROW ? (uint32_t)((min(left, GU_BK) * p.lda - i0) * 2) : OPEN;
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q) {
-      const __amdgpu_buffer_rsrc_t rs =
-          gu_rsrc(p.a + q * p.part_stride + (AROW ? (int64_t)r0 * p.lda + i0 : (int64_t)i0 * p.lda + r0), abytes);
-#pragma unroll
-      for (int j = 0; j < OpA::LOADS; ++j)
-        h.a[q * OpA::LOADS + j] =
-            __builtin_amdgcn_raw_buffer_load_b128(rs, AROW || aseg[j] < left ? avo[j] : kLaneOob, 0, 0);
-    }
-    const uint16_t* base = p.b + (BROW ? (int64_t)r0 * p.ldb + j0 : (int64_t)j0 * p.ldb + r0);
-    const uint32_t bbytes = !live ? 0 : BROW ? (uint32_t)((min(left, GU_BK) * p.ldb - j0) * 2) : OPEN;
-    const __amdgpu_buffer_rsrc_t rs = gu_rsrc(base, bbytes);
-    const __amdgpu_buffer_rsrc_t ru = GATE ? gu_rsrc(base + (int64_t)p.J * p.ldb, bbytes) : rs;
-#pragma unroll
-    for (int j = 0; j < OpB::LOADS; ++j)
-      h.b[j] = __builtin_amdgcn_raw_buffer_load_b128(up[j] ? ru : rs, BROW || bseg[j] < left ? bvo[j] : kLaneOob, 0, 0);
-    at += KG;
-  };
-  constexpr int PUTS = PARTS * OpA::LOADS + OpB::LOADS;
-  auto put = [&](const Held& h, int buf, int k) __attribute__((always_inline)) {
-    uint8_t* to = s_all + buf * STAGE + kg * SLICE + lane * 16;
-    if (k < PARTS * OpA::LOADS)
-      *reinterpret_cast<u32x4_t*>(to + k / OpA::LOADS * OpA::BYTES + (wave * OpA::LOADS + k % OpA::LOADS) * 1024) = h.a[k];
-    else
-      *reinterpret_cast<u32x4_t*>(to + A_BYTES + (wave * OpB::LOADS + k - PARTS * OpA::LOADS) * 1024) =
-          h.b[k - PARTS * OpA::LOADS];
-  };
-
   f32x4_t acc[SI][SJ];
 #pragma unroll
   for (int a = 0; a < SI; ++a)
@@ -336,35 +307,21 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
   };
 
   const int steps = p.steps;
-  Held held[2];
-  if constexpr (REGS) {
-    fetch(held[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    fetch(held[1]);
-    __builtin_amdgcn_sched_barrier(0);
+  auto first = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < PUTS; ++k) put(held[0], 0, k);
-    __builtin_amdgcn_sched_barrier(0);
-    fetch(held[0]);
-    __builtin_amdgcn_sched_barrier(0);
-  } else {
-    load_stage(0);
-    load_stage(1);
-    vm_wait();
-  }
-  lds_barrier();
+    for (int s = 0; s < SJ; ++s) read_b(0, 0, s);
 #pragma unroll
-  for (int s = 0; s < SJ; ++s) read_b(0, 0, s);
-#pragma unroll
-  for (int q = 0; q < CA; ++q) read_a(0, q);
+    for (int q = 0; q < CA; ++q) read_a(0, q);
+  };
 
-  // Stage st, from buffer buf.  `next`: what the registers hold of stage st + 1.
-  auto step = [&](int buf, Held& next) __attribute__((always_inline)) {
+  // Stage st, from buffer buf; stage st + 1 is in buffer `after`.  `mine`: this
+  // wave's loads are of stage st + 1, and then of the one that takes st's place.
+  auto step = [&](int buf, int after, bool mine) __attribute__((always_inline)) {
     // reads in the order of need: A of the first half and B of the second
     // between them, then A of the second
     constexpr int READS = NQ - CA + SJ;
     constexpr int FRONT = NQ - HOLD;               // groups before the barrier
-    int done = 0, puts = 0;
+    int done = 0;
 #pragma unroll
     for (int q = 0; q < FRONT; ++q) {
       __builtin_amdgcn_sched_barrier(0);
@@ -386,27 +343,13 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
       }
       done = upto;
       mults(q);
-      if constexpr (REGS) {
-        // the next stage goes to the other buffer in the first half of the
-        // groups, and the registers take the stage after the one that follows it
-        constexpr int OVER = FRONT >= 4 ? FRONT / 2 : 1;
-        const int all = q + 1 >= OVER ? PUTS : PUTS * (q + 1) / OVER;
-#pragma unroll
-        for (int k = 0; k < PUTS; ++k)
-          if (k >= puts && k < all) put(next, buf ^ 1, k);
-        if (q == OVER - 1) {
-          __builtin_amdgcn_sched_barrier(0);
-          fetch(next);
-        }
-        puts = all;
-      }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (!REGS) vm_wait();
+    if (mine) vm_wait();
     lds_barrier();
     u32x4_t na[CA], nb[SJ];
     {
-      const uint8_t* nx = s_all + (buf ^ 1) * STAGE + kg * SLICE;
+      const uint8_t* nx = s_all + after * STAGE + kg * SLICE;
 #pragma unroll
       for (int s = 0; s < SJ; ++s) nb[s] = OpB::read(nx + A_BYTES, wj * SJ * 16, s, 0);
 #pragma unroll
@@ -416,38 +359,64 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
 #pragma unroll
     for (int q = NQ - HOLD; q < NQ; ++q) {
       mults(q);
-      if constexpr (!REGS) {
-        __builtin_amdgcn_sched_barrier(0);
-        if (q == NQ - HOLD) {
-          load_a(buf);
-          if (HOLD == 1) load_b(buf);
-        }
-        if (q == NQ - HOLD + 1) load_b(buf);
+      __builtin_amdgcn_sched_barrier(0);
+      if (q == NQ - HOLD && mine) {
+        load_a(buf);
+        if (HOLD == 1) load_b(buf);
       }
+      if (q == NQ - HOLD + 1 && mine) load_b(buf);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (!REGS) at += KG;
+    if (mine) at += (TURNS ? 2 : 1) * KG;
 #pragma unroll
     for (int s = 0; s < SJ; ++s) fb[0][s] = nb[s];
 #pragma unroll
     for (int q = 0; q < CA; ++q) fa[q] = na[q];
   };
-  if constexpr (REGS) {
+  if constexpr (TURNS) {
+    int st = 0, buf = 0;
+    auto one = [&](bool mine) __attribute__((always_inline)) {
+      const int after = buf == 2 ? 0 : buf + 1;
+      step(buf, after, mine);
+      buf = after;
+      return ++st < steps;
+    };
+    // Stage 1 is the other half's: the waves that have loaded stage 0 begin with a
+    // step without loads.  From there on a step with and one without follow one
+    // another for every wave.
+    bool more = true;
+    if (turn == 0) {
+      load_stage(0);
+      vm_wait();
+      lds_barrier();
+      load_stage(2);
+      first();
+      more = one(false);
+    } else {
+      load_stage(1);
+      lds_barrier();
+      first();
+    }
 #pragma unroll 1
-    for (int st = 0; st < steps; st += 2) {
-      step(0, held[1]);
-      if (st + 1 >= steps) break;
-      step(1, held[0]);
+    while (more) {
+      more = one(true);
+      if (!more) break;
+      more = one(false);
     }
   } else {
+    load_stage(0);
+    load_stage(1);
+    vm_wait();
+    lds_barrier();
+    first();
 #pragma unroll 1
-    for (int st = 0; st < steps; ++st) step(st & 1, held[0]);
-    vm_wait();    // the loads past the last stage land before LDS is used again
+    for (int st = 0; st < steps; ++st) step(st & 1, st & 1 ^ 1, true);
   }
+  vm_wait();      // the loads past the last stage land before LDS is used again
 
   if constexpr (KG > 1) {
     lds_barrier();
-    f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_all) + wave * SI * SJ * 64 + lane;
+    f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_all) + wid % NW * SI * SJ * 64 + lane;
     constexpr int GROUP = NW * SI * SJ * 64;
     if (kg > 0) {
 #pragma unroll
@@ -491,7 +460,7 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
   }
 }
 
-template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, bool REGS, int OCC>
+template <bool AROW, bool BROW, int WI, int WJ, int SI, int SJ, int KG, int PARTS, bool GATE, bool TURNS, int OCC>
 static hipError_t launch_tiles(TileArgs a, hipStream_t stream) {
   constexpr int BM = WI * SI * 16, BN = WJ * SJ * 16, CN = GATE ? BN / 2 : BN;
   a.tiles_i = (a.I + BM - 1) / BM;
@@ -499,7 +468,7 @@ static hipError_t launch_tiles(TileArgs a, hipStream_t stream) {
   const int stages = ((a.R + GU_BK - 1) / GU_BK + KG - 1) / KG;
   a.steps = (stages + a.splits - 1) / a.splits;
   const int64_t groups = (int64_t)a.tiles_i * a.tiles_j * a.splits;
-  hipLaunchKernelGGL((gu_tile_kernel<AROW, BROW, WI, WJ, SI, SJ, KG, PARTS, GATE, REGS, OCC>), dim3((unsigned)groups),
+  hipLaunchKernelGGL((gu_tile_kernel<AROW, BROW, WI, WJ, SI, SJ, KG, PARTS, GATE, TURNS, OCC>), dim3((unsigned)groups),
                      dim3(WI * WJ * KG * 64), 0, stream, a);
   return hipGetLastError();
 }
@@ -538,7 +507,7 @@ struct StreamArgs {
 // Bound by memory where the weights come from there, and by the start of the
 // stream where they do not (33.6 MB of w13, one row: 10.7 us a call, 8.0 at best,
 // for 6.6 at a copy's rate).  Tiles with 17 rows and more: at 16 rows the stream
-// takes 11.6 us, the smallest tiles 14.9; a row more would take a second x.
+// takes 11.6 us, at 17 the smallest tiles 15.8; a row more would take a second x.
 constexpr int GS_WAVES = 8;
 constexpr int GS_ROWS = 16;
 
@@ -770,17 +739,17 @@ int64_t gate_up_workgroups(int32_t M, int32_t N, int32_t K) {
 // of the least estimate: whole rounds of workgroups, and for shares the sums
 // written, read and added at 4.5 TB/s in one more launch.  The sides measured, us
 // (the instance taken first; sN: in N shares, without the launch that adds them):
-//   gate/up, K 4,096, 2,048 columns of h: 64 rows 32 x 64 tiles 16.0, 64 x 64
-//     19.4, 64 x 128 27; 256 rows 64 x 64 21.8, 64 x 128 28.5, 32 x 64 28.7; 512
-//     rows 64 x 128 30.0, 64 x 64 37.9, 128 x 128 38.2; 1,024 rows 128 x 128
-//     40.7, 64 x 128 53.2, 128 x 256 58; 2,048 rows 128 x 256 65.9, 128 x 128
-//     75.9, 256 x 256 88.6; 4,096 rows 256 x 256 102.7, 128 x 256 124.5
-//   dx of 1,237 rows (2,560 columns, sum over 2,832): 128 x 128 36.2, 128 x 256
-//     in s2 33.2, 256 x 256 in s4 36.8, 64 x 128 40.5
-//   dx of 64 rows (4,096 columns and sums): 64 x 128 in s8 12.8, s4 14.1, 128 x
-//     128 in s8 15.5
-//   dw13 of 2,832 x 2,560 over 1,237 rows: 256 x 128 30.3, 128 x 256 31.9, 256 x
-//     256 in s2 33.4, alone 44.7; 128 x 128 37.5
+//   gate/up, K 4,096, 2,048 columns of h: 64 rows 32 x 64 tiles 14.7, 64 x 64
+//     18.4, 64 x 128 24.5; 256 rows 64 x 64 19.6, 64 x 128 25.3, 32 x 64 26.4; 512
+//     rows 64 x 128 26.8, 64 x 64 34.1, 128 x 128 36.3; 1,024 rows 128 x 128
+//     38.5, 64 x 128 47.3, 128 x 256 50.5; 2,048 rows 128 x 256 59.5, 128 x 128
+//     75.6, 256 x 256 93.3; 4,096 rows 256 x 256 106.7, 128 x 256 113.4
+//   dx of 1,237 rows (2,560 columns, sum over 2,832): 128 x 128 30.1, 128 x 256
+//     in s2 30.4, 64 x 128 35.8, 256 x 256 in s4 37.1
+//   dx of 64 rows (4,096 columns and sums): 64 x 128 in s8 12.2, s4 13.3, 128 x
+//     128 in s8 13.3; from three parts 64 x 128 in s8 15.8, 64 x 256 in s8 19.3
+//   dw13 of 2,832 x 2,560 over 1,237 rows: 256 x 128 27.9, 128 x 128 31.9, 256 x
+//     256 in s2 33.5, alone 44.7
 struct TileConfig {
   int bm, bn, kg, fit;    // rows, columns (gate and up: of w13), groups, workgroups that run at once
   float stage, alone;     // a stage with `fit` workgroups, and with one per CU at most
@@ -813,26 +782,25 @@ static TilePlan tile_plan(const TileConfig (&configs)[COUNT], int gate, int64_t 
   return best;
 }
 
-static const TileConfig kForward[] = {{256, 256, 1, 256, 1.57f, 1.57f}, {128, 256, 1, 256, .98f, .98f},
-                                      {128, 128, 2, 256, .58f, .58f},   {64, 128, 2, 256, .42f, .42f},
-                                      {64, 64, 4, 256, .29f, .29f},     {32, 64, 4, 256, .2f, .2f}};
-static const TileConfig kDx[] = {{256, 256, 1, 256, 1.65f, 1.65f}, {128, 256, 1, 256, .95f, .95f},
-                                 {128, 128, 2, 256, .58f, .58f}, {64, 128, 1, 768, .7f, .7f},
-                                 {64, 128, 2, 256, .4f, .4f}};
-static const TileConfig kDx3[] = {{128, 256, 1, 256, 2.1f, 2.1f}, {64, 256, 1, 256, 1.25f, 1.4f},
-                                  {64, 128, 1, 512, 1.3f, 1.05f}};
-static const TileConfig kDw[] = {{256, 256, 1, 256, 1.7f, 1.7f}, {256, 128, 1, 256, 1.f, 1.f},
-                                 {128, 128, 2, 256, .58f, .58f}};
+static const TileConfig kForward[] = {{256, 256, 1, 256, 1.57f, 1.57f}, {128, 256, 1, 256, .88f, .88f},
+                                      {128, 128, 1, 256, .56f, .56f},   {64, 128, 2, 256, .37f, .37f},
+                                      {64, 64, 2, 256, .26f, .26f},     {32, 64, 4, 256, .19f, .19f}};
+static const TileConfig kDx[] = {{256, 256, 1, 256, 1.65f, 1.65f}, {128, 256, 1, 256, .93f, .93f},
+                                 {128, 128, 1, 256, .6f, .6f}, {64, 128, 1, 512, .68f, .4f}};
+static const TileConfig kDx3[] = {{128, 256, 1, 256, 2.1f, 2.1f}, {64, 256, 1, 256, 1.3f, 1.3f},
+                                  {64, 128, 1, 256, .7f, .7f}};
+static const TileConfig kDw[] = {{256, 256, 1, 256, 1.7f, 1.7f}, {256, 128, 1, 256, .93f, .93f},
+                                 {128, 128, 1, 256, .6f, .6f}};
 static const TileConfig kDw3[] = {{128, 256, 1, 256, 2.2f, 2.2f}};
 constexpr int GU_SPLITS = 16;
 
 static hipError_t launch_forward(int config, const TileArgs& a, hipStream_t s) {
   switch (config) {
     case 0: return launch_tiles<false, false, 2, 4, 8, 4, 1, 1, true, false, 2>(a, s);
-    case 1: return launch_tiles<false, false, 2, 4, 4, 4, 1, 1, true, false, 2>(a, s);
-    case 2: return launch_tiles<false, false, 2, 2, 4, 4, 2, 1, true, false, 2>(a, s);
+    case 1: return launch_tiles<false, false, 2, 4, 4, 4, 1, 1, true, true, 2>(a, s);
+    case 2: return launch_tiles<false, false, 4, 2, 2, 4, 1, 1, true, true, 2>(a, s);
     case 3: return launch_tiles<false, false, 2, 2, 2, 4, 2, 1, true, true, 2>(a, s);
-    case 4: return launch_tiles<false, false, 4, 1, 1, 4, 4, 1, true, true, 4>(a, s);
+    case 4: return launch_tiles<false, false, 4, 1, 1, 4, 2, 1, true, true, 2>(a, s);
     default: return launch_tiles<false, false, 2, 1, 1, 4, 4, 1, true, true, 2>(a, s);
   }
 }
@@ -840,15 +808,14 @@ static hipError_t launch_forward(int config, const TileArgs& a, hipStream_t s) {
 static hipError_t launch_dx(int parts, int config, const TileArgs& a, hipStream_t s) {
   if (parts == 1) switch (config) {
     case 0: return launch_tiles<false, true, 2, 4, 8, 4, 1, 1, false, false, 2>(a, s);
-    case 1: return launch_tiles<false, true, 2, 4, 4, 4, 1, 1, false, false, 2>(a, s);
-    case 2: return launch_tiles<false, true, 2, 2, 4, 4, 2, 1, false, false, 2>(a, s);
-    case 3: return launch_tiles<false, true, 2, 2, 2, 4, 1, 1, false, false, 3>(a, s);
-    default: return launch_tiles<false, true, 2, 2, 2, 4, 2, 1, false, true, 2>(a, s);
+    case 1: return launch_tiles<false, true, 2, 4, 4, 4, 1, 1, false, true, 2>(a, s);
+    case 2: return launch_tiles<false, true, 4, 2, 2, 4, 1, 1, false, true, 2>(a, s);
+    default: return launch_tiles<false, true, 4, 2, 1, 4, 1, 1, false, true, 4>(a, s);
   }
   switch (config) {
     case 0: return launch_tiles<false, true, 2, 4, 4, 4, 1, 3, false, false, 2>(a, s);
     case 1: return launch_tiles<false, true, 2, 4, 2, 4, 1, 3, false, false, 2>(a, s);
-    default: return launch_tiles<false, true, 2, 2, 2, 4, 1, 3, false, false, 2>(a, s);
+    default: return launch_tiles<false, true, 4, 2, 1, 4, 1, 3, false, true, 2>(a, s);
   }
 }
 
@@ -856,8 +823,8 @@ static hipError_t launch_dw(int parts, int config, const TileArgs& a, hipStream_
   if (parts == 3) return launch_tiles<true, true, 2, 4, 4, 4, 1, 3, false, false, 2>(a, s);
   switch (config) {
     case 0: return launch_tiles<true, true, 2, 4, 8, 4, 1, 1, false, false, 2>(a, s);
-    case 1: return launch_tiles<true, true, 4, 2, 4, 4, 1, 1, false, false, 2>(a, s);
-    default: return launch_tiles<true, true, 2, 2, 4, 4, 2, 1, false, false, 2>(a, s);
+    case 1: return launch_tiles<true, true, 4, 2, 4, 4, 1, 1, false, true, 2>(a, s);
+    default: return launch_tiles<true, true, 4, 2, 2, 4, 1, 1, false, true, 2>(a, s);
   }
 }
 

@@ -41,7 +41,8 @@ SHAPES = [(17, 2912, 2704), (1414, 4144, 144), (676, 16, 2824), (921, 32, 8), (2
           (18, 2432, 8), (2354, 16, 1688), (2707, 2640, 672), (2766, 1456, 272), (2339, 2320, 136), (65, 3680, 2104),
           (2482, 16, 3144), (199, 784, 3040), (27, 400, 16), (2476, 3120, 8), (193, 4480, 8), (199, 4192, 72),
           (98, 4336, 8), (16, 4112, 2056), (9, 6000, 264), (1, 4400, 8200), (237, 2832, 200), (250, 4112, 1032),
-          (450, 2832, 72), (513, 4112, 520)]
+          (450, 2832, 72), (513, 4112, 520), (774, 4224, 8), (1001, 2080, 8), (2795, 4048, 280), (2103, 3888, 136),
+          (1050, 992, 8), (2163, 1616, 152), (1, 976, 2176)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
