@@ -560,8 +560,8 @@ int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, 
  * y              out, f32 or bf16 (RNE).
  * Every row is written, whatever T; equal calls return equal bits.  The order of
  * the f32 sums depends on the sizes and on the form, not on the values.  Meant
- * for few rows: a dense call works through the weights once per 4, 8 or 16 rows
- * (groups of 32, 64, more), a routed one once per pair.
+ * for few rows: a dense call works through the weights once per 16 rows at best
+ * (groups of 32 or 64 and few rows: per 4 or 8), a routed one once per pair.
  * Limits: N <= 2^30, K <= 2^23, K % group == 0, N even with the activation,
  * E*N*K/2 < 2^40, T <= 2^24, 1 <= k <= 64, T*k <= 2^24; codes and x 16-byte
  * aligned, scales and y to their type; rows of y (dense: rows / 4, 8 or 16,

@@ -411,6 +411,13 @@ static hipError_t launch_w4_lane(const W4Args& a, int act, hipStream_t stream) {
 // token r / S with the lane groups of scale group r % S alone, the rest zero; a
 // lane's four results are whole group sums of one column.
 //
+// ALL: 16 tokens, also where a chunk has several scale groups.  A matrix
+// instruction takes 32 consecutive k, lane group g the 8 k from 8 g, so that its
+// results, or a chain's of G / 32, are whole group sums with no zeros laid out:
+// 4 / S as many converts a token, S as many sums to scale a chunk.  The sums of x
+// (S times as many too) lie in LDS, and with S = 4 chunks are finished one by one;
+// what does not fit the registers then is a few addresses.
+//
 // The walk is w4_lane_kernel's: a wave keeps x of its 512 k (four chunks) in
 // registers, with the sums of x per group, and goes through 16-column tiles, BT to
 // a block (with ACT half of them gate and half up tiles).  Codes are loaded in
@@ -419,20 +426,23 @@ static hipError_t launch_w4_lane(const W4Args& a, int act, hipStream_t stream) {
 // handed to the lanes that need them through the LDS crossbar.
 //
 // Measured (us; 131,072 x 4,096): groups of 128, 2 rows 53, 16 rows 60, 64 rows
-// 170; groups of 32, 2 to 4 rows 51 to 54, 5 to 8 (two row blocks) 77.  4,096 x
-// 4,096: groups of 32, 2 to 8 rows 6.2, 16 rows 9, 64 rows 21; groups of 128, 64
-// rows 11.8.  One row block is bound by memory (5.2 TB/s at 2 rows); with more the
-// codes come from L2 and each is converted and multiplied again for every row
-// block, which bounds it then: that product is for few rows.
-template <int S, bool ACT, bool SB, bool VEC, bool Z, int BT>
+// 170; groups of 32, 2 to 4 rows 51 to 54, 5 to 8 (two row blocks) 77, 9 to 16
+// (ALL) 78, 64 258 (509 by blocks of 4).  4,096 x 4,096: groups of 32, 2 to 8 rows
+// 6.2, 16 rows 9, 64 rows 15; groups of 128, 64 rows 11.8.  One row block is bound
+// by memory (5.2 TB/s at 2 rows); with more the codes come from L2 and each is
+// converted and multiplied again for every row block, which bounds it then: that
+// product is for few rows.
+template <int S, bool ALL, bool ACT, bool SB, bool VEC, bool Z, int BT>
 __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   const W4Args& p = la.a;
   constexpr int SZ = SB ? 2 : 4;
   constexpr int SW = SB ? (S + 1) / 2 : S;            // scale words of a chunk
-  constexpr int R = 4 / S;                            // tokens a lane holds
+  constexpr int D = ALL ? 1 : S;                      // rows of the operand that a token takes
+  constexpr int R = 4 / D;                            // tokens a lane holds
   constexpr int HALF = ACT ? BT / 2 : BT;             // tiles of a block that are columns of y
   __shared__ float s_sum[2][BT * R][W4_WAVES][64];
   __shared__ __attribute__((aligned(256))) uint8_t s_codes[W4_WAVES][4096];
+  __shared__ __attribute__((aligned(16))) float s_sx[ALL ? W4_WAVES : 1][ALL ? 4 * S : 1][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -446,7 +456,7 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   const int id = blockIdx.x >> 3;
   const int cg = id / la.row_blocks * 8 + (blockIdx.x & 7), rb = id % la.row_blocks;
   if (cg >= p.col_groups) return;
-  const int t0 = rb * (16 / S);                          // first token
+  const int t0 = rb * (16 / D);                          // first token
   const int row0 = cg * la.blocks * HALF * 16;           // first column of y
   const int rows = min(la.blocks * HALF * 16, cols - row0);
   const int blocks = (rows + HALF * 16 - 1) / (HALF * 16);
@@ -457,8 +467,9 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   const uint32_t cvo = (uint32_t)g * (uint32_t)(K / 2) + n16 * 16;
   uint8_t* own = s_codes[wave];
   const uint32_t srow = (uint32_t)(n16 * groups);
-  const bool mine = S == 1 || (S == 2 ? (g >> 1) == (n16 & 1) : g == (n16 & 3));
-  const uint32_t xrow = mine && t0 + n16 / S < p.T ? (uint32_t)(n16 / S * K * 2 + g * 64) : kLaneOob;
+  const bool mine = D == 1 || (S == 2 ? (g >> 1) == (n16 & 1) : g == (n16 & 3));
+  constexpr int XG = ALL ? 8 : 32, XS = ALL ? 32 : 8;    // k from a lane group, and a step, to the next
+  const uint32_t xrow = mine && t0 + n16 / D < p.T ? (uint32_t)(n16 / D * K * 2 + g * XG * 2) : kLaneOob;
 
   const f32x4_t zero4 = {0.f, 0.f, 0.f, 0.f};
   const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
@@ -496,27 +507,39 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   };
 
   u32x4_t x[4][4];
-  f32x4_t sx[4];
-  const __amdgpu_buffer_rsrc_t xr = w4_rsrc(p.x, (int64_t)t0 * K * 2, (int64_t)min(16 / S, p.T - t0) * K * 2);
+  constexpr int SX = ALL ? S : 1, CH = 4 / SX;           // sums of a chunk, and steps to each
+  f32x4_t sx[4];                                          // (not ALL: they lie in LDS)
+  const int64_t x0 = (int64_t)t0 * K * 2, xbytes = (int64_t)min(16 / D, p.T - t0) * K * 2;
   auto load_x = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const bool in = u * 512 + c * 128 + g * 32 < K;
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        x[c][s] = __builtin_amdgcn_raw_buffer_load_b128(xr, (in ? xrow : kLaneOob) + s * 16, u * 1024 + c * 256, 0);
+      for (int s = 0; s < 4; ++s) {
+        const bool in = u * 512 + c * 128 + (ALL ? s : g) * 32 < K;
+        x[c][s] = __builtin_amdgcn_raw_buffer_load_b128(w4_rsrc(p.x, x0, !ALL || in ? xbytes : 0),
+                                                        (ALL || in ? xrow : kLaneOob) + s * XS * 2, u * 1024 + c * 256, 0);
+      }
     }
   };
   auto sum_x = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      sx[c] = zero4;
+      f32x4_t v[SX];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         x[c][s] = x_order(x[c][s]);
-        sx[c] = w4_mfma(x[c][s], ones, sx[c]);
+        v[s / CH] = w4_mfma(x[c][s], ones, s % CH ? v[s / CH] : zero4);
+      }
+      if constexpr (ALL) {
+        if (n16 == 0) {
+#pragma unroll
+          for (int o = 0; o < S; ++o) *reinterpret_cast<f32x4_t*>(&s_sx[wave][c * S + o][g * 4]) = v[o];
+        }
+      } else {
+        sx[c] = v[0];
       }
     }
+    if (ALL) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
 
   load_x(wave);
@@ -534,45 +557,76 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
     for (int u = wave; u < total; u += waves) {
 #pragma unroll
       for (int i = 0; i < BT; ++i) {
-        f32x4_t d[4];
         uint32_t sw[4][S], zw[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        auto scales_of = [&](int c) __attribute__((always_inline)) {
           const int from = (n16 | c << 4) << 2;
 #pragma unroll
           for (int j = 0; j < SW; ++j) sw[c][j] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)ring[i].scale[j]);
           zw[c] = Z ? (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)ring[i].zero) : 0x08080808u;
-        }
+        };
+        if constexpr (!(ALL && S == 4))
+#pragma unroll
+          for (int c = 0; c < 4; ++c) scales_of(c);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<u32x4_t*>(own + (c * 4 + g) * 256 + ((n16 ^ (c * 4 + g)) << 4)) = ring[i].codes[c];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        u32x4_t q[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          q[c] = *reinterpret_cast<const u32x4_t*>(own + n16 * 256 + (((c * 4 + g) ^ n16) << 4));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          d[c] = zero4;
-#pragma unroll
-          for (int s = 0; s < 4; ++s) d[c] = w4_mfma(x[c][s], codes_to_bf16(q[c][s]), d[c]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        load(i, ring[i]);
-        __builtin_amdgcn_sched_barrier(0);
         float acc[R];
 #pragma unroll
         for (int j = 0; j < R; ++j) acc[j] = 0.f;
+        f32x4_t d[4][SX];
+        auto products = [&](int c) __attribute__((always_inline)) {
+          u32x4_t q;
+          if constexpr (ALL) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+            for (int s = 0; s < 4; ++s)
+              q[s] = *reinterpret_cast<const uint32_t*>(own + n16 * 256 + (((c * 4 + s) ^ n16) << 4) + g * 4);
+          } else {
+            q = *reinterpret_cast<const u32x4_t*>(own + n16 * 256 + (((c * 4 + g) ^ n16) << 4));
+          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int o = j % S;
+          for (int s = 0; s < 4; ++s)
+            d[c][s / CH] = w4_mfma(x[c][s], codes_to_bf16(q[s]), s % CH ? d[c][s / CH] : zero4);
+        };
+        auto add = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+          for (int o = 0; o < S; ++o) {
             const float sc = SB ? ((o & 1) ? bf16_hi(sw[c][o >> 1]) : bf16_lo(sw[c][o >> 1])) : __uint_as_float(sw[c][o]);
             const float z = (float)((zw[c] >> (8 * o)) & 0xFFu);
-            acc[j / S] = fmaf(sc, fmaf(-z, sx[c][j], d[c][j]), acc[j / S]);
+            f32x4_t v;
+            if constexpr (ALL) v = *reinterpret_cast<const f32x4_t*>(&s_sx[wave][c * S + o][g * 4]);
+            else v = sx[c];
+            // result j: token j and every group's own sum, or token j / S and group j % S
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+              const int k = ALL ? j : j * S + o, e = ALL ? o : 0;
+              acc[j] = fmaf(sc, fmaf(-z, v[k], d[c][e][k]), acc[j]);
+            }
           }
+        };
+        if constexpr (ALL && S == 4) {
+          // chunk by chunk: all sums of a tile do not fit the registers
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            __builtin_amdgcn_sched_barrier(0);
+            scales_of(c);
+            products(c);
+            add(c);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          load(i, ring[i]);
+          __builtin_amdgcn_sched_barrier(0);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) products(c);
+          __builtin_amdgcn_sched_barrier(0);
+          load(i, ring[i]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) add(c);
+        }
 #pragma unroll
         for (int j = 0; j < R; ++j) {
           float* to = &sums[i * R + j][wave][lane];
@@ -606,9 +660,10 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   }
 }
 
-template <int S, bool ACT, bool SB, bool VEC, bool Z, int BT>
+template <int S, bool ALL, bool ACT, bool SB, bool VEC, bool Z, int BT>
 static hipError_t launch_w4_few_t(const W4Args& a, hipStream_t stream) {
-  W4LaneArgs la = {a, 0, (a.T + 16 / S - 1) / (16 / S)};
+  constexpr int PER = ALL ? 16 : 16 / S;
+  W4LaneArgs la = {a, 0, (a.T + PER - 1) / PER};
   const int64_t cols = ACT ? a.N / 2 : a.N;
   constexpr int COLS = 16 * (ACT ? BT / 2 : BT);
   const int64_t blocks = (cols + COLS - 1) / COLS;
@@ -619,19 +674,35 @@ static hipError_t launch_w4_few_t(const W4Args& a, hipStream_t stream) {
   la.blocks = (int)w4_hold((blocks + room - 1) / room, COLS, a.K);
   la.a.col_groups = (int)((blocks + la.blocks - 1) / la.blocks);
   const int64_t groups = ((int64_t)la.a.col_groups + 7) / 8 * 8 * la.row_blocks;
-  hipLaunchKernelGGL((w4_few_kernel<S, ACT, SB, VEC, Z, BT>), dim3((unsigned)groups), dim3(waves * 64), 0, stream, la);
+  hipLaunchKernelGGL((w4_few_kernel<S, ALL, ACT, SB, VEC, Z, BT>), dim3((unsigned)groups), dim3(waves * 64), 0, stream, la);
   return hipGetLastError();
+}
+
+template <int S, bool ALL, bool SB, bool VEC, bool Z>
+static hipError_t launch_w4_few_rows(const W4Args& a, int act, hipStream_t stream) {
+  // four tiles a block where that still leaves a block per CU: one join for twice
+  // the codes (131,072 x 4,096, 5 rows, groups of 128: 55.7 us, 60.4 with two);
+  // else two, so that more CUs have one (4,096 x 4,096: 6.7, 10.1 with four)
+  const int64_t rows = ALL ? (a.T + 15) / 16 : (a.T + 16 / S - 1) / (16 / S), wide = a.N / 64 * rows;
+  if constexpr (!(ALL && S == 4))
+    if (wide >= 256)
+      return act ? launch_w4_few_t<S, ALL, true, SB, VEC, Z, 4>(a, stream) : launch_w4_few_t<S, ALL, false, SB, VEC, Z, 4>(a, stream);
+  return act ? launch_w4_few_t<S, ALL, true, SB, VEC, Z, 2>(a, stream) : launch_w4_few_t<S, ALL, false, SB, VEC, Z, 2>(a, stream);
 }
 
 template <int S, bool SB, bool VEC, bool Z>
 static hipError_t launch_w4_few_z(const W4Args& a, int act, hipStream_t stream) {
-  // four tiles a block where that still leaves a block per CU: one join for twice
-  // the codes (131,072 x 4,096, 5 rows, groups of 128: 55.7 us, 60.4 with two);
-  // else two, so that more CUs have one (4,096 x 4,096: 6.7, 10.1 with four)
-  const int64_t rows = (a.T + 16 / S - 1) / (16 / S), wide = a.N / 64 * rows;
-  if (wide >= 256)
-    return act ? launch_w4_few_t<S, true, SB, VEC, Z, 4>(a, stream) : launch_w4_few_t<S, false, SB, VEC, Z, 4>(a, stream);
-  return act ? launch_w4_few_t<S, true, SB, VEC, Z, 2>(a, stream) : launch_w4_few_t<S, false, SB, VEC, Z, 2>(a, stream);
+  if constexpr (S > 1) {
+    // ALL where it saves row blocks enough and its blocks leave no CU idle, or
+    // where it saves many (us with and without; groups of 32: 16,384 x 8,192, 8
+    // rows 31.7, 26.8, 16 rows 36, 44; 8,192 x 8,192, 9 rows 20, 25, 64 rows 58,
+    // 78; 4,096 x 4,096, 16 rows 10.7, 9.3, 32 rows 11.2, 13.3; groups of 64:
+    // 16,384 x 4,096, 9 rows 13.3, 15.1; 4,096 x 4,096, 16 rows 8.8, 6.6)
+    const int64_t few = (a.T + 16 / S - 1) / (16 / S), all = (a.T + 15) / 16;
+    if (few > S / 2 && (a.N / 32 * all >= 256 || few >= 8))
+      return launch_w4_few_rows<S, true, SB, VEC, Z>(a, act, stream);
+  }
+  return launch_w4_few_rows<S, false, SB, VEC, Z>(a, act, stream);
 }
 
 template <int S, bool SB, bool VEC>

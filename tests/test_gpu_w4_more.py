@@ -10,7 +10,7 @@ import torch
 
 import moe_grouped_gemm_route_amd as moe
 from tests.gpu_util import DEV
-from tests.test_gpu_w4 import BAD, dev, ids_of, problem, ref, run
+from tests.test_gpu_w4 import BAD, check as near, dev, ids_of, problem, ref, run
 
 pytestmark = pytest.mark.gpu
 
@@ -41,6 +41,46 @@ def test_every_number_of_rows(T, G):
     check(problem(2, 50, 640, G, rows=T, exact=True, scale=torch.bfloat16))
 
 
+# the same with 16 rows a block under narrow groups: many rows, or several with
+# many columns; k that ends inside a chunk, a group and a unit
+MANY = [(9, 8200, 96, 32), (13, 8193, 160, 32), (17, 16390, 320, 64), (29, 40, 8224, 32), (57, 70, 9280, 64),
+        (64, 33, 4640, 32), (31, 8207, 64, 64), (12, 16400, 192, 64), (48, 130, 512, 32), (61, 2100, 448, 64),
+        (33, 2, 32, 32), (80, 17, 64, 64)]
+
+
+@pytest.mark.parametrize("case", MANY)
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("scale", [torch.float32, torch.bfloat16])
+def test_many_rows_of_narrow_groups(case, zeros, scale):
+    T, N, K, G = case
+    check(problem(15, N, K, G, rows=T, zeros=zeros, exact=True, scale=scale))
+
+
+@pytest.mark.parametrize("case", [(31, 66, 576, 32), (60, 34, 1088, 64), (11, 8208, 128, 32)])
+@pytest.mark.parametrize("out", [moe.F32, moe.BF16])
+def test_activation_of_many_rows_of_narrow_groups(case, out):
+    T, N, K, G = case
+    p = problem(16, N, K, G, rows=T, scale=torch.bfloat16)
+    near(run(p, out_dtype=out, act=moe.ACT_SILU_MUL), ref(p, act=True), out)
+
+
+@pytest.mark.parametrize("G", [32, 64])
+def test_a_row_that_is_not_finite_stays_alone_among_many(G):
+    p = problem(17, 40, 704, G, rows=62, exact=True)
+    clean = run(p)
+    for value in (float("inf"), float("nan")):
+        for t in (0, 21, 61):
+            x = p["x"].clone()
+            x[t, 577] = value
+            y = run(dict(p, x=x))
+            keep = torch.arange(62, device=y.device) != t
+            assert torch.equal(y[keep], clean[keep]) and bool(y[t].isnan().all())
+    p["scales"][11] = float("nan")
+    y = run(p)
+    keep = torch.arange(40, device=y.device) != 11
+    assert torch.equal(y[:, keep], clean[:, keep]) and bool(y[:, 11].isnan().all())
+
+
 @pytest.mark.parametrize("case", [(2, 3, 4, 40, 4640, 32), (1, 7, 5, 600, 4352, 128), (3, 5, 3, 4500, 96, 32)])
 def test_long_pairs(case):
     T, k, E, N, K, G = case
@@ -55,7 +95,8 @@ def test_long_pairs(case):
 
 
 @pytest.mark.parametrize("scale", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("case", [(1, 64, 512, 32), (4, 64, 512, 32), (7, 48, 512, 64), (12, 40, 512, 128)])
+@pytest.mark.parametrize("case", [(1, 64, 512, 32), (4, 64, 512, 32), (7, 48, 512, 64), (12, 40, 512, 128),
+                                  (30, 40, 512, 32), (58, 40, 512, 64)])
 def test_scales_and_zero_points_that_start_anywhere(case, scale):
     T, N, K, G = case
     p = problem(5, N, K, G, rows=T, scale=scale, exact=True)
