@@ -146,8 +146,8 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 }
 
 // WI x WJ waves of SI x SJ 16 x 16 subtiles each, KG such groups of waves that
-// take every KG-th 64 r; two stages.  PARTS: A comes as that many bf16 matrices,
-// each multiplied with the same B.
+// take every KG-th 64 r; two stages in LDS, or three (TURNS).  PARTS: A comes as
+// that many bf16 matrices, each multiplied with the same B.
 //
 // The walk.  A stage's 2 SI PARTS operand groups (one A subtile, SJ matrix
 // instructions) run in order; operands are read from LDS two groups ahead.
@@ -171,9 +171,9 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 // stage on its way, 0.41 with two, 0.47 with four: one more half of the waves and
 // one more buffer are worth it, three more are not.
 //
-// What bounds it.  256 x 256 tiles: the matrix pipes, 1.34 PFLOP/s forward and
+// What bounds it.  256 x 256 tiles: the matrix pipes, 1.22 to 1.29 PFLOP/s forward and
 // 1.18 to 1.26 backward at 4,096 rows, where a library product reaches 1.22 to
-// 1.26; 53 % of the pipes' cycles at the clock that the chip holds.  Of 116 us of
+// 1.26; 60 % of the pipes' busy cycles at the clock that the chip holds.  Of 116 us of
 // such a product 88 are left without the loads, 91 without the LDS reads and 71
 // without the matrix instructions.  Smaller tiles: the loads from L2 (14 to 18 TB/s
 // over the chip with two stages on their way), since with fewer rows each weight
