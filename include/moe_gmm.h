@@ -603,7 +603,8 @@ int moe_gate_up(const uint16_t* x, const uint16_t* w13, int32_t M, int32_t N, in
  * to bf16 (half a step, as the result's own rounding); for an f32 result it is
  * kept as the sum of three bf16 values, 24 bits, at three times the products.
  * (A |d| past the largest bf16, 3.39e38, counts as infinite.)  Sums f32, in a
- * fixed order; no atomics.
+ * fixed order; no atomics.  Infinities and NaN in x, w13 and d reach the results
+ * that their products enter, as the formulas have them, and no others.
  *
  * dh             [M, N/2] f32 or bf16 (dh_dtype).
  * x, w13         as given to moe_gate_up; x may be NULL without dw13, w13 without

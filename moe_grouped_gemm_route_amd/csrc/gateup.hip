@@ -65,7 +65,7 @@ struct TileArgs {
   const uint16_t* b;       // likewise with J
   int64_t lda, ldb;
   int I, J, R;             // J: columns of out (with GATE: of h)
-  int64_t part_stride;     // PARTS matrices, this far apart, add up to A
+  int64_t part_stride;     // PARTS matrices, this far apart, add up to A (of f32 results)
   int splits, steps;       // shares of the sum over r, and stages of a share
   int tiles_i, tiles_j;
   void* out;               // [I, J]; with splits > 1 f32 [splits, I, J]
@@ -149,6 +149,16 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 // take every KG-th 64 r; two stages in LDS, or three (TURNS).  PARTS: A comes as
 // that many bf16 matrices, each multiplied with the same B.
 //
+// PARTS and infinities.  The second and third part of a value are zero or of the
+// other sign as often as not, so an infinite B makes the sum NaN (0 inf, inf - inf)
+// where A B is an infinity.  A tile of which a result is NaN is therefore walked a
+// second time, with the first part in place of all three, and the results that were
+// NaN are written again: each has a term that is not finite, so the first parts'
+// sum is the infinity or the NaN that the whole values' is.  Finite tiles pay for
+// the comparison and a barrier (us without and with: dx of 64 rows 21.8, 22.1; dw13
+// of 64 rows of 4,096 x 4,096 24.7, 25.1; dx and dw13 of 1,237 rows 89, 90; the two
+// walks as one loop 0.3 to 1 more on the small ones).
+//
 // The walk.  A stage's 2 SI PARTS operand groups (one A subtile, SJ matrix
 // instructions) run in order; operands are read from LDS two groups ahead.
 // The last quarter of the groups has all of its operands in registers, and the
@@ -192,7 +202,8 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
   constexpr int SLICE = A_BYTES + OpB::BYTES;
   constexpr int STAGE = KG * SLICE;
   constexpr int JOIN = (KG - 1) * BM * BN * 4;
-  constexpr int LDS = BUFS * STAGE > JOIN ? BUFS * STAGE : JOIN;
+  constexpr int FLAGS = PARTS > 1 && TURNS ? NW * 4 : 0;
+  constexpr int LDS = BUFS * STAGE + FLAGS > JOIN ? BUFS * STAGE + FLAGS : JOIN;
   static_assert(!GATE || !BROW, "w13's rows are columns of out");
   static_assert(!GATE || SJ == 4, "a wave holds a pair of gate and a pair of up subtiles");
   __shared__ __attribute__((aligned(1024))) uint8_t s_all[LDS];
@@ -245,7 +256,9 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
 
   // The next stage to load: this group's KG stages on from its last.
   const int stages = (p.R + GU_BK - 1) / GU_BK;
-  int at = (split * p.steps + turn) * KG + lg;
+  const int begin = (split * p.steps + turn) * KG + lg;
+  int at = begin;
+  int64_t part_stride = p.part_stride;
   const uint32_t l0 = lds_addr(s_all) + lg * SLICE;
   constexpr uint32_t OPEN = 0x7FFE0000u;   // lanes outside are marked: the range need not end anywhere
   auto load_a = [&](int buf) __attribute__((always_inline)) {
@@ -255,7 +268,7 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
     const uint32_t bytes = AROW ? (uint32_t)((min(left, GU_BK) * p.lda - i0) * 2) : OPEN;
 #pragma unroll
     for (int q = 0; q < PARTS; ++q) {
-      const uint16_t* base = p.a + q * p.part_stride + (AROW ? (int64_t)r0 * p.lda + i0 : (int64_t)i0 * p.lda + r0);
+      const uint16_t* base = p.a + q * part_stride + (AROW ? (int64_t)r0 * p.lda + i0 : (int64_t)i0 * p.lda + r0);
       const u32x4_t rs = only_if(live, make_rsrc(base, bytes));
 #pragma unroll
       for (int j = 0; j < OpA::LOADS; ++j) {
@@ -284,10 +297,6 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
     at += (TURNS ? 2 : 1) * KG;
   };
   f32x4_t acc[SI][SJ];
-#pragma unroll
-  for (int a = 0; a < SI; ++a)
-#pragma unroll
-    for (int s = 0; s < SJ; ++s) acc[a][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   constexpr int SP = SI * PARTS;
   constexpr int NQ = 2 * SP;                       // operand groups of a stage
@@ -373,46 +382,102 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
 #pragma unroll
     for (int q = 0; q < CA; ++q) fa[q] = na[q];
   };
-  if constexpr (TURNS) {
-    int st = 0, buf = 0;
-    auto one = [&](bool mine) __attribute__((always_inline)) {
-      const int after = buf == 2 ? 0 : buf + 1;
-      step(buf, after, mine);
-      buf = after;
-      return ++st < steps;
-    };
-    // Stage 1 is the other half's: the waves that have loaded stage 0 begin with a
-    // step without loads.  From there on a step with and one without follow one
-    // another for every wave.
-    bool more = true;
-    if (turn == 0) {
+  auto walk = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int a = 0; a < SI; ++a)
+#pragma unroll
+      for (int s = 0; s < SJ; ++s) acc[a][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if constexpr (TURNS) {
+      int st = 0, buf = 0;
+      auto one = [&](bool mine) __attribute__((always_inline)) {
+        const int after = buf == 2 ? 0 : buf + 1;
+        step(buf, after, mine);
+        buf = after;
+        return ++st < steps;
+      };
+      // Stage 1 is the other half's: the waves that have loaded stage 0 begin with a
+      // step without loads.  From there on a step with and one without follow one
+      // another for every wave.
+      bool more = true;
+      if (turn == 0) {
+        load_stage(0);
+        vm_wait();
+        lds_barrier();
+        load_stage(2);
+        first();
+        more = one(false);
+      } else {
+        load_stage(1);
+        lds_barrier();
+        first();
+      }
+#pragma unroll 1
+      while (more) {
+        more = one(true);
+        if (!more) break;
+        more = one(false);
+      }
+    } else {
       load_stage(0);
+      load_stage(1);
       vm_wait();
       lds_barrier();
-      load_stage(2);
       first();
-      more = one(false);
-    } else {
-      load_stage(1);
-      lds_barrier();
-      first();
-    }
 #pragma unroll 1
-    while (more) {
-      more = one(true);
-      if (!more) break;
-      more = one(false);
+      for (int st = 0; st < steps; ++st) step(st & 1, st & 1 ^ 1, true);
     }
-  } else {
-    load_stage(0);
-    load_stage(1);
-    vm_wait();
+    vm_wait();      // the loads past the last stage land before LDS is used again
+  };
+
+  const int c16 = lane & 15, g = lane >> 4;
+  if constexpr (PARTS > 1) {
+    static_assert(KG == 1 && !GATE && SI * SJ * 4 <= 64, "a bit per result of a lane");
+    uint64_t nan = 0;                      // the first walk's results that were
+    // A word of wave w's, where nothing is read or on its way once its own loads have
+    // landed: with two buffers in the last stage's, where its loads past the end went.
+    auto flag = [&](int w) __attribute__((always_inline)) {
+      return reinterpret_cast<uint32_t*>(s_all + (TURNS ? BUFS * STAGE + w * 4 : (steps - 1 & 1) * STAGE + w * OpA::LOADS * 1024));
+    };
+    walk();
+    const int64_t row0 = (int64_t)split * p.I + i0 + wi * SI * 16 + c16;
+    const int rows = p.I - i0 - wi * SI * 16 - c16, col0 = j0 + wj * SJ * 16 + g * 4;
+    float* const out = static_cast<float*>(p.out) + row0 * p.J + col0;
+#pragma unroll
+    for (int a = 0; a < SI; ++a) {
+      if (a * 16 >= rows) continue;
+#pragma unroll
+      for (int c = 0; c < SJ; ++c)
+        if (col0 + c * 16 < p.J) gu_store4(out, false, (int64_t)a * 16 * p.J + c * 16, acc[a][c]);
+    }
+    bool bad = false;
+#pragma unroll
+    for (int q = 0; q < SI * SJ * 2; ++q)
+      bad |= __builtin_isunordered(acc[q / SJ / 2][q / 2 % SJ][q % 2 * 2], acc[q / SJ / 2][q / 2 % SJ][q % 2 * 2 + 1]);
+    const uint64_t any = __ballot(bad);
+    if (lane == 0) *flag(wid) = any != 0;
     lds_barrier();
-    first();
-#pragma unroll 1
-    for (int st = 0; st < steps; ++st) step(st & 1, st & 1 ^ 1, true);
+    uint32_t all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) all |= *flag(w);
+    if (__builtin_expect(uniform(all) == 0, 1)) return;
+#pragma unroll
+    for (int q = 0; q < SI * SJ * 4; ++q) {
+      const float v = acc[q / SJ / 4][q / 4 % SJ][q % 4];
+      nan |= (uint64_t)(v != v) << q;
+    }
+    lds_barrier();
+    part_stride = 0;
+    at = begin;
+    walk();
+#pragma unroll
+    for (int q = 0; q < SI * SJ * 4; ++q) {
+      const int a = q / SJ / 4, c = q / 4 % SJ;
+      if (nan >> q & 1 && a * 16 < rows && col0 + c * 16 < p.J) out[(int64_t)a * 16 * p.J + c * 16 + q % 4] = acc[a][c][q % 4];
+    }
+    return;
+  } else {
+    walk();
   }
-  vm_wait();      // the loads past the last stage land before LDS is used again
 
   if constexpr (KG > 1) {
     lds_barrier();
@@ -430,7 +495,6 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
       for (int q = 0; q < SI * SJ; ++q) acc[q / SJ][q % SJ] += sum[k * GROUP + q * 64];
   }
 
-  const int c16 = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int a = 0; a < SI; ++a) {
     const int row = i0 + wi * SI * 16 + a * 16 + c16;
