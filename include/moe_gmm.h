@@ -564,8 +564,9 @@ int moe_gmm_dgrad(const void* packed, int fmt, int32_t E, int32_t N, int32_t K, 
  * (groups of 32 or 64 and few rows: per 4 or 8), a routed one once per pair.
  * Limits: N <= 2^30, K <= 2^23, K % group == 0, N even with the activation,
  * E*N*K/2 < 2^40, T <= 2^24, 1 <= k <= 64, T*k <= 2^24; codes and x 16-byte
- * aligned, scales and y to their type; rows of y (dense: rows / 4, 8 or 16,
- * rounded up) * (N/16 + 8) <= 8,388,607, with N/2 for N with the activation.
+ * aligned, scales, topk_ids, topk_weights and y to their type; rows of y (dense:
+ * rows / 4, 8 or 16, rounded up) * (N/16 + 8) <= 8,388,607, with N/2 for N with the
+ * activation.
  */
 int moe_w4_gemv(const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros, int32_t group,
                 int32_t E, int32_t N, int32_t K, const uint16_t* x, int32_t x_rows, int32_t T,

@@ -378,6 +378,8 @@ int moe_w4_gemv(const uint8_t* codes, const void* scales, int scale_dtype, const
   if (!aligned16(codes) || !aligned16(x) || ((uintptr_t)scales & (scale_dtype == MOE_BF16 ? 1 : 3)))
     return MOE_ERR_SHAPE;
   if (((uintptr_t)y & (y_dtype == MOE_BF16 ? 1 : 3))) return MOE_ERR_SHAPE;
+  // scalar loads, which leave out the low bits of an address
+  if (((uintptr_t)topk_ids & 3) || ((uintptr_t)topk_weights & 3)) return MOE_ERR_SHAPE;
   // workgroups of up to 512 work-items
   if (moe::w4_workgroups(N, group, T, k, topk_ids != nullptr, topk_weights != nullptr, act) > kMaxWorkgroups / 2)
     return MOE_ERR_SHAPE;

@@ -1,0 +1,23 @@
+"""Argument checks of the dense operators beside tests/test_dense_abi_cpu.py (no
+GPU needed: every call here is rejected before any HIP call)."""
+
+import ctypes
+
+import pytest
+
+import moe_grouped_gemm_route_amd as moe
+from tests.test_grads_abi_cpu import A, ERR_SHAPE, _call
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_w4_ids_and_weights_lie_at_whole_words(off):
+    """They are read by scalar loads, which leave out the low two bits of an
+    address: a call with others would take the entries before."""
+    order = "codes scales sdt zeros group E N K x rows T ids w k y odt act".split()
+    base = dict(codes=A, scales=A, sdt=0, zeros=None, group=32, E=8, N=64, K=256, x=A, rows=4, T=4, ids=A, w=A, k=2,
+                y=A, odt=0, act=0)
+    odd = ctypes.c_void_p((1 << 30) + off)
+    f = moe.library().moe_w4_gemv
+    assert _call(f, order, base, ids=odd) == ERR_SHAPE
+    assert _call(f, order, base, w=odd) == ERR_SHAPE
+    assert _call(f, order, base, ids=odd, w=None) == ERR_SHAPE
