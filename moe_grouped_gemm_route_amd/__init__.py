@@ -519,6 +519,7 @@ def moe_gmm_dgrad(packed, fmt, E, N, K, dy, group_offsets, M, out_dtype=F32, act
 # What a small call costs is its checks: these read each property once.
 _U8, _I32, _F32T, _BF16T, _I16, _U16 = (torch.uint8, torch.int32, torch.float32, torch.bfloat16, torch.int16,
                                         torch.uint16)
+_WANTED = {None, F32, BF16}
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -636,7 +637,8 @@ def gate_up(x, w13, out_dtype=F32, preact_dtype=None, out=None, preact=None):
 def gate_up_bwd_workspace_bytes(M, N, K, dx_dtype=F32, dw_dtype=F32):
     """moe_gate_up_bwd_workspace_bytes; a dtype of None: that gradient is not
     wanted."""
-    if (M | N | K) >> 31:   # (ctypes passes the low 32 bits)
+    dx_dtype, dw_dtype = _FLOATS.get(dx_dtype, dx_dtype), _FLOATS.get(dw_dtype, dw_dtype)
+    if (M | N | K) >> 31 or not {dx_dtype, dw_dtype} <= _WANTED:   # (ctypes passes the low 32 bits)
         return 0
     return library().moe_gate_up_bwd_workspace_bytes(M, N, K, dx_dtype is not None, dx_dtype or 0,
                                                      dw_dtype is not None, dw_dtype or 0)

@@ -4,6 +4,7 @@ GPU needed: every call here is rejected before any HIP call)."""
 import ctypes
 
 import pytest
+import torch
 
 import moe_grouped_gemm_route_amd as moe
 from tests.test_grads_abi_cpu import A, ERR_SHAPE, _call
@@ -21,3 +22,16 @@ def test_w4_ids_and_weights_lie_at_whole_words(off):
     assert _call(f, order, base, ids=odd) == ERR_SHAPE
     assert _call(f, order, base, w=odd) == ERR_SHAPE
     assert _call(f, order, base, ids=odd, w=None) == ERR_SHAPE
+
+
+def test_workspace_bytes_take_the_types_that_the_gradients_take():
+    """F32 and BF16 or their torch types, as gate_up_bwd's dx_dtype and dw_dtype."""
+    f = moe.gate_up_bwd_workspace_bytes
+    both = {moe.F32: torch.float32, moe.BF16: torch.bfloat16, None: None}
+    for x in both:
+        for w in both:
+            assert f(100, 512, 256, both[x], both[w]) == f(100, 512, 256, x, w)
+            assert f(100, 512, 256, both[x], w) == f(100, 512, 256, x, w)
+    assert f(100, 512, 256, torch.bfloat16, None) > 0
+    assert f(100, 512, 256, torch.float16, None) == 0 and f(100, 512, 256, None, torch.int32) == 0
+    assert f(100, 512, 256, torch.float16, moe.F32) == 0
