@@ -364,7 +364,8 @@ int moe_w4_gemv(const uint8_t* codes, const void* scales, int scale_dtype, const
   // a sum of activations is not the activation of a sum
   if (topk_weights && act != MOE_ACT_NONE) return MOE_ERR_UNSUPPORTED;
   if (group != 32 && group != 64 && group != 128 && group != 256) return MOE_ERR_SHAPE;
-  // 64 rows of x and 16 columns of codes are addressed with 32-bit byte offsets
+  // 16 rows of x, and up to 2^30 bytes of a workgroup's codes (a block of 64 columns
+  // at least), are addressed with 32-bit byte offsets
   if (E < 1 || N < 1 || N > kMaxCols || K < 1 || K > (1 << 23) || K % group != 0) return MOE_ERR_SHAPE;
   if ((int64_t)N * (K / 2) >= kMaxCodeBytes / E) return MOE_ERR_SHAPE;
   if (act == MOE_ACT_SILU_MUL && N % 2 != 0) return MOE_ERR_SHAPE;

@@ -424,7 +424,7 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
       lds_barrier();
       first();
 #pragma unroll 1
-      for (int st = 0; st < steps; ++st) step(st & 1, st & 1 ^ 1, true);
+      for (int st = 0; st < steps; ++st) step(st & 1, (st & 1) ^ 1, true);
     }
     vm_wait();      // the loads past the last stage land before LDS is used again
   };
@@ -436,7 +436,7 @@ __global__ __launch_bounds__(WI * WJ * KG * 64, OCC) void gu_tile_kernel(TileArg
     // A word of wave w's, where nothing is read or on its way once its own loads have
     // landed: with two buffers in the last stage's, where its loads past the end went.
     auto flag = [&](int w) __attribute__((always_inline)) {
-      return reinterpret_cast<uint32_t*>(s_all + (TURNS ? BUFS * STAGE + w * 4 : (steps - 1 & 1) * STAGE + w * OpA::LOADS * 1024));
+      return reinterpret_cast<uint32_t*>(s_all + (TURNS ? BUFS * STAGE + w * 4 : ((steps - 1) & 1) * STAGE + w * OpA::LOADS * 1024));
     };
     walk();
     const int64_t row0 = (int64_t)split * p.I + i0 + wi * SI * 16 + c16;
@@ -537,12 +537,6 @@ static hipError_t launch_tiles(TileArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// v of the lane that a DPP control names, every lane having one.
-template <int CTRL>
-__device__ __forceinline__ float dpp_add(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
-}
-
 constexpr int GS_NT = 2;       // non-temporal: weights are read once
 
 // ---------------------------------------------------------------------------
@@ -581,7 +575,7 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
   __shared__ float s_part[2][GS_WAVES][4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
+  const int waves = blockDim.x >> 6;                        // a unit of every block each at least
   const int n16 = lane & 15, g = lane >> 4;
   const int K = (int)p.K;
   const int total = (K + 255) >> 8;
@@ -636,14 +630,14 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
     for (int o = threadIdx.x >> 3; o < p.M * 8; o += blockDim.x >> 3) {
       const int w = threadIdx.x & 7, c = o & 7, row = o >> 3;
       float gt = 0.f, ut = 0.f;
-      if (w < min(waves, total)) {
+      if (w < waves) {
         const float* from = &part[w][row & 3][(row >> 2) * 16 + c];
         gt = from[0];
         ut = from[8];
       }
-      gt += dpp_add<0xB1>(gt), ut += dpp_add<0xB1>(ut);
-      gt += dpp_add<0x4E>(gt), ut += dpp_add<0x4E>(ut);
-      gt += dpp_add<0x141>(gt), ut += dpp_add<0x141>(ut);
+      gt += dpp_from<0xB1>(gt), ut += dpp_from<0xB1>(ut);
+      gt += dpp_from<0x4E>(gt), ut += dpp_from<0x4E>(ut);
+      gt += dpp_from<0x141>(gt), ut += dpp_from<0x141>(ut);
       if (w != 0 || c >= live) continue;
       const float h = gu_silu(gt) * ut;
       const int col = j0 + blk * 8 + c;
@@ -663,13 +657,8 @@ __global__ __launch_bounds__(GS_WAVES * 64) void gu_stream_kernel(StreamArgs p) 
     }
   };
 
-  // the tiles of this wave: `per` units of each block.  Every wave takes part in
-  // every join, also where a block's units do not reach it.
-  const int per = wave < total ? (total - wave + waves - 1) / waves : 0;
-  if (per == 0) {
-    for (int b = 0; b < blocks; ++b) join(b);
-    return;
-  }
+  // the tiles of this wave: `per` units of each block
+  const int per = (total - wave + waves - 1) / waves;
   int u = 0, blk = 0;
   while (blk < blocks) {
 #pragma unroll

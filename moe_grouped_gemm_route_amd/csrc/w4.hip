@@ -130,12 +130,6 @@ __device__ __forceinline__ V scalar_load(const V* p) {
   return *(const __attribute__((address_space(4))) V*)(uintptr_t)p;
 }
 
-// v of the lane that a quad permutation names.
-template <int CTRL>
-__device__ __forceinline__ float quad_xor(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
-}
-
 // A wave multiplies 4 rows x 512 k of codes at a time, 1 KiB in one load of whole
 // 256-byte runs (loads in the matrix unit's order would be 64 cache accesses a
 // KiB instead of 16, and the L1 takes one a cycle).  Lane l holds 32 codes of one
@@ -178,7 +172,7 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
   __shared__ __attribute__((aligned(16))) float s_sum[2][W4_RING][W4_WAVES][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
+  const int waves = blockDim.x >> 6;                // a unit each at least
   const int g = lane >> 4, q4 = lane & 3, r = (lane & 15) >> 2;
   const int block = g * 4 + q4;
   const int K = (int)p.K, groups = (int)p.groups;
@@ -325,8 +319,8 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
         for (int s = 0; s < 4; ++s) d = w4_mfma(x[s], w[s], d);
         // over the four lanes of the row's 64 bytes
         float f = sc * fmaf(-z, sx, own(d));
-        f += quad_xor<0xB1>(f);
-        f += quad_xor<0x4E>(f);
+        f += dpp_from<0xB1>(f);
+        f += dpp_from<0x4E>(f);
         if (q4 == 0) {
           float* to = &sums[i][wave][r * 4 + g];
           *to = u == wave ? f : *to + f;
@@ -347,13 +341,13 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_lane_kernel(W4LaneArgs la) {
     const int live = min(rows - b * HALF * 4, HALF * 4);    // rows of y of the block
     auto total_of = [&](int quad, int row) __attribute__((always_inline)) {
       float f = 0.f;
-      if (w < min(waves, total)) {
+      if (w < waves) {
         const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&sums[quad][w][row * 4]);
         f = (v[0] + v[1]) + (v[2] + v[3]);
       }
-      f += quad_xor<0xB1>(f);
-      f += quad_xor<0x4E>(f);
-      return f + quad_xor<0x141>(f);                        // the other quad of eight lanes
+      f += dpp_from<0xB1>(f);
+      f += dpp_from<0x4E>(f);
+      return f + dpp_from<0x141>(f);                        // the other quad of eight lanes
     };
     for (int row = threadIdx.x >> 3; row < HALF * 4; row += blockDim.x >> 3) {
       float f = total_of(row >> 2, row & 3);
@@ -445,7 +439,7 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
   __shared__ __attribute__((aligned(16))) float s_sx[ALL ? W4_WAVES : 1][ALL ? 4 * S : 1][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
+  const int waves = blockDim.x >> 6;                  // a unit each at least
   const int n16 = lane & 15, g = lane >> 4;
   const int K = (int)p.K, groups = (int)p.groups;
   const int64_t N = p.N;
@@ -641,14 +635,13 @@ __global__ __launch_bounds__(W4_WAVES * 64) void w4_few_kernel(W4LaneArgs la) {
     }
     lds_barrier();
 
-    const int live_waves = min(waves, total);
     const int live = min(rows - b * HALF * 16, HALF * 16);
     for (int o = threadIdx.x; o < HALF * R * 64; o += blockDim.x) {
       const int l = o & 63, j = (o >> 6) % R, c = (o >> 6) / R;
       const int t = t0 + (l >> 4) * R + j, col = c * 16 + (l & 15);
       if (t >= p.T || col >= live) continue;
       float f = 0.f, h = 0.f;
-      for (int w = 0; w < live_waves; ++w) {
+      for (int w = 0; w < waves; ++w) {
         f += sums[c * R + j][w][l];
         if (ACT) h += sums[(c + HALF) * R + j][w][l];
       }

@@ -28,6 +28,12 @@ __device__ __forceinline__ uint32_t dpp_or(uint32_t other, uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)other, (int)v, CTRL, ROWS, 0xF, false);
 }
 
+// v of the lane that the DPP control CTRL names, where every lane has one.
+template <int CTRL>
+__device__ __forceinline__ float dpp_from(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_or(float other, float v) {
   return __uint_as_float(dpp_or<CTRL, ROWS>(__float_as_uint(other), __float_as_uint(v)));
