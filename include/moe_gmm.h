@@ -603,6 +603,8 @@ int moe_gate_up(const uint16_t* x, const uint16_t* w13, int32_t M, int32_t N, in
  * d is computed in f32.  For a bf16 result it is the product's operand rounded
  * to bf16 (half a step, as the result's own rounding); for an f32 result it is
  * kept as the sum of three bf16 values, 24 bits, at three times the products.
+ * (A bf16 gradient of the unrounded d is the f32 one, rounded: 1.66e-3 of error for
+ * 2.35e-3 in the 2-norm.)
  * (A |d| past the largest bf16, 3.39e38, counts as infinite.)  Sums f32, in a
  * fixed order; no atomics.  Infinities and NaN in x, w13 and d reach the results
  * that their products enter, as the formulas have them, and no others.

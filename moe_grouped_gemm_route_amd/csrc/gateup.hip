@@ -901,6 +901,13 @@ hipError_t launch_gate_up(const uint16_t* x, const uint16_t* w, int32_t M, int32
 
 // The plan of the gradients: bf16 parts of d, and each product's instance and
 // shares, whose f32 sums lie behind d (dx's are added up before dw13's begin).
+//
+// Parts.  A bf16 result takes the first part alone, d rounded to bf16: the matrix
+// unit has no operand between bf16's 8 bits and a second product, and dh, the kept
+// sums and the result are mostly bf16 themselves.  Both sides, 4,096 rows of 4,096 x
+// 4,096, both gradients: one part 240 us, 2-norm of the error 2.35e-3 of the
+// result's; three parts 630 us, 7e-7, and 1.66e-3 once rounded to bf16.  A mixed call
+// does the same, so that a gradient's bits do not depend on the other's type.
 struct BwdPlan {
   int parts;
   TilePlan dx, dw;
