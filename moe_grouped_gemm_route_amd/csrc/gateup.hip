@@ -181,9 +181,10 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int ti, int tj, int& 
 // stage on its way, 0.41 with two, 0.47 with four: one more half of the waves and
 // one more buffer are worth it, three more are not.
 //
-// What bounds it.  256 x 256 tiles: the matrix pipes, 1.22 to 1.29 PFLOP/s forward and
-// 1.18 to 1.26 backward at 4,096 rows, where a library product reaches 1.22 to
-// 1.26; 60 % of the pipes' busy cycles at the clock that the chip holds.  Of 116 us of
+// What bounds it.  256 x 256 tiles: the matrix pipes, 1.16 to 1.21 PFLOP/s forward at
+// 4,096 rows with the sums kept, 1.22 to 1.29 at 16,384, and 1.18 to 1.26 backward at
+// 4,096, where a library product reaches 1.22 to 1.26; 60 % of the pipes' busy cycles
+// at the clock that the chip holds.  Of 116 us of
 // such a product 88 are left without the loads, 91 without the LDS reads and 71
 // without the matrix instructions.  Smaller tiles: the loads from L2 (14 to 18 TB/s
 // over the chip with two stages on their way), since with fewer rows each weight
@@ -902,9 +903,9 @@ hipError_t launch_gate_up(const uint16_t* x, const uint16_t* w, int32_t M, int32
 // The plan of the gradients: bf16 parts of d, and each product's instance and
 // shares, whose f32 sums lie behind d (dx's are added up before dw13's begin).
 //
-// Parts.  A bf16 result takes the first part alone, d rounded to bf16: the matrix
-// unit has no operand between bf16's 8 bits and a second product, and dh, the kept
-// sums and the result are mostly bf16 themselves.  Both sides, 4,096 rows of 4,096 x
+// Parts.  A bf16 result takes the first part alone, d rounded to bf16: a bf16 factor
+// is multiplied by bf16 only, so that more bits of d are further products, and dh,
+// the kept sums and the result are mostly bf16 themselves.  Both sides, 4,096 rows of 4,096 x
 // 4,096, both gradients: one part 240 us, 2-norm of the error 2.35e-3 of the
 // result's; three parts 630 us, 7e-7, and 1.66e-3 once rounded to bf16.  A mixed call
 // does the same, so that a gradient's bits do not depend on the other's type.
