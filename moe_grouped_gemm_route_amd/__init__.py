@@ -560,7 +560,8 @@ def w4_gemv(codes, scales, x, zeros=None, topk_ids=None, topk_weights=None, out_
     With topk_ids [T, k] int32: codes [E, N, K/2], scales and zeros [E, N, K/G],
     x [T, K] or [T*k, K] -> y [T*k, N], a row per pair (zeros for an id outside
     [0, E)); with topk_weights [T, k] float32 -> y [T, N], a token's rows summed.
-    act=ACT_SILU_MUL: N/2 columns (not with topk_weights)."""
+    act=ACT_SILU_MUL: N/2 columns (not with topk_weights).  out: a tensor of
+    out_dtype to write."""
     nd = 2 if topk_ids is None else 3
     _is(codes, _U8, nd, "codes")
     sdt = _float(scales, "scales", nd)
@@ -620,7 +621,8 @@ def _gate_up_shape(x, w13):
 def gate_up(x, w13, out_dtype=F32, preact_dtype=None, out=None, preact=None):
     """moe_gate_up.  x bf16 [M, K], w13 bf16 [N, K] (gate rows, then up rows) ->
     h [M, N/2]; with preact_dtype (F32 or BF16), or a preact tensor [M, N] to
-    write, (h, preact): the sums that gate_up_bwd takes."""
+    write, (h, preact): the sums that gate_up_bwd takes.  out: a tensor of
+    out_dtype to write."""
     M, N, K = _gate_up_shape(x, w13)
     index = x.get_device()
     _one_device(index, w13, out, preact)
@@ -647,7 +649,8 @@ def gate_up_bwd_workspace_bytes(M, N, K, dx_dtype=F32, dw_dtype=F32):
 def gate_up_bwd(dh, x, w13, preact, dx_dtype=F32, dw_dtype=F32, dx=None, dw13=None, ws=None):
     """moe_gate_up_bwd.  dh [M, N/2] float32 or bfloat16, x and w13 as given to
     gate_up, the preact it kept -> (dx [M, K], dw13 [N, K]); a dtype of None
-    leaves that gradient out (None in its place).  dx, dw13: tensors to write.
+    leaves that gradient out (None in its place).  dx, dw13: tensors to write, whose
+    types stand for dx_dtype and dw_dtype.
     ws: a device tensor of at least gate_up_bwd_workspace_bytes, 256-byte
     aligned, or None to allocate one."""
     hdt = _float(dh, "dh", 2)
